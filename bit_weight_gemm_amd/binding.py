@@ -38,7 +38,8 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
             "biloco_gemm_check", "biloco_default_schedule", "biloco_schedules_for",
             "biloco_quant_weight_nvfp4", "biloco_quant_weight_workspace_bytes",
             "biloco_peel_decompose", "biloco_peel_workspace_bytes", "biloco_gemm_lowrank_quant",
-            "biloco_gemm_lowrank_quant_noalloc"]
+            "biloco_gemm_lowrank_quant_noalloc", "biloco_kv_append", "biloco_attn_paged",
+            "biloco_attn_workspace_bytes", "biloco_norm_gate_residual"]
 
 # size of the device array biloco_gemm_lowrank_quant_noalloc works in
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -95,6 +96,20 @@ def lib() -> ctypes.CDLL:
         L.biloco_default_schedule.argtypes = [i32, i32, i32, i32]
         L.biloco_schedules_for.restype = i32
         L.biloco_schedules_for.argtypes = [i32, i32, i32, i32, ctypes.POINTER(i32), i32]
+        f32 = ctypes.c_float
+        cache = [p, p, p, p, i32, i32, i32, i32]
+        ragged = [p, p, p, i32, i32, i32, i32]
+        L.biloco_kv_append.restype = st
+        L.biloco_kv_append.argtypes = cache + [p, i64, p, i64, p, i64, i32, p, i32, ctypes.c_char_p, p, i32,
+                                               i32, i32] + ragged + [p, i64, p]
+        L.biloco_attn_paged.restype = st
+        L.biloco_attn_paged.argtypes = cache + [p, i64, i32] + ragged + [i32, f32, i32, i32, p, i64, p, p,
+                                                                         sz, p]
+        L.biloco_attn_workspace_bytes.restype = st
+        L.biloco_attn_workspace_bytes.argtypes = [i32] * 7 + [ctypes.POINTER(sz)]
+        L.biloco_norm_gate_residual.restype = st
+        L.biloco_norm_gate_residual.argtypes = [p, i64, p, p, i64, f32, p, i64, i32, p, f32, f32, i32, i32, p,
+                                                i64, p, i64, p, p, p]
         _lib = L
     return _lib
 
@@ -280,3 +295,160 @@ def biloco_schedules_for(M: int, N: int, K: int, r: int) -> list:
     buf = (ctypes.c_int32 * 8)()
     n = lib().biloco_schedules_for(M, N, K, r, buf, 8)
     return [int(buf[i]) for i in range(min(n, 8))]
+
+
+# ---------------------------------------------------------------- decoder-layer operators
+# `cache` is the tuple (k_codes [pages][kv_heads][page][dim], v_codes
+# [pages][kv_heads][page/8][dim][8], k_scales [pages][kv_heads], v_scales
+# likewise), uint8, contiguous.  q, k, v and o are bf16 [tokens][heads][dim] whose
+# heads and channels are contiguous; their token strides are free.
+
+def biloco_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> tuple:
+    """Uninitialised cache arrays in the layouts above (plain allocation)."""
+    def new(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+    return (new(num_pages, kv_heads, page_size, head_dim),
+            new(num_pages, kv_heads, page_size // 8, head_dim, 8),
+            new(num_pages, kv_heads), new(num_pages, kv_heads))
+
+
+def _cache_args(cache):
+    k, v, ks, vs = cache
+    pages, kv_heads, page, dim = k.shape
+    if tuple(v.shape) != (pages, kv_heads, page // 8, dim, 8) or tuple(ks.shape) != (pages, kv_heads) or \
+            tuple(vs.shape) != (pages, kv_heads):
+        raise ValueError("cache arrays of different shapes")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("cache arrays must be contiguous")
+    return (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, kv_heads, page, dim)
+
+
+def _rows(t, heads, dim, what):
+    """Token stride of a [tokens][heads][dim] bf16 tensor."""
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape[1] != heads or t.shape[2] != dim or s[2] != 1 or \
+            (s[1] != dim and heads > 1):
+        raise ValueError(f"{what}: bf16 [tokens][{heads}][{dim}] with contiguous heads expected")
+    return s[0] if t.shape[0] > 1 else heads * dim
+
+
+def _ints(t, shape, what):
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {shape} expected")
+    return t.data_ptr()
+
+
+def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_table, max_q_len: int,
+                     q_out=None, pair_axis: bytes | None = None, interleaved: bool = False, stream=None):
+    """Rotate q and k, quantise and append k and v; returns q_out (None without q).
+    positions int32 [axes][T]; cos_sin fp32 [n_pos][rot_dim] (None: no rotation);
+    pair_axis: one byte per pair, the axis it turns by."""
+    cargs = _cache_args(cache)
+    kv_heads, dim = cargs[5], cargs[7]
+    T, B = k.shape[0], kv_len.shape[0]
+    n_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
+    axes = positions.shape[0] if rot else 0
+    heads = q.shape[1] if q is not None else 0
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k and v have different numbers of tokens")
+    if pair_axis is not None and len(pair_axis) != rot // 2:
+        raise ValueError("pair_axis has one byte per pair")
+    if rot and (cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous()):
+        raise ValueError("cos_sin: contiguous fp32 expected")
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=q.device)
+    if T == 0 or B == 0:      # empty tensors have no addresses
+        return q_out
+    _ok(lib().biloco_kv_append(
+        *cargs, _p(q), _rows(q, heads, dim, "q") if heads else 0, k.data_ptr(), _rows(k, kv_heads, dim, "k"),
+        v.data_ptr(), _rows(v, kv_heads, dim, "v"), heads, _ints(positions, (axes, T), "positions") if rot else None,
+        axes, pair_axis, _p(cos_sin), n_pos, rot, int(interleaved), _ints(q_start, (B + 1,), "q_start"),
+        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, block_table.shape[1]), "block_table"),
+        block_table.shape[1], B, T, max_q_len, _p(q_out),
+        _rows(q_out, heads, dim, "q_out") if heads else 0, _stream(stream)), "biloco_kv_append")
+    return q_out
+
+
+def biloco_attn_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int,
+                                max_kv_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().biloco_attn_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len,
+                                          ctypes.byref(out)), "biloco_attn_workspace_bytes")
+    return int(out.value)
+
+
+def biloco_attn_paged(cache, q, q_start, kv_len, block_table, max_q_len: int, max_kv_len: int, scale: float,
+                      window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Causal attention of the new tokens q over the cache; returns out."""
+    cargs = _cache_args(cache)
+    kv_heads, dim = cargs[5], cargs[7]
+    T, heads, _ = q.shape
+    B = kv_len.shape[0]
+    if out is None:
+        out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=q.device)
+    if out.shape[0] != T:
+        raise ValueError("out has another number of tokens than q")
+    if T == 0 or B == 0:
+        return out
+    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, heads)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse: contiguous fp32 [tokens][heads] expected")
+    if workspace is None:
+        n = biloco_attn_workspace_bytes(B, T, heads, kv_heads, dim, max_q_len, max_kv_len)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+    _ok(lib().biloco_attn_paged(
+        *cargs, q.data_ptr(), _rows(q, heads, dim, "q"), heads, _ints(q_start, (B + 1,), "q_start"),
+        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, block_table.shape[1]), "block_table"),
+        block_table.shape[1], B, T, max_q_len, max_kv_len, scale, window, sinks, out.data_ptr(),
+        _rows(out, heads, dim, "out"), _p(lse), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _stream(stream)), "biloco_attn_paged")
+    return out
+
+
+def _row_stride(t, T, C, dtypes, what):
+    if t.dtype not in dtypes or tuple(t.shape) != (T, C) or (t.stride(1) != 1 and C > 1):
+        raise ValueError(f"{what}: [{T}][{C}] of {dtypes} with contiguous rows expected")
+    return t.stride(0) if T > 1 else max(t.stride(0), C)
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def _weight(w, C, what):
+    if w is None:
+        return None
+    if w.dtype is not torch.bfloat16 or tuple(w.shape) != (C,) or not w.is_contiguous():
+        raise ValueError(f"{what}: contiguous bf16 [{C}] expected")
+    return w.data_ptr()
+
+
+def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+                              w_offset: float = 0.0, res_out=None, h=None, a_codes=None, a_scales=None,
+                              stream=None):
+    """r' = res + res_scale * gate * norm(x), h = norm(r'); returns (r', h).
+    gate [1][C] (every token) or [T][C].  a_codes and a_scales: h's FP4
+    quantisation (outputs)."""
+    T, C = x.shape
+    fp32 = res.dtype is torch.float32
+    kinds = (torch.float32,) if fp32 else _BF16
+    if res_out is None:
+        res_out = torch.empty((T, C), dtype=res.dtype, device=x.device)
+    if h is None:
+        h = torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
+    if T == 0:
+        return res_out, h
+    gate_stride = 0
+    if gate is not None:
+        one = gate.shape[0] == 1
+        gate_stride = _row_stride(gate, 1 if one else T, C, _BF16, "gate")
+        gate_stride = 0 if one else gate_stride
+    for t, shape, what in ((a_codes, (T, C // 2), "a_codes"), (a_scales, (T, C // 16), "a_scales")):
+        if t is not None and (t.dtype is not torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{what}: contiguous uint8 {shape} expected")
+    _ok(lib().biloco_norm_gate_residual(
+        x.data_ptr(), _row_stride(x, T, C, _BF16, "x"), _weight(post_w, C, "post_w"), _p(gate), gate_stride,
+        res_scale, res.data_ptr(), _row_stride(res, T, C, kinds, "res"), int(fp32), _weight(pre_w, C, "pre_w"),
+        eps, w_offset, T, C, res_out.data_ptr(), _row_stride(res_out, T, C, kinds, "res_out"), h.data_ptr(),
+        _row_stride(h, T, C, _BF16, "h"), _p(a_codes), _p(a_scales), _stream(stream)),
+        "biloco_norm_gate_residual")
+    return res_out, h

@@ -134,4 +134,61 @@ constexpr int kComposedMaxRank = 1024;   // the correction's lookup tables fit 3
 bool composed_supported(int M, int N, int K, int r);
 hipError_t launch_gemm_composed(const GemmArgs &a, bool mfma_correction, hipStream_t stream);
 
+// ---------------------------------------------------------------- decoder-layer operators
+struct KvAppendArgs {
+    uint8_t *kc, *vc, *ks, *vs;
+    int num_pages, kv_heads, page, dim;
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    int q_heads;
+    const int *positions;
+    int axes;
+    uint64_t axis_bits[2];      // two bits per pair
+    const float *cos_sin;
+    int n_pos, rot, interleaved;
+    const int *q_start, *kv_len, *table;
+    int max_pages, B, T, max_q;
+    uint16_t *q_out;
+    int64_t q_out_stride;
+};
+hipError_t launch_kv_append(const KvAppendArgs &a, hipStream_t stream);
+
+struct AttnArgs {
+    const uint8_t *kc, *vc, *ks, *vs;
+    int num_pages, kv_heads, page, dim;
+    const uint16_t *q;
+    int64_t q_stride;
+    int q_heads;
+    const int *q_start, *kv_len, *table;
+    int max_pages, B, T, max_q, max_kv;
+    float scale;
+    int window, sinks;
+    uint16_t *o;
+    int64_t o_stride;
+    float *lse;
+    void *ws;
+};
+size_t attn_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv);
+hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
+
+struct NormArgs {
+    const uint16_t *x;
+    int64_t x_stride;
+    const uint16_t *post_w, *gate;
+    int64_t gate_stride;
+    float res_scale;
+    const void *res;
+    int64_t res_stride;
+    int res_fp32;
+    const uint16_t *pre_w;
+    float eps, w_offset;
+    int T, C;
+    void *res_out;
+    int64_t res_out_stride;
+    uint16_t *h;
+    int64_t h_stride;
+    uint8_t *a_codes, *a_scales;
+};
+hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
+
 }  // namespace biloco

@@ -329,6 +329,135 @@ int32_t biloco_default_schedule(int32_t M, int32_t N, int32_t K, int32_t r);
 int32_t biloco_schedules_for(int32_t M, int32_t N, int32_t K, int32_t r,
                              int32_t *out, int32_t cap);
 
+/* ------------------------------------------------------------------------
+ * The operators of a decoder layer between two products: the QKV product's
+ * rows into a paged 8-bit key/value cache, attention over that cache, and
+ * the norms around a block.  Serving only (no gradients).
+ *
+ * The paged cache.  page_size tokens (16, 32, 64 or 128) of one key/value
+ * head form a block with one scale:
+ *   k_codes   uint8 [num_pages][kv_heads][page_size][head_dim]      E4M3
+ *   v_codes   uint8 [num_pages][kv_heads][page_size/8][head_dim][8] E4M3: the
+ *             eight values of one channel over eight successive tokens are
+ *             neighbours (the order in which P V takes them)
+ *   k_scales, v_scales  uint8 [num_pages][kv_heads]: byte b is the scale
+ *             2^(b - 127), 1 <= b <= 246 (every code times it is finite)
+ * A value is its code times its block's scale.  head_dim is 64 or 128.
+ *
+ * The ragged batch.  B sequences, T new tokens in all (device arrays):
+ *   q_start   int32 [B+1]: sequence b's new tokens are rows q_start[b] ..
+ *             q_start[b+1] - 1; q_start[0] = 0, non-decreasing, q_start[B] = T
+ *   kv_len    int32 [B]: cached tokens of the sequence INCLUDING the new ones;
+ *             the i-th of n new tokens is token kv_len[b] - n + i
+ *   block_table int32 [B][max_pages]: token a of the sequence is slot
+ *             a % page_size of page block_table[b][a / page_size].  A page
+ *             belongs to one sequence while it is written to.  Entries of pages
+ *             that hold no token of the sequence are not used.
+ * max_q_len bounds the new tokens of a sequence on the host (1 <= max_q_len).
+ * Contents that break these rules give unspecified values, but no access
+ * outside the arrays: token rows, page ids and table columns are checked in
+ * the kernels. */
+
+/* Rotation of q and k by position, quantisation of k and v, and their append
+ * to the cache.  For every new token t and head, with R = rot_dim / 2 pairs:
+ *   pair i is (x[i], x[i + R]), or (x[2i], x[2i + 1]) if interleaved != 0
+ *   (a, b) -> (a c - b s, b c + a s), c = cos_sin[p][i], s = cos_sin[p][R + i],
+ *   p = positions[pair_axis[i]][t]  (fp32; products and sums rounded one by one)
+ * Channels from rot_dim on stay as they are.  q_out is the rotated q, rounded
+ * once to bf16 (it may be q itself).  The rotated k (fp32) and v are quantised:
+ * a block's scale byte is the smallest b >= 1 with max|x| <= 448 * 2^(b - 127)
+ * over the block's new tokens, but never less than the block's present byte if
+ * the block holds earlier tokens of the sequence; if the byte grows, the
+ * earlier tokens' codes are re-expressed in the new scale (exact unless they
+ * leave E4M3's normal range, then rounded to nearest even).  Codes round to
+ * nearest, ties to even.  NaN, infinities and magnitudes above 448 * 2^119 become
+ * NaN codes and do not enter the scale.  Slots of later tokens are left as they are.
+ *   q [T][q_heads][head_dim] bf16, k and v [T][kv_heads][head_dim] bf16; the
+ *          token strides q_stride, k_stride, v_stride, q_out_stride are in
+ *          elements (multiples of 8, at least heads * head_dim), so q, k and v
+ *          can be slices of one product's rows.  q_heads = 0 (q, q_out NULL)
+ *          appends only.
+ *   positions int32 [axes][T], 1 <= axes <= 4
+ *   pair_axis HOST array uint8 [rot_dim/2], each < axes, or NULL (all 0); read
+ *          before the call returns
+ *   cos_sin fp32 [n_pos][rot_dim]: R cosines, then R sines.  A position outside
+ *          [0, n_pos) makes the pairs that use it NaN.
+ * rot_dim % 16 == 0, 0 <= rot_dim <= head_dim.  T = 0 or B = 0 does nothing.
+ * One launch.  Bit-exact. */
+biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_scales,
+                               uint8_t *v_scales, int32_t num_pages, int32_t kv_heads,
+                               int32_t page_size, int32_t head_dim,
+                               const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                               int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                               int32_t q_heads, const int32_t *positions, int32_t axes,
+                               const uint8_t *pair_axis, const float *cos_sin, int32_t n_pos,
+                               int32_t rot_dim, int32_t interleaved,
+                               const int32_t *q_start, const int32_t *kv_len,
+                               const int32_t *block_table, int32_t max_pages, int32_t B,
+                               int32_t T, int32_t max_q_len, uint16_t *q_out,
+                               int64_t q_out_stride, hipStream_t stream);
+
+/* Causal attention of the new tokens over the cache.  Query head h reads
+ * key/value head h / (q_heads / kv_heads).  A token at position p (its place in
+ * the sequence) sees token j when j <= p and, with window > 0, also
+ * p - j < window or j < sinks (the first tokens stay visible):
+ *   s_j = scale * q . k_j,  w = softmax over the visible j,  o = sum_j w_j v_j
+ *   lse = log(sum over visible j of exp(s_j))
+ * A row that sees nothing (more new tokens than cached ones) gives o = 0 and
+ * lse = -inf.  Tokens that a row does not see never affect it, whatever their
+ * codes hold (NaN included).  Sums, maxima and o are kept in fp32; the weights
+ * are rounded to bf16 for the product with v, whose codes and scales are exact
+ * in bf16.
+ *   q [T][q_heads][head_dim] bf16 and o likewise, token strides in elements
+ *     (multiples of 8); o must not overlap an input
+ *   lse fp32 [T][q_heads] or NULL
+ *   window 0: no window.  sinks >= 0.  scale finite and > 0.
+ *   max_kv_len bounds kv_len on the host; it and max_q_len shape the launch.
+ *   workspace: >= biloco_attn_workspace_bytes(...) bytes, no fill needed; not
+ *     shared by calls that can run at the same time.
+ * q_heads must be a multiple of kv_heads.  T = 0 or B = 0 does nothing.
+ * One to three launches. */
+biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
+                                const uint8_t *k_scales, const uint8_t *v_scales,
+                                int32_t num_pages, int32_t kv_heads, int32_t page_size,
+                                int32_t head_dim, const uint16_t *q, int64_t q_stride,
+                                int32_t q_heads, const int32_t *q_start, const int32_t *kv_len,
+                                const int32_t *block_table, int32_t max_pages, int32_t B,
+                                int32_t T, int32_t max_q_len, int32_t max_kv_len, float scale,
+                                int32_t window, int32_t sinks, uint16_t *o, int64_t o_stride,
+                                float *lse, void *workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* Bytes of workspace biloco_attn_paged needs for these sizes (0 is possible).
+ * No HIP call. */
+biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
+                                          int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
+                                          size_t *bytes);
+
+/* The norm after a block, its gate and residual scale, and the norm before the
+ * next block, for each of T rows of C channels:
+ *   n  = x * rsqrt(mean(x^2) + eps) * (w_offset + post_w)   (x if post_w is NULL)
+ *   r' = res + res_scale * gate * n                          (gate 1 if NULL)
+ *   h  = r' * rsqrt(mean(r'^2) + eps) * (w_offset + pre_w)
+ * in fp32; res_out is r' rounded once to its type, h is computed from the
+ * unrounded r' and rounded once to bf16.  With a_codes and a_scales (both or
+ * neither) h's FP4 quantisation is written too, bit for bit what
+ * biloco_quant_act_fp4 makes of h: the next product's activation operands.
+ *   x bf16, gate bf16 (gate_stride 0: one row for all tokens), res and res_out
+ *   bf16, or fp32 if res_fp32 != 0; h bf16; post_w and pre_w bf16 [C].  Row
+ *   strides in elements, at least C.  res_out may be res (same stride).
+ *   a_codes [T][C/2], a_scales [T][C/16]: C % 32 == 0.
+ * 1 <= C <= 32768, any C (multiples of 8 with strides that are multiples of 8
+ * run faster).  T = 0 does nothing.  One launch. */
+biloco_status biloco_norm_gate_residual(const uint16_t *x, int64_t x_stride,
+                                        const uint16_t *post_w, const uint16_t *gate,
+                                        int64_t gate_stride, float res_scale, const void *res,
+                                        int64_t res_stride, int32_t res_fp32,
+                                        const uint16_t *pre_w, float eps, float w_offset,
+                                        int32_t T, int32_t C, void *res_out,
+                                        int64_t res_out_stride, uint16_t *h, int64_t h_stride,
+                                        uint8_t *a_codes, uint8_t *a_scales, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
