@@ -18,8 +18,8 @@ LIB = os.path.join(PKG, "libbiloco_hip.so")
 
 SOURCES = ["biloco_api.cpp", "k_prep.hip", "k_unfused.hip", "k_fused_gemv.hip", "k_fused_mfma.hip",
            "k_composed.hip", "k_peel.hip", "scratch.hip", "biloco_layer_api.cpp", "k_kv_append.hip",
-           "k_attn.hip", "k_norm.hip"]
-HEADERS = ["biloco_device.h", "biloco_internal.h", os.path.join("..", "..", "include", "biloco.h")]
+           "k_attn.hip", "k_attn_tiles.hip", "k_norm.hip"]
+HEADERS = ["biloco_device.h", "biloco_internal.h", "attn_device.h", os.path.join("..", "..", "include", "biloco.h")]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

@@ -139,7 +139,7 @@ biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads,
     if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, 1);
     if (st != BILOCO_OK) return st;
     if (q_heads % kv_heads != 0) return BILOCO_ERR_INVALID_VALUE;
-    if (q_heads > 4096) return BILOCO_ERR_UNSUPPORTED;
+    if (q_heads > 4096 || (int64_t)T * q_heads > INT32_MAX) return BILOCO_ERR_UNSUPPORTED;
     *bytes = attn_ws_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
     return BILOCO_OK;
 }

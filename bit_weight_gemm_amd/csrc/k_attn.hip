@@ -20,121 +20,15 @@
 // 4 q4 + i of the tiles f = 0, 1 are tokens 32 kk + 8 q4 + 4 f + i.  Channels
 // are taken in the order in which a lane's 16-byte load brings them: channel
 // 64 c + 16 q4 + 8 s + j is slot 8 q4 + j of step (c, s).
-#include "biloco_device.h"
-#include "biloco_internal.h"
+#include "attn_device.h"
 
 namespace biloco {
 
 namespace {
 
-typedef __bf16 bf16x2a_t __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8a_t __attribute__((ext_vector_type(8)));
-typedef float f32x2a_t __attribute__((ext_vector_type(2)));
-typedef float f32x4a_t __attribute__((ext_vector_type(4)));
+using namespace attn;
 
-constexpr int kChunk = 64;         // tokens a wave takes at a time
-constexpr int kWaves = 4;          // waves of a workgroup, one chunk each per unit
 constexpr int kSplitGrid = 512;    // workgroups of a call that splits the token axis
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ f32x4a_t mfma16(u32x4_t a, u32x4_t b, f32x4a_t c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8a_t, a),
-                                                   __builtin_bit_cast(bf16x8a_t, b), c, 0, 0, 0);
-}
-// Eight codes times a power of two as eight bf16.
-__device__ __forceinline__ u32x4_t widen8(uint32_t lo, uint32_t hi, float s) {
-    u32x4_t r;
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
-    return r;
-}
-__device__ __forceinline__ uint32_t narrow2a(float a, float b) {      // round to nearest even
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2a_t){a, b}, bf16x2a_t));
-}
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-__device__ __forceinline__ float exp2a(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// One sequence of the batch: its rows and the tokens they see, as chunks of
-// 64 in the order sinks, then window.
-struct Seq {
-    int first, n, past;      // first row, rows, position of the first new token
-    int lo, hi;              // tokens [lo, hi) by the window, plus those below `sinks`
-    int lo0, ns, nc;         // first chunk's start, sink chunks, chunks
-    int tiles;               // row tiles
-    int units;               // 4-chunk units of an item (at least one if it has rows)
-};
-
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    const uint32_t lo = (uint32_t)uniform((int)(uint32_t)v), hi = (uint32_t)uniform((int)(v >> 32));
-    return (int64_t)(((uint64_t)hi << 32) | lo);
-}
-
-__device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, int kv_len, int tile_rows) {
-    Seq s;
-    s.first = min(max(start, 0), a.T);
-    s.n = min(max(stop, s.first), a.T) - s.first;
-    const int len = (int)min((int64_t)max(kv_len, 0), (int64_t)a.max_pages * a.page);
-    s.past = len - s.n;
-    s.hi = len;
-    s.lo = a.window > 0 ? max(s.past - a.window + 1, 0) : 0;
-    s.lo0 = s.lo & ~(kChunk - 1);
-    const int sink = min(a.sinks, s.lo0);
-    s.ns = (sink + kChunk - 1) / kChunk;
-    s.nc = s.ns + (max(s.hi - s.lo0, 0) + kChunk - 1) / kChunk;
-    const int64_t rows = (int64_t)s.n * (a.q_heads / a.kv_heads);
-    s.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-    s.units = s.n > 0 ? max((s.nc + kWaves - 1) / kWaves, 1) : 0;
-    return s;
-}
-
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int tile_rows) {
-    return seq_from(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], tile_rows);
-}
-// The same for a sequence that the whole workgroup works on: held in scalar
-// registers.
-__device__ __forceinline__ Seq seq_uniform(const AttnArgs &a, int b, int tile_rows) {
-    return seq_from(a, uniform(a.q_start[b]), uniform(a.q_start[b + 1]), uniform(a.kv_len[b]), tile_rows);
-}
-
-// Work is a flat list of units: sequence, key/value head, row tile, unit.
-__device__ __forceinline__ int64_t seq_units(const AttnArgs &a, const Seq &s) {
-    return (int64_t)s.units * s.tiles * a.kv_heads;
-}
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor((long long)v, o, 64);
-    return v;
-}
-__device__ __forceinline__ int64_t total_units(const AttnArgs &a, int tile_rows) {
-    int64_t sum = 0;
-    for (int b = threadIdx.x & 63; b < a.B; b += 64) sum += seq_units(a, seq_of(a, b, tile_rows));
-    return wave_sum64(sum);
-}
-// The sequence that holds unit u, and the units before it.  u < total.
-__device__ __forceinline__ int find_seq(const AttnArgs &a, int tile_rows, int64_t u, int64_t &before) {
-    const int lane = threadIdx.x & 63;
-    before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-        const int64_t mine = b0 + lane < a.B ? seq_units(a, seq_of(a, b0 + lane, tile_rows)) : 0;
-        int64_t upto = mine;      // inclusive prefix sum
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int64_t t = __shfl_up((long long)upto, o, 64);
-            if (lane >= o) upto += t;
-        }
-        const uint64_t past = __ballot(before + upto > u);
-        if (past) {
-            const int l = __ffsll((long long)past) - 1;
-            before += __shfl((long long)(upto - mine), l, 64);
-            return b0 + l;
-        }
-        before += __shfl((long long)upto, 63, 64);
-    }
-    return a.B - 1;
-}
 
 template <int D>
 struct Stage {
@@ -185,9 +79,7 @@ struct Piece {
         }
     }
 
-    __device__ __forceinline__ int start_of(int c) const {
-        return c < s.ns ? c * kChunk : s.lo0 + (c - s.ns) * kChunk;
-    }
+    __device__ __forceinline__ int start_of(int c) const { return s.c.start(c); }
 
     // Page of token j (a token past the last one reads the last one's page).
     __device__ __forceinline__ int page_of(int j) const {
@@ -232,28 +124,11 @@ struct Piece {
         }
     }
 
-    // No branches: `lo` is the window's first token of a row, 0 without one.
-    __device__ __forceinline__ int low_of(int pos) const { return a.window > 0 ? pos - a.window + 1 : 0; }
-    __device__ __forceinline__ bool sees(int pos, int lo, int j) const {
-        return (bool)((j <= pos) & ((j >= lo) | (j < a.sinks)));
-    }
-    static constexpr uint32_t kOnes = 0x38383838u;      // the code of 1, four times
-    // 0xFF for each NaN code (0x7F or 0xFF), else 0x00.
-    static __device__ __forceinline__ u32x4_t nan_bytes(u32x4_t w) {
-        const u32x4_t t = (w & 0x7F7F7F7Fu) + 0x01010101u;
-        return ((t & 0x80808080u) >> 7) * 255u;
-    }
-    // Four 0x00 / 0xFF bytes for four bits.
-    static __device__ __forceinline__ uint32_t spread4(uint32_t bits) {
-        return ((bits & 1u) | ((bits & 2u) << 7) | ((bits & 4u) << 14) | ((bits & 8u) << 21)) * 255u;
-    }
-
     // One chunk; the next one's keys are asked for as soon as this one's are
     // used up, its values likewise.
     __device__ __forceinline__ void step(Stage<D> &st, Pages &g, int chunk, int next, bool more) {
         const int j0 = start_of(chunk);
-        const bool full = j0 + kChunk - 1 <= p_min &&
-                          (a.window == 0 || p_max - j0 < a.window || j0 + kChunk <= a.sinks);
+        const bool full = all_see(a, p_min, p_max, j0);
         bool odd = false;
         if (!full) {
             // Tokens that no row sees can hold anything: zero codes, scale 1.
@@ -261,12 +136,7 @@ struct Piece {
             uint32_t bad = 0;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int t = j0 + 32 * kk + 8 * q4 + j;
-                    bits |= (uint32_t)((t <= p_max) & ((t >= low_of(p_min)) | (t < a.sinks))) << j;
-                }
+                const uint32_t bits = any_sees8(a, p_min, p_max, j0 + 32 * kk + 8 * q4);
                 const uint32_t m0 = spread4(bits), m1 = spread4(bits >> 4);
                 if (bits == 0) st.vs[kk] = 127;
 #pragma unroll
@@ -312,14 +182,14 @@ struct Piece {
                     mx = fmaxf(mx, sc[r][t][i]);
                 }
             if (!full) {      // the maximum is that of the visible
-                const int lo = low_of(p[r]);
+                const int lo = low_of(a, p[r]);
                 mx = -__builtin_inff();
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = j0 + 32 * (t >> 1) + 8 * q4 + 4 * (t & 1) + i;
-                        sc[r][t][i] = sees(p[r], lo, j) ? sc[r][t][i] : -__builtin_inff();
+                        sc[r][t][i] = sees(a, p[r], lo, j) ? sc[r][t][i] : -__builtin_inff();
                         mx = fmaxf(mx, sc[r][t][i]);
                     }
             }
@@ -377,10 +247,7 @@ struct Piece {
         for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-                uint32_t bits = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    bits |= (uint32_t)sees(p[r], low_of(p[r]), j0 + 32 * kk + 8 * q4 + j) << j;
+                const uint32_t bits = sees8(a, p[r], j0 + 32 * kk + 8 * q4);
                 const u32x4_t seen = widen8(spread4(bits) & kOnes, spread4(bits >> 4) & kOnes, 1.0f);
 #pragma unroll
                 for (int n = 0; n < D / 32; ++n) {
@@ -401,7 +268,7 @@ struct Piece {
 
     // The wave's share of units [u0, u1).
     __device__ __forceinline__ void run(int u0, int u1) {
-        const int c1 = min(u1 * kWaves, s.nc);
+        const int c1 = min(u1 * kWaves, s.c.nc);
         int c = u0 * kWaves + wave;
         if (c >= c1) return;
         Stage<D> st;
@@ -492,11 +359,16 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int wg, int slot) {
     return static_cast<float *>(a.ws) + (int64_t)(2 * wg + slot) * (16 * R) * (D + 2);
 }
 
+// Work is a flat list of units: sequence, key/value head, row tile, unit.
+__device__ __forceinline__ int64_t seq_units(const AttnArgs &a, const Seq &s) {
+    return (int64_t)s.units * s.tiles * a.kv_heads;
+}
+
 // direct: a workgroup an item (sequence, head, row tile).  Otherwise the flat
 // list of units is cut into equal shares, one a workgroup.
 template <int D, int R>
 __global__ void __launch_bounds__(256, D * R <= 128 ? 2 : 1)
-attn_rows_kernel(const AttnArgs a, int direct, int max_tiles) {
+attn_rows_kernel(const AttnArgs a, int which, int direct, int max_tiles) {
     __shared__ float lo[kWaves][16][D + 4];
     __shared__ float lm[kWaves][16][2];
     int64_t u = 0, end = 1, before = 0;
@@ -505,20 +377,23 @@ attn_rows_kernel(const AttnArgs a, int direct, int max_tiles) {
     if (direct) {
         const int tile = (int)(blockIdx.x % max_tiles), h = (int)(blockIdx.x / max_tiles % a.kv_heads);
         b = (int)(blockIdx.x / max_tiles / a.kv_heads);
-        s = seq_uniform(a, b, 16 * R);
+        s = seq_uniform(a, b, 16 * R, which);
         if (tile >= s.tiles) return;
         item = h * s.tiles + tile;
         u = (int64_t)item * s.units;
         end = u + s.units;
     } else {
-        const int64_t total = uniform(total_units(a, 16 * R));
+        const auto units = [&](int i) { return seq_units(a, seq_of(a, i, 16 * R, which)); };
+        int64_t total = 0;
+        for (int i = threadIdx.x & 63; i < a.B; i += 64) total += units(i);
+        total = uniform(wave_sum64(total));
         const int64_t share = (total + gridDim.x - 1) / gridDim.x;
         u = (int64_t)blockIdx.x * share;
         end = min(u + share, total);
         if (u >= end) return;
-        b = uniform(find_seq(a, 16 * R, u, before));
+        b = uniform(find_seq(a.B, u, before, units));
         before = uniform(before);
-        s = seq_uniform(a, b, 16 * R);
+        s = seq_uniform(a, b, 16 * R, which);
     }
     while (true) {
         item = (int)((u - before) / s.units);
@@ -533,7 +408,7 @@ attn_rows_kernel(const AttnArgs a, int direct, int max_tiles) {
         __syncthreads();      // lo and lm are free again
         while (u >= before + seq_units(a, s)) {      // ends: u < total
             before += seq_units(a, s);
-            s = seq_uniform(a, ++b, 16 * R);
+            s = seq_uniform(a, ++b, 16 * R, which);
         }
     }
 }
@@ -541,18 +416,18 @@ attn_rows_kernel(const AttnArgs a, int direct, int max_tiles) {
 // Joins the pieces of one row of an item that several workgroups shared.
 template <int D, int R>
 __global__ void __launch_bounds__(256)
-attn_join_kernel(const AttnArgs a, int shares, int max_tiles) {
+attn_join_kernel(const AttnArgs a, int which, int shares, int max_tiles) {
     __shared__ float lo[kWaves][D];
     __shared__ float ll[kWaves][2];
     const int row = (int)(blockIdx.x % (16 * R)), item = (int)(blockIdx.x / (16 * R));
     const int tile = item % max_tiles, h = item / max_tiles % a.kv_heads, b = item / max_tiles / a.kv_heads;
-    const Seq s = seq_of(a, b, 16 * R);
+    const Seq s = seq_of(a, b, 16 * R, which);
     const int G = a.q_heads / a.kv_heads;
     if (tile >= s.tiles || (int64_t)tile * 16 * R + row >= (int64_t)s.n * G) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t before = 0, total = 0;
     for (int i = lane; i < a.B; i += 64) {
-        const int64_t n = seq_units(a, seq_of(a, i, 16 * R));
+        const int64_t n = seq_units(a, seq_of(a, i, 16 * R, which));
         total += n;
         before += i < b ? n : 0;
     }
@@ -603,30 +478,41 @@ attn_join_kernel(const AttnArgs a, int shares, int max_tiles) {
 struct Plan {
     int R, max_tiles, direct, grid;
     int64_t items;
+    bool rows, tiles;      // which kernels the call needs
+    size_t rows_bytes, tiles_bytes;
 };
 
-// What the host can know: at most this many rows, tiles and units.
-Plan plan_of(int B, int T, int q_heads, int kv_heads, int max_q, int max_kv) {
+// What the host can know: at most this many rows, tiles and units.  A batch
+// of more tokens than its longest sequence has may hold sequences of few and
+// of many rows: both kernels are then launched, each taking its own.
+Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv) {
     Plan p;
-    const int64_t rows = (int64_t)(max_q < T ? max_q : T) * (q_heads / kv_heads);
+    const int G = q_heads / kv_heads;
+    const int64_t most = (int64_t)(max_q < T ? max_q : T) * G;
+    p.tiles = most > kMostRows;
+    p.rows = !p.tiles || B > 1;
+    const int64_t rows = p.tiles ? (most < kMostRows ? most : kMostRows) : most;
     p.R = rows <= 16 ? 1 : 2;
     p.max_tiles = (int)((rows + 16 * p.R - 1) / (16 * p.R));
     p.items = (int64_t)B * kv_heads * p.max_tiles;
     const int units = (max_kv + kChunk * kWaves - 1) / (kChunk * kWaves);
     p.direct = units <= 3;
     p.grid = p.direct ? 0 : kSplitGrid;
+    p.rows_bytes = p.rows ? (size_t)p.grid * 2 * (16 * p.R) * (dim + 2) * sizeof(float) : 0;
+    p.tiles_bytes = p.tiles ? attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv).ws_bytes : 0;
     return p;
 }
 
 template <int D, int R>
 hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
     if (p.items * 16 * R > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int which = p.tiles ? kFewRows : kAllSeqs;
     hipLaunchKernelGGL((attn_rows_kernel<D, R>), dim3((unsigned)(p.direct ? p.items : p.grid)), dim3(256), 0, stream,
-                       a, p.direct, p.max_tiles);
+                       a, which, p.direct, p.max_tiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.direct) return e;
-    hipLaunchKernelGGL((attn_join_kernel<D, R>), dim3((unsigned)(p.items * 16 * R)), dim3(256), 0, stream, a, p.grid,
-                       p.max_tiles);
+    hipLaunchKernelGGL((attn_join_kernel<D, R>), dim3((unsigned)(p.items * 16 * R)), dim3(256), 0, stream, a, which,
+                       p.grid, p.max_tiles);
     return hipGetLastError();
 }
 
@@ -639,12 +525,18 @@ hipError_t launch_dim(const AttnArgs &a, const Plan &p, hipStream_t stream) {
 
 size_t attn_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv) {
     if (B == 0 || T == 0) return 0;
-    const Plan p = plan_of(B, T, q_heads, kv_heads, max_q, max_kv);
-    return (size_t)p.grid * 2 * (16 * p.R) * (dim + 2) * sizeof(float);
+    const Plan p = plan_of(B, T, q_heads, kv_heads, dim, max_q, max_kv);
+    return p.rows_bytes + p.tiles_bytes;
 }
 
 hipError_t launch_attn(const AttnArgs &a, hipStream_t stream) {
-    const Plan p = plan_of(a.B, a.T, a.q_heads, a.kv_heads, a.max_q, a.max_kv);
+    const Plan p = plan_of(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_q, a.max_kv);
+    if (p.tiles) {      // first: the longest workgroups
+        AttnArgs t = a;
+        t.ws = static_cast<char *>(a.ws) + p.rows_bytes;
+        const hipError_t e = launch_attn_tiles(t, p.rows ? kManyRows : kAllSeqs, stream);
+        if (e != hipSuccess || !p.rows) return e;
+    }
     return a.dim == 64 ? launch_dim<64>(a, p, stream) : launch_dim<128>(a, p, stream);
 }
 
