@@ -45,6 +45,8 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lib = None
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class BilocoError(RuntimeError):
@@ -128,6 +130,10 @@ def _p(t):
 
 def _stream(stream):
     if stream is None:
+        # the current device's current stream, without building a Stream object
+        # (0.2 us instead of 2.9)
+        if torch.cuda.is_initialized():
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -298,6 +304,8 @@ def biloco_schedules_for(M: int, N: int, K: int, r: int) -> list:
 
 
 # ---------------------------------------------------------------- decoder-layer operators
+_bf16, _fp32, _int32, _uint8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
 # `cache` is the tuple (k_codes [pages][kv_heads][page][dim], v_codes
 # [pages][kv_heads][page/8][dim][8], k_scales [pages][kv_heads], v_scales
 # likewise), uint8, contiguous.  q, k, v and o are bf16 [tokens][heads][dim] whose
@@ -312,29 +320,32 @@ def biloco_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int
             new(num_pages, kv_heads), new(num_pages, kv_heads))
 
 
+# The checks below run on every call of a decode step: plain comparisons of
+# attributes, no helper objects.
+
 def _cache_args(cache):
     k, v, ks, vs = cache
-    pages, kv_heads, page, dim = k.shape
-    if tuple(v.shape) != (pages, kv_heads, page // 8, dim, 8) or tuple(ks.shape) != (pages, kv_heads) or \
-            tuple(vs.shape) != (pages, kv_heads):
+    shape = k.shape
+    pages, kv_heads, page, dim = shape
+    if v.shape != (pages, kv_heads, page // 8, dim, 8) or ks.shape != (pages, kv_heads) or \
+            vs.shape != (pages, kv_heads):
         raise ValueError("cache arrays of different shapes")
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
         raise ValueError("cache arrays must be contiguous")
-    return (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, kv_heads, page, dim)
+    return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, kv_heads, page, dim
 
 
-def _rows(t, heads, dim, what):
-    """Token stride of a [tokens][heads][dim] bf16 tensor."""
-    s = t.stride()
-    if t.dtype is not torch.bfloat16 or t.shape[1] != heads or t.shape[2] != dim or s[2] != 1 or \
-            (s[1] != dim and heads > 1):
-        raise ValueError(f"{what}: bf16 [tokens][{heads}][{dim}] with contiguous heads expected")
-    return s[0] if t.shape[0] > 1 else heads * dim
+def _rows(t, shape, what):
+    """Token stride of a bf16 tensor [tokens][heads][dim] whose heads are contiguous."""
+    a, b, c = t.stride()
+    if t.shape != shape or t.dtype is not _bf16 or c != 1 or (b != shape[2] and shape[1] > 1):
+        raise ValueError(f"{what}: bf16 {list(shape)} with contiguous heads expected")
+    return a if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _ints(t, shape, what):
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous int32 {shape} expected")
+    if t.shape != shape or t.dtype is not _int32 or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {list(shape)} expected")
     return t.data_ptr()
 
 
@@ -343,29 +354,34 @@ def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_
     """Rotate q and k, quantise and append k and v; returns q_out (None without q).
     positions int32 [axes][T]; cos_sin fp32 [n_pos][rot_dim] (None: no rotation);
     pair_axis: one byte per pair, the axis it turns by."""
-    cargs = _cache_args(cache)
-    kv_heads, dim = cargs[5], cargs[7]
-    T, B = k.shape[0], kv_len.shape[0]
-    n_pos, rot = cos_sin.shape if cos_sin is not None else (0, 0)
-    axes = positions.shape[0] if rot else 0
-    heads = q.shape[1] if q is not None else 0
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("q, k and v have different numbers of tokens")
+    ck, cv, cks, cvs, pages, kv_heads, page, dim = _cache_args(cache)
+    T, (B, max_pages) = k.shape[0], block_table.shape
+    rot = n_pos = axes = heads = sq = so = 0
+    pos = table = pq = po = None
+    if cos_sin is not None:
+        (n_pos, rot), axes = cos_sin.shape, positions.shape[0]
+        if cos_sin.dtype is not _fp32 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin: contiguous fp32 expected")
+        pos, table = _ints(positions, (axes, T), "positions"), cos_sin.data_ptr()
     if pair_axis is not None and len(pair_axis) != rot // 2:
         raise ValueError("pair_axis has one byte per pair")
-    if rot and (cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous()):
-        raise ValueError("cos_sin: contiguous fp32 expected")
-    if q is not None and q_out is None:
-        q_out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=q.device)
     if T == 0 or B == 0:      # empty tensors have no addresses
-        return q_out
-    _ok(lib().biloco_kv_append(
-        *cargs, _p(q), _rows(q, heads, dim, "q") if heads else 0, k.data_ptr(), _rows(k, kv_heads, dim, "k"),
-        v.data_ptr(), _rows(v, kv_heads, dim, "v"), heads, _ints(positions, (axes, T), "positions") if rot else None,
-        axes, pair_axis, _p(cos_sin), n_pos, rot, int(interleaved), _ints(q_start, (B + 1,), "q_start"),
-        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, block_table.shape[1]), "block_table"),
-        block_table.shape[1], B, T, max_q_len, _p(q_out),
-        _rows(q_out, heads, dim, "q_out") if heads else 0, _stream(stream)), "biloco_kv_append")
+        return q_out if q is None or q_out is not None else torch.empty_like(q)
+    kv = (T, kv_heads, dim)
+    sk, sv = _rows(k, kv, "k"), _rows(v, kv, "v")
+    if q is not None:
+        heads = q.shape[1]
+        qs = (T, heads, dim)
+        if q_out is None:
+            q_out = torch.empty(qs, dtype=_bf16, device=q.device)
+        sq, so = _rows(q, qs, "q"), _rows(q_out, qs, "q_out")
+        pq, po = q.data_ptr(), q_out.data_ptr()
+    st = lib().biloco_kv_append(
+        ck, cv, cks, cvs, pages, kv_heads, page, dim, pq, sq, k.data_ptr(), sk, v.data_ptr(), sv, heads, pos, axes,
+        pair_axis, table, n_pos, rot, interleaved, _ints(q_start, (B + 1,), "q_start"), _ints(kv_len, (B,), "kv_len"),
+        _ints(block_table, (B, max_pages), "block_table"), max_pages, B, T, max_q_len, po, so, _stream(stream))
+    if st:
+        _ok(st, "biloco_kv_append")
     return q_out
 
 
@@ -380,44 +396,40 @@ def biloco_attn_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, hea
 def biloco_attn_paged(cache, q, q_start, kv_len, block_table, max_q_len: int, max_kv_len: int, scale: float,
                       window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of the new tokens q over the cache; returns out."""
-    cargs = _cache_args(cache)
-    kv_heads, dim = cargs[5], cargs[7]
-    T, heads, _ = q.shape
-    B = kv_len.shape[0]
+    ck, cv, cks, cvs, pages, kv_heads, page, dim = _cache_args(cache)
+    shape = q.shape
+    T, heads, _ = shape
+    B, max_pages = block_table.shape
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=torch.bfloat16, device=q.device)
-    if out.shape[0] != T:
-        raise ValueError("out has another number of tokens than q")
-    if T == 0 or B == 0:
-        return out
-    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (T, heads)
-                            or not lse.is_contiguous()):
+        out = torch.empty((T, heads, dim), dtype=_bf16, device=q.device)
+    if lse is not None and (lse.shape != (T, heads) or lse.dtype is not _fp32 or not lse.is_contiguous()):
         raise ValueError("lse: contiguous fp32 [tokens][heads] expected")
+    if T == 0 or B == 0:      # empty tensors have no addresses
+        return out
+    shape = (T, heads, dim)
+    sq, so = _rows(q, shape, "q"), _rows(out, shape, "out")
     if workspace is None:
         n = biloco_attn_workspace_bytes(B, T, heads, kv_heads, dim, max_q_len, max_kv_len)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-    _ok(lib().biloco_attn_paged(
-        *cargs, q.data_ptr(), _rows(q, heads, dim, "q"), heads, _ints(q_start, (B + 1,), "q_start"),
-        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, block_table.shape[1]), "block_table"),
-        block_table.shape[1], B, T, max_q_len, max_kv_len, scale, window, sinks, out.data_ptr(),
-        _rows(out, heads, dim, "out"), _p(lse), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream)), "biloco_attn_paged")
+        workspace = torch.empty(max(n, 16), dtype=_uint8, device=q.device)
+    st = lib().biloco_attn_paged(
+        ck, cv, cks, cvs, pages, kv_heads, page, dim, q.data_ptr(), sq, heads, _ints(q_start, (B + 1,), "q_start"),
+        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, max_pages), "block_table"), max_pages, B, T, max_q_len,
+        max_kv_len, scale, window, sinks, out.data_ptr(), so, None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        _ok(st, "biloco_attn_paged")
     return out
 
 
-def _row_stride(t, T, C, dtypes, what):
-    if t.dtype not in dtypes or tuple(t.shape) != (T, C) or (t.stride(1) != 1 and C > 1):
-        raise ValueError(f"{what}: [{T}][{C}] of {dtypes} with contiguous rows expected")
-    return t.stride(0) if T > 1 else max(t.stride(0), C)
+def _row_stride(t, T, C, dtype, what):
+    a, b = t.stride()
+    if t.shape != (T, C) or t.dtype is not dtype or (b != 1 and C > 1):
+        raise ValueError(f"{what}: {dtype} [{T}][{C}] with contiguous rows expected")
+    return a if T > 1 else C
 
 
-_BF16 = (torch.bfloat16,)
-
-
-def _weight(w, C, what):
-    if w is None:
-        return None
-    if w.dtype is not torch.bfloat16 or tuple(w.shape) != (C,) or not w.is_contiguous():
+def _vector(w, C, what):
+    if w.shape != (C,) or w.dtype is not _bf16 or not w.is_contiguous():
         raise ValueError(f"{what}: contiguous bf16 [{C}] expected")
     return w.data_ptr()
 
@@ -429,26 +441,36 @@ def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: 
     gate [1][C] (every token) or [T][C].  a_codes and a_scales: h's FP4
     quantisation (outputs)."""
     T, C = x.shape
-    fp32 = res.dtype is torch.float32
-    kinds = (torch.float32,) if fp32 else _BF16
+    kind = res.dtype
+    if kind is not _fp32 and kind is not _bf16:
+        raise ValueError("res: bf16 or fp32 expected")
     if res_out is None:
-        res_out = torch.empty((T, C), dtype=res.dtype, device=x.device)
+        res_out = torch.empty((T, C), dtype=kind, device=x.device)
     if h is None:
-        h = torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
-    if T == 0:
+        h = torch.empty((T, C), dtype=_bf16, device=x.device)
+    if T == 0:      # empty tensors have no addresses
         return res_out, h
-    gate_stride = 0
+    gate_stride, pg, pc, ps = 0, None, None, None
     if gate is not None:
         one = gate.shape[0] == 1
-        gate_stride = _row_stride(gate, 1 if one else T, C, _BF16, "gate")
-        gate_stride = 0 if one else gate_stride
-    for t, shape, what in ((a_codes, (T, C // 2), "a_codes"), (a_scales, (T, C // 16), "a_scales")):
-        if t is not None and (t.dtype is not torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous()):
-            raise ValueError(f"{what}: contiguous uint8 {shape} expected")
-    _ok(lib().biloco_norm_gate_residual(
-        x.data_ptr(), _row_stride(x, T, C, _BF16, "x"), _weight(post_w, C, "post_w"), _p(gate), gate_stride,
-        res_scale, res.data_ptr(), _row_stride(res, T, C, kinds, "res"), int(fp32), _weight(pre_w, C, "pre_w"),
-        eps, w_offset, T, C, res_out.data_ptr(), _row_stride(res_out, T, C, kinds, "res_out"), h.data_ptr(),
-        _row_stride(h, T, C, _BF16, "h"), _p(a_codes), _p(a_scales), _stream(stream)),
-        "biloco_norm_gate_residual")
+        gate_stride = _row_stride(gate, 1 if one else T, C, _bf16, "gate")
+        if one and T > 1:
+            gate_stride = 0
+        pg = gate.data_ptr()
+    if a_codes is not None:
+        if a_codes.shape != (T, C // 2) or a_codes.dtype is not _uint8 or not a_codes.is_contiguous():
+            raise ValueError("a_codes: contiguous uint8 [tokens][C/2] expected")
+        pc = a_codes.data_ptr()
+    if a_scales is not None:
+        if a_scales.shape != (T, C // 16) or a_scales.dtype is not _uint8 or not a_scales.is_contiguous():
+            raise ValueError("a_scales: contiguous uint8 [tokens][C/16] expected")
+        ps = a_scales.data_ptr()
+    st = lib().biloco_norm_gate_residual(
+        x.data_ptr(), _row_stride(x, T, C, _bf16, "x"), None if post_w is None else _vector(post_w, C, "post_w"), pg,
+        gate_stride, res_scale, res.data_ptr(), _row_stride(res, T, C, kind, "res"), kind is _fp32,
+        _vector(pre_w, C, "pre_w"), eps, w_offset, T, C, res_out.data_ptr(),
+        _row_stride(res_out, T, C, kind, "res_out"), h.data_ptr(), _row_stride(h, T, C, _bf16, "h"), pc, ps,
+        _stream(stream))
+    if st:
+        _ok(st, "biloco_norm_gate_residual")
     return res_out, h

@@ -14,7 +14,6 @@ typedef float f32x4a_t __attribute__((ext_vector_type(4)));
 typedef float f32x16a_t __attribute__((ext_vector_type(16)));
 
 constexpr int kChunk = 64;         // tokens a wave takes at a time
-constexpr int kWaves = 4;          // waves of a workgroup
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ f32x4a_t mfma16(u32x4_t a, u32x4_t b, f32x4a_t c) {
@@ -90,9 +89,7 @@ __device__ __forceinline__ uint32_t spread4(uint32_t bits) {
 struct Seq {
     int first, n, past;      // first row, new tokens, position of the first one
     int hi;                  // tokens it has
-    Span64 c;                // its chunks
-    int tiles;               // row tiles
-    int units;               // 4-chunk units of an item (at least one if it has rows)
+    Span64 c;                // the chunks its rows need
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -101,7 +98,7 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, int kv_len, int tile_rows, int which) {
+__device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, int kv_len, int which) {
     Seq s;
     s.first = min(max(start, 0), a.T);
     s.n = min(max(stop, s.first), a.T) - s.first;
@@ -110,18 +107,16 @@ __device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, 
     s.hi = (int)min((int64_t)max(kv_len, 0), (int64_t)a.max_pages * a.page);
     s.past = s.hi - s.n;
     s.c = span_of(a, s.past, s.hi - 1);
-    s.tiles = s.n > 0 ? (rows + tile_rows - 1) / tile_rows : 0;
-    s.units = s.n > 0 ? max((s.c.nc + kWaves - 1) / kWaves, 1) : 0;
     return s;
 }
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int tile_rows, int which) {
-    return seq_from(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], tile_rows, which);
+__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int which) {
+    return seq_from(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], which);
 }
 // The same for a sequence that the whole workgroup works on: held in scalar
 // registers.
-__device__ __forceinline__ Seq seq_uniform(const AttnArgs &a, int b, int tile_rows, int which) {
-    return seq_from(a, uniform(a.q_start[b]), uniform(a.q_start[b + 1]), uniform(a.kv_len[b]), tile_rows, which);
+__device__ __forceinline__ Seq seq_uniform(const AttnArgs &a, int b, int which) {
+    return seq_from(a, uniform(a.q_start[b]), uniform(a.q_start[b + 1]), uniform(a.kv_len[b]), which);
 }
 
 __device__ __forceinline__ int64_t wave_sum64(int64_t v) {

@@ -21,7 +21,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128, kWaves = 4;
 constexpr int kWantItems = 512;      // workgroups that fill the chip (two a CU)
 
 __device__ __forceinline__ f32x16a_t mfma32(u32x4_t a, u32x4_t b, f32x16a_t c) {
@@ -261,6 +261,10 @@ __device__ __forceinline__ float *tile_part(const AttnArgs &a, int64_t item, int
     return static_cast<float *>(a.ws) + (item * splits + split) * kTileRows * (D + 2);
 }
 
+__device__ __forceinline__ int64_t tiles_of(const AttnArgs &a, const Seq &s) {
+    return (s.n * (a.q_heads / a.kv_heads) + kTileRows - 1) / kTileRows;
+}
+
 // Workgroups: row tile (the last first: under causality the longest),
 // split, key/value head.  Heads run fastest, so the tiles of one head meet in
 // one XCD's L2 where the number of heads is a multiple of 8.
@@ -271,9 +275,9 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
     const int h = (int)(blockIdx.x % a.kv_heads), rest = (int)(blockIdx.x / a.kv_heads);
     const int split = rest % splits, at = tiles - 1 - rest / splits;
     int64_t before = 0;
-    const int b = uniform(find_seq(a.B, at, before, [&](int i) { return (int64_t)seq_of(a, i, kTileRows, which).tiles; }));
+    const int b = uniform(find_seq(a.B, at, before, [&](int i) { return tiles_of(a, seq_of(a, i, which)); }));
     if (b < 0) return;
-    const Seq s = seq_uniform(a, b, kTileRows, which);
+    const Seq s = seq_uniform(a, b, which);
     const int G = a.q_heads / a.kv_heads, rows = s.n * G, r0 = (at - (int)uniform(before)) * kTileRows;
     const int shift = 31 - __clz(a.page), last = s.hi - 1;
     const int *table = a.table + (int64_t)b * a.max_pages;
@@ -352,9 +356,9 @@ attn_tiles_join_kernel(const AttnArgs a, int which, int splits) {
     const int64_t item = blockIdx.x / (kTileRows / 4);
     const int h = (int)(item % a.kv_heads), at = (int)(item / a.kv_heads);
     int64_t before = 0;
-    const int b = uniform(find_seq(a.B, at, before, [&](int i) { return (int64_t)seq_of(a, i, kTileRows, which).tiles; }));
+    const int b = uniform(find_seq(a.B, at, before, [&](int i) { return tiles_of(a, seq_of(a, i, which)); }));
     if (b < 0) return;
-    const Seq s = seq_uniform(a, b, kTileRows, which);
+    const Seq s = seq_uniform(a, b, which);
     const int G = a.q_heads / a.kv_heads, lane = threadIdx.x & 63;
     const int row = (int)(blockIdx.x % (kTileRows / 4)) * 4 + (int)(threadIdx.x >> 6);
     const int whole = (at - (int)uniform(before)) * kTileRows + row;
