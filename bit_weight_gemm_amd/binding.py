@@ -304,8 +304,6 @@ def biloco_schedules_for(M: int, N: int, K: int, r: int) -> list:
 
 
 # ---------------------------------------------------------------- decoder-layer operators
-_bf16, _fp32, _int32, _uint8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
 # `cache` is the tuple (k_codes [pages][kv_heads][page][dim], v_codes
 # [pages][kv_heads][page/8][dim][8], k_scales [pages][kv_heads], v_scales
 # likewise), uint8, contiguous.  q, k, v and o are bf16 [tokens][heads][dim] whose
@@ -320,33 +318,26 @@ def biloco_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int
             new(num_pages, kv_heads), new(num_pages, kv_heads))
 
 
-# The checks below run on every call of a decode step: plain comparisons of
-# attributes, no helper objects.
+# The checks of types, shapes and strides and the call itself are in a CPython
+# extension (csrc/layer_binding.cpp), which halves a decode step's calls.
 
-def _cache_args(cache):
-    k, v, ks, vs = cache
-    shape = k.shape
-    pages, kv_heads, page, dim = shape
-    if v.shape != (pages, kv_heads, page // 8, dim, 8) or ks.shape != (pages, kv_heads) or \
-            vs.shape != (pages, kv_heads):
-        raise ValueError("cache arrays of different shapes")
-    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
-        raise ValueError("cache arrays must be contiguous")
-    return k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, kv_heads, page, dim
+_layer = None
 
 
-def _rows(t, shape, what):
-    """Token stride of a bf16 tensor [tokens][heads][dim] whose heads are contiguous."""
-    a, b, c = t.stride()
-    if t.shape != shape or t.dtype is not _bf16 or c != 1 or (b != shape[2] and shape[1] > 1):
-        raise ValueError(f"{what}: bf16 {list(shape)} with contiguous heads expected")
-    return a if shape[0] > 1 else shape[1] * shape[2]
-
-
-def _ints(t, shape, what):
-    if t.shape != shape or t.dtype is not _int32 or not t.is_contiguous():
-        raise ValueError(f"{what}: contiguous int32 {list(shape)} expected")
-    return t.data_ptr()
+def _ext():
+    """The extension, calling the loaded library's entry points."""
+    global _layer
+    if _layer is None:
+        L = lib()
+        try:
+            from . import _layer_binding as m
+        except ImportError as e:
+            raise RuntimeError("the tensor binding is missing: build it with "
+                               "`python -m bit_weight_gemm_amd.build`") from e
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                 for f in (L.biloco_kv_append, L.biloco_attn_paged, L.biloco_norm_gate_residual)))
+        _layer = m
+    return _layer
 
 
 def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_table, max_q_len: int,
@@ -354,32 +345,12 @@ def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_
     """Rotate q and k, quantise and append k and v; returns q_out (None without q).
     positions int32 [axes][T]; cos_sin fp32 [n_pos][rot_dim] (None: no rotation);
     pair_axis: one byte per pair, the axis it turns by."""
-    ck, cv, cks, cvs, pages, kv_heads, page, dim = _cache_args(cache)
-    T, (B, max_pages) = k.shape[0], block_table.shape
-    rot = n_pos = axes = heads = sq = so = 0
-    pos = table = pq = po = None
-    if cos_sin is not None:
-        (n_pos, rot), axes = cos_sin.shape, positions.shape[0]
-        if cos_sin.dtype is not _fp32 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin: contiguous fp32 expected")
-        pos, table = _ints(positions, (axes, T), "positions"), cos_sin.data_ptr()
-    if pair_axis is not None and len(pair_axis) != rot // 2:
-        raise ValueError("pair_axis has one byte per pair")
-    if T == 0 or B == 0:      # empty tensors have no addresses
-        return q_out if q is None or q_out is not None else torch.empty_like(q)
-    kv = (T, kv_heads, dim)
-    sk, sv = _rows(k, kv, "k"), _rows(v, kv, "v")
-    if q is not None:
-        heads = q.shape[1]
-        qs = (T, heads, dim)
-        if q_out is None:
-            q_out = torch.empty(qs, dtype=_bf16, device=q.device)
-        sq, so = _rows(q, qs, "q"), _rows(q_out, qs, "q_out")
-        pq, po = q.data_ptr(), q_out.data_ptr()
-    st = lib().biloco_kv_append(
-        ck, cv, cks, cvs, pages, kv_heads, page, dim, pq, sq, k.data_ptr(), sk, v.data_ptr(), sv, heads, pos, axes,
-        pair_axis, table, n_pos, rot, interleaved, _ints(q_start, (B + 1,), "q_start"), _ints(kv_len, (B,), "kv_len"),
-        _ints(block_table, (B, max_pages), "block_table"), max_pages, B, T, max_q_len, po, so, _stream(stream))
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k.shape[0] == 0:      # an empty tensor has no address
+        return q_out
+    st = (_layer or _ext()).kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_table, max_q_len,
+                                      q_out, pair_axis, interleaved, _stream(stream))
     if st:
         _ok(st, "biloco_kv_append")
     return q_out
@@ -396,42 +367,21 @@ def biloco_attn_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, hea
 def biloco_attn_paged(cache, q, q_start, kv_len, block_table, max_q_len: int, max_kv_len: int, scale: float,
                       window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of the new tokens q over the cache; returns out."""
-    ck, cv, cks, cvs, pages, kv_heads, page, dim = _cache_args(cache)
-    shape = q.shape
-    T, heads, _ = shape
-    B, max_pages = block_table.shape
     if out is None:
-        out = torch.empty((T, heads, dim), dtype=_bf16, device=q.device)
-    if lse is not None and (lse.shape != (T, heads) or lse.dtype is not _fp32 or not lse.is_contiguous()):
-        raise ValueError("lse: contiguous fp32 [tokens][heads] expected")
-    if T == 0 or B == 0:      # empty tensors have no addresses
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if q.shape[0] == 0:      # an empty tensor has no address
         return out
-    shape = (T, heads, dim)
-    sq, so = _rows(q, shape, "q"), _rows(out, shape, "out")
     if workspace is None:
-        n = biloco_attn_workspace_bytes(B, T, heads, kv_heads, dim, max_q_len, max_kv_len)
-        workspace = torch.empty(max(n, 16), dtype=_uint8, device=q.device)
-    st = lib().biloco_attn_paged(
-        ck, cv, cks, cvs, pages, kv_heads, page, dim, q.data_ptr(), sq, heads, _ints(q_start, (B + 1,), "q_start"),
-        _ints(kv_len, (B,), "kv_len"), _ints(block_table, (B, max_pages), "block_table"), max_pages, B, T, max_q_len,
-        max_kv_len, scale, window, sinks, out.data_ptr(), so, None if lse is None else lse.data_ptr(),
-        workspace.data_ptr(), workspace.nbytes, _stream(stream))
+        _, kv_heads, _, dim = cache[0].shape
+        n = biloco_attn_workspace_bytes(kv_len.shape[0], q.shape[0], q.shape[1], kv_heads, dim, max_q_len, max_kv_len)
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+        if stream is not None:      # it may be given out again on its own stream
+            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    st = (_layer or _ext()).attn_paged(cache, q, q_start, kv_len, block_table, max_q_len, max_kv_len, scale, window,
+                                       sinks, out, lse, workspace, _stream(stream))
     if st:
         _ok(st, "biloco_attn_paged")
     return out
-
-
-def _row_stride(t, T, C, dtype, what):
-    a, b = t.stride()
-    if t.shape != (T, C) or t.dtype is not dtype or (b != 1 and C > 1):
-        raise ValueError(f"{what}: {dtype} [{T}][{C}] with contiguous rows expected")
-    return a if T > 1 else C
-
-
-def _vector(w, C, what):
-    if w.shape != (C,) or w.dtype is not _bf16 or not w.is_contiguous():
-        raise ValueError(f"{what}: contiguous bf16 [{C}] expected")
-    return w.data_ptr()
 
 
 def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
@@ -440,37 +390,14 @@ def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: 
     """r' = res + res_scale * gate * norm(x), h = norm(r'); returns (r', h).
     gate [1][C] (every token) or [T][C].  a_codes and a_scales: h's FP4
     quantisation (outputs)."""
-    T, C = x.shape
-    kind = res.dtype
-    if kind is not _fp32 and kind is not _bf16:
-        raise ValueError("res: bf16 or fp32 expected")
     if res_out is None:
-        res_out = torch.empty((T, C), dtype=kind, device=x.device)
+        res_out = torch.empty(res.shape, dtype=res.dtype, device=x.device)
     if h is None:
-        h = torch.empty((T, C), dtype=_bf16, device=x.device)
-    if T == 0:      # empty tensors have no addresses
+        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    if x.shape[0] == 0:      # an empty tensor has no address
         return res_out, h
-    gate_stride, pg, pc, ps = 0, None, None, None
-    if gate is not None:
-        one = gate.shape[0] == 1
-        gate_stride = _row_stride(gate, 1 if one else T, C, _bf16, "gate")
-        if one and T > 1:
-            gate_stride = 0
-        pg = gate.data_ptr()
-    if a_codes is not None:
-        if a_codes.shape != (T, C // 2) or a_codes.dtype is not _uint8 or not a_codes.is_contiguous():
-            raise ValueError("a_codes: contiguous uint8 [tokens][C/2] expected")
-        pc = a_codes.data_ptr()
-    if a_scales is not None:
-        if a_scales.shape != (T, C // 16) or a_scales.dtype is not _uint8 or not a_scales.is_contiguous():
-            raise ValueError("a_scales: contiguous uint8 [tokens][C/16] expected")
-        ps = a_scales.data_ptr()
-    st = lib().biloco_norm_gate_residual(
-        x.data_ptr(), _row_stride(x, T, C, _bf16, "x"), None if post_w is None else _vector(post_w, C, "post_w"), pg,
-        gate_stride, res_scale, res.data_ptr(), _row_stride(res, T, C, kind, "res"), kind is _fp32,
-        _vector(pre_w, C, "pre_w"), eps, w_offset, T, C, res_out.data_ptr(),
-        _row_stride(res_out, T, C, kind, "res_out"), h.data_ptr(), _row_stride(h, T, C, _bf16, "h"), pc, ps,
-        _stream(stream))
+    st = (_layer or _ext()).norm_gate_residual(x, res, pre_w, post_w, gate, res_scale, eps, w_offset, res_out, h,
+                                               a_codes, a_scales, _stream(stream))
     if st:
         _ok(st, "biloco_norm_gate_residual")
     return res_out, h

@@ -80,12 +80,42 @@ def build_floor(verbose: bool = True) -> str:
     return FLOOR_LIB
 
 
+BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
+BINDING = os.path.join(PKG, "_layer_binding.so")
+
+
+def build_binding(verbose: bool = True) -> str:
+    """The CPython extension that marshals torch tensors for the decoder-layer
+    entry points (host code only, g++ against torch's headers)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", BINDING_SRC, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += ["-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", f"-Wl,-rpath,{libs}"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{p.stderr}")
+    os.replace(tmp, BINDING)
+    if verbose:
+        print(f"built {BINDING}")
+    return BINDING
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
     usage: dict = {}
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, BUILD, (), usage), srcs))
+        binding.result()
     # the kernels' register use, for tests/test_build_resources.py
     import json
     with open(RESOURCES, "w") as f:
