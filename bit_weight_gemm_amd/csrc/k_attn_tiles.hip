@@ -37,7 +37,7 @@ __device__ __forceinline__ f32x16a_t zero16() {
 
 template <int D>
 struct TileLds {
-    uint8_t k[2][kChunk * D], v[2][kChunk * D];
+    alignas(16) uint8_t k[2][kChunk * D], v[2][kChunk * D];
     float ks[2][8], vs[2][8];      // per eight tokens
     uint16_t nan[2][kChunk * D / 16];      // NaN codes of each 16 bytes of v, valid where odd is set
     int odd[2][kWaves];
@@ -303,7 +303,7 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
                 ld.load(a, shift, h, span.start(c + 1));
                 if (c + 2 < c1) ld.look_up(a, table, shift, last, span.start(c + 2));
             }
-            if (j0 <= w.p_max) w.step(a, lds, buf, j0, c2);
+            w.step(a, lds, buf, j0, c2);
             if (c + 1 < c1) ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
             __syncthreads();
         }
