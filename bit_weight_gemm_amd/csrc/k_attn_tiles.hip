@@ -37,9 +37,10 @@ __device__ __forceinline__ f32x16a_t zero16() {
 
 template <int D>
 struct TileLds {
-    alignas(16) uint8_t k[2][kChunk * D], v[2][kChunk * D];
-    float ks[2][8], vs[2][8];      // per eight tokens
-    uint16_t nan[2][kChunk * D / 16];      // NaN codes of each 16 bytes of v, valid where odd is set
+    alignas(16) uint8_t k[2][kChunk * D];       // codes, rows of tokens (k_slot)
+    alignas(16) uint16_t v[2][kChunk * D];      // bf16 [token / 8][channel][8]
+    int ks[2][8];                               // scale bytes, per eight tokens
+    uint16_t nan[2][kChunk * D / 16];      // NaN codes of each 16 bytes of v's codes, valid where odd is set
     int odd[2][kWaves];
 };
 
@@ -50,50 +51,54 @@ __device__ __forceinline__ int k_slot(int token, int slot) {
     return token * D + 16 * (slot ^ (D == 128 ? (token >> 1) & 7 : (token >> 2) & 3));
 }
 
+// A chunk's way into LDS.  A thread moves 16 bytes N times: of K's token
+// tid / (D / 16) + 32 i, and of V's token group tid / (D / 2) + 4 i.  The
+// tokens of a wave lie within 16 aligned ones, so its pages are uniform.
 template <int D>
 struct Loader {
-    static constexpr int N = D / 64;      // 16-byte loads of K, and of V, a thread
+    static constexpr int N = D / 64;
     u32x4_t k[N], v[N];
-    uint32_t scale;
-    int idk[N], idv[N], ids;
+    uint32_t scale[N], kscale;      // of the value group; of eight keys (the first eight threads)
+    int id[N], kid;
 
     // The pages of the chunk at j0, one chunk ahead of their use.
-    __device__ __forceinline__ void look_up(const AttnArgs &a, const int *table, int shift, int last, int j0) {
-        const int tid = threadIdx.x;
+    __device__ __forceinline__ void look_up(const int *table, int shift, int last, int j0) {
+        const int wave = uniform((int)(threadIdx.x >> 6));
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            idk[i] = table[min(j0 + tid / (D / 16) + 32 * i, last) >> shift];
-            idv[i] = table[min(j0 + 8 * (tid / (D / 2) + 4 * i), last) >> shift];
-        }
-        ids = table[min(j0 + 8 * (tid & 7), last) >> shift];
+        for (int i = 0; i < N; ++i) id[i] = table[min(j0 + 32 * i + (N == 2 ? 8 : 16) * wave, last) >> shift];
+        kid = table[min(j0 + 8 * (int)(threadIdx.x & 7), last) >> shift];
     }
     __device__ __forceinline__ void load(const AttnArgs &a, int shift, int h, int j0) {
-        const int tid = threadIdx.x;
+        const int tid = threadIdx.x, wave = uniform(tid >> 6);
         const auto block = [&](int id) {
             return (int64_t)((uint32_t)id < (uint32_t)a.num_pages ? id : 0) * a.kv_heads + h;
         };
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int tk = (j0 + tid / (D / 16) + 32 * i) & (a.page - 1), tv = (j0 + 8 * (tid / (D / 2) + 4 * i)) & (a.page - 1);
-            k[i] = *reinterpret_cast<const u32x4_t *>(a.kc + (((block(idk[i]) << shift) + tk) * D + 16 * (tid % (D / 16))));
-            v[i] = *reinterpret_cast<const u32x4_t *>(a.vc + (((block(idv[i]) << shift) + tv) * D + 16 * (tid % (D / 2))));
+            const int64_t at = block(uniform(id[i]));
+            const int slot = (j0 + 32 * i + (N == 2 ? 8 : 16) * wave) & (a.page - 1);      // of the wave's first token
+            const int64_t from = ((at << shift) + slot) * D;
+            k[i] = *reinterpret_cast<const u32x4_t *>(a.kc + from + 16 * (tid & 63));
+            v[i] = *reinterpret_cast<const u32x4_t *>(a.vc + from + 16 * (tid & 63));
+            scale[i] = a.vs[at];
         }
-        scale = (tid & 8 ? a.vs : a.ks)[block(ids)];
+        if (wave == 0) kscale = a.ks[block(kid)];
     }
-    // Into LDS.  In a chunk that not every row of the tile (positions p_min to
-    // p_max) sees whole, tokens that no row sees can hold anything: their codes
-    // become zero and their scale 1.  NaN codes are taken out of the values and
-    // noted apart (see mark_nan).
+    // In a chunk that not every row of the tile (positions p_min to p_max) sees
+    // whole, tokens that no row sees can hold anything: their codes become zero
+    // and their scale 1.  NaN codes are taken out of the values and noted apart
+    // (see mark_nan).
     __device__ __forceinline__ void store(const AttnArgs &a, TileLds<D> &lds, int buf, int j0, int p_min, int p_max) {
         const int tid = threadIdx.x;
-        const bool whole = all_see(a, p_min, p_max, j0);
-        if (!whole) {
+        bool odd = false;
+        if (!all_see(a, p_min, p_max, j0)) {
             uint32_t any = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t bits = any_sees8(a, p_min, p_max, j0 + 8 * (tid / (D / 2) + 4 * i));
                 const uint32_t m0 = spread4(bits), m1 = spread4(bits >> 4);
                 v[i] &= u32x4_t{m0, m1, m0, m1};
+                if (bits == 0) scale[i] = 127;
                 const u32x4_t bad = nan_bytes(v[i]);
                 v[i] &= ~bad;
                 const u32x4_t four = ((bad & 0x08040201u) * 0x01010101u) >> 24;      // a bit a byte
@@ -101,21 +106,18 @@ struct Loader {
                 lds.nan[buf][tid + 256 * i] = (uint16_t)all;
                 any |= all;
             }
-            if (__ballot(any != 0)) {
-                if ((tid & 63) == 0) lds.odd[buf][tid >> 6] = 1;
-            } else if ((tid & 63) == 0) {
-                lds.odd[buf][tid >> 6] = 0;
-            }
-            if ((tid & 8) && any_sees8(a, p_min, p_max, j0 + 8 * (tid & 7)) == 0) scale = 127;
-        } else if ((tid & 63) == 0) {
-            lds.odd[buf][tid >> 6] = 0;
+            odd = __ballot(any != 0) != 0;
         }
+        if ((tid & 63) == 0) lds.odd[buf][tid >> 6] = odd;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             *reinterpret_cast<u32x4_t *>(&lds.k[buf][k_slot<D>(tid / (D / 16) + 32 * i, tid % (D / 16))]) = k[i];
-            *reinterpret_cast<u32x4_t *>(&lds.v[buf][16 * (tid + 256 * i)]) = v[i];
+            const float s = scale_of(scale[i]);
+            u32x4_t *to = reinterpret_cast<u32x4_t *>(&lds.v[buf][16 * (tid + 256 * i)]);
+            to[0] = widen8(v[i].x, v[i].y, s);
+            to[1] = widen8(v[i].z, v[i].w, s);
         }
-        if (tid < 16) (tid & 8 ? lds.vs : lds.ks)[buf][tid & 7] = scale_of(scale);
+        if (tid < 8) lds.ks[buf][tid] = (int)kscale;
     }
 };
 
@@ -149,7 +151,7 @@ struct Rows32 {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             sc[t] = zero16();
-            const float s = lds.ks[buf][4 * t + (token >> 3)];
+            const float s = scale_of(lds.ks[buf][4 * t + (token >> 3)]);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 const u32x4_t w = *reinterpret_cast<const u32x4_t *>(&lds.k[buf][k_slot<D>(32 * t + token, 2 * c + (lane >> 5))]);
@@ -199,15 +201,11 @@ struct Rows32 {
         const int lane = threadIdx.x & 63, h = lane >> 5;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float s = lds.vs[buf][2 * c + h];
 #pragma unroll
-            for (int n = 0; n < D / 64; ++n) {
-                const u32x4_t w =
-                    *reinterpret_cast<const u32x4_t *>(&lds.v[buf][(2 * c + h) * (8 * D) + 512 * n + 16 * (lane & 31)]);
-                o[2 * n] = mfma32(widen8(w.x, w.y, s), pt[c], o[2 * n]);
-                o[2 * n + 1] = mfma32(widen8(w.z, w.w, s), pt[c], o[2 * n + 1]);
+            for (int n = 0; n < D / 32; ++n) {
+                const u32x4_t w = *reinterpret_cast<const u32x4_t *>(&lds.v[buf][8 * ((2 * c + h) * D + 32 * n + (lane & 31))]);
+                o[n] = mfma32(w, pt[c], o[n]);
             }
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
 
@@ -216,22 +214,20 @@ struct Rows32 {
     __device__ __forceinline__ void mark_nan(const AttnArgs &a, const TileLds<D> &lds, int buf, int j0) {
         const int lane = threadIdx.x & 63, h = lane >> 5;
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n)
+        for (int n = 0; n < D / 32; ++n) {
+            f32x16a_t x = zero16();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                f32x16a_t x = zero16();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint32_t mine = sees8(a, p, j0 + 16 * c + 8 * h);
-                    const uint32_t bad = lds.nan[buf][(2 * c + h) * (D / 2) + 32 * n + (lane & 31)] >> (8 * k);
-                    x = mfma32(widen8(spread4(bad) & kOnes, spread4(bad >> 4) & kOnes, 1.0f),
-                               widen8(spread4(mine) & kOnes, spread4(mine >> 4) & kOnes, 1.0f), x);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[2 * n + k][i] = x[i] > 0.0f ? __builtin_nanf("") : o[2 * n + k][i];
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t mine = sees8(a, p, j0 + 16 * c + 8 * h);
+                const uint32_t bad = lds.nan[buf][(2 * c + h) * (D / 2) + 16 * n + ((lane & 31) >> 1)] >> (8 * (lane & 1));
+                x = mfma32(widen8(spread4(bad) & kOnes, spread4(bad >> 4) & kOnes, 1.0f),
+                           widen8(spread4(mine) & kOnes, spread4(mine >> 4) & kOnes, 1.0f), x);
                 __builtin_amdgcn_sched_barrier(0);
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[n][i] = x[i] > 0.0f ? __builtin_nanf("") : o[n][i];
+            __builtin_amdgcn_sched_barrier(0);
+        }
     }
 
     __device__ __forceinline__ void step(const AttnArgs &a, const TileLds<D> &lds, int buf, int j0, float c2) {
@@ -292,16 +288,16 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
     w.init(a, s, h, r0 + 32 * wave, rows);
     if (c0 < c1) {
         Loader<D> ld;
-        ld.look_up(a, table, shift, last, span.start(c0));
+        ld.look_up(table, shift, last, span.start(c0));
         ld.load(a, shift, h, span.start(c0));
-        if (c0 + 1 < c1) ld.look_up(a, table, shift, last, span.start(c0 + 1));
+        if (c0 + 1 < c1) ld.look_up(table, shift, last, span.start(c0 + 1));
         ld.store(a, lds, 0, span.start(c0), p_min, p_max);
         __syncthreads();
         for (int c = c0; c < c1; ++c) {
             const int buf = (c - c0) & 1, j0 = span.start(c);
             if (c + 1 < c1) {
                 ld.load(a, shift, h, span.start(c + 1));
-                if (c + 2 < c1) ld.look_up(a, table, shift, last, span.start(c + 2));
+                if (c + 2 < c1) ld.look_up(table, shift, last, span.start(c + 2));
             }
             w.step(a, lds, buf, j0, c2);
             if (c + 1 < c1) ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
@@ -314,16 +310,13 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
     if (row >= rows) return;
     if (splits > 1) {
         float *part = tile_part<D>(a, (int64_t)at * a.kv_heads + h, splits, split);
-        float *dst = part + (row - r0) * D + 8 * half;
+        float *dst = part + (row - r0) * D + 4 * half;
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n)
+        for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x16a_t &x = w.o[2 * n], &y = w.o[2 * n + 1];
-                float *to = dst + 64 * n + 16 * i;
-                *reinterpret_cast<f32x4a_t *>(to) = f32x4a_t{x[4 * i], y[4 * i], x[4 * i + 1], y[4 * i + 1]};
-                *reinterpret_cast<f32x4a_t *>(to + 4) = f32x4a_t{x[4 * i + 2], y[4 * i + 2], x[4 * i + 3], y[4 * i + 3]};
-            }
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
+                    f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
         if (half == 0) {
             part[kTileRows * D + 2 * (row - r0)] = w.m;
             part[kTileRows * D + 2 * (row - r0) + 1] = l;
@@ -333,19 +326,14 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int i = row / G, g = row - i * G;
     const int64_t t = s.first + i;
-    uint16_t *dst = a.o + t * a.o_stride + (int64_t)(h * G + g) * D + 8 * half;
+    uint16_t *dst = a.o + t * a.o_stride + (int64_t)(h * G + g) * D + 4 * half;
 #pragma unroll
-    for (int n = 0; n < D / 64; ++n)
+    for (int n = 0; n < D / 32; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f32x16a_t &x = w.o[2 * n], &y = w.o[2 * n + 1];
-            u32x4_t v;
-            v.x = narrow2a(x[4 * j] * inv, y[4 * j] * inv);
-            v.y = narrow2a(x[4 * j + 1] * inv, y[4 * j + 1] * inv);
-            v.z = narrow2a(x[4 * j + 2] * inv, y[4 * j + 2] * inv);
-            v.w = narrow2a(x[4 * j + 3] * inv, y[4 * j + 3] * inv);
-            *reinterpret_cast<u32x4_t *>(dst + 64 * n + 16 * j) = v;
-        }
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint2 *>(dst + 32 * n + 8 * j) =
+                make_uint2(narrow2a(w.o[n][4 * j] * inv, w.o[n][4 * j + 1] * inv),
+                           narrow2a(w.o[n][4 * j + 2] * inv, w.o[n][4 * j + 3] * inv));
     if (a.lse && half == 0) a.lse[t * a.q_heads + h * G + g] = (w.m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
