@@ -35,21 +35,18 @@ __device__ __forceinline__ f32x16a_t zero16() {
     return z;
 }
 
+// Codes wait in LDS as bf16, scale included: keys as [channel / 8][token][8],
+// values as [token / 8][channel][8], so that the 16-byte reads of both products
+// run over neighbouring addresses.  The rows of keys are 32 bytes longer than
+// their 64 tokens, which spreads the banks that a wave's writes meet.
 template <int D>
 struct TileLds {
-    alignas(16) uint8_t k[2][kChunk * D];       // codes, rows of tokens (k_slot)
-    alignas(16) uint16_t v[2][kChunk * D];      // bf16 [token / 8][channel][8]
-    int ks[2][8];                               // scale bytes, per eight tokens
+    static constexpr int kRow = 8 * kChunk + 16;
+    alignas(16) uint16_t k[2][D / 8 * kRow];
+    alignas(16) uint16_t v[2][kChunk * D];
     uint16_t nan[2][kChunk * D / 16];      // NaN codes of each 16 bytes of v's codes, valid where odd is set
     int odd[2][kWaves];
 };
-
-// 16-byte slot of a token's row of K in LDS: rotated so that the 16 tokens
-// that one phase of a 16-byte read takes lie in different banks.
-template <int D>
-__device__ __forceinline__ int k_slot(int token, int slot) {
-    return token * D + 16 * (slot ^ (D == 128 ? (token >> 1) & 7 : (token >> 2) & 3));
-}
 
 // A chunk's way into LDS.  A thread moves 16 bytes N times: of K's token
 // tid / (D / 16) + 32 i, and of V's token group tid / (D / 2) + 4 i.  The
@@ -58,15 +55,14 @@ template <int D>
 struct Loader {
     static constexpr int N = D / 64;
     u32x4_t k[N], v[N];
-    uint32_t scale[N], kscale;      // of the value group; of eight keys (the first eight threads)
-    int id[N], kid;
+    uint32_t kscale[N], vscale[N];
+    int id[N];
 
     // The pages of the chunk at j0, one chunk ahead of their use.
     __device__ __forceinline__ void look_up(const int *table, int shift, int last, int j0) {
         const int wave = uniform((int)(threadIdx.x >> 6));
 #pragma unroll
         for (int i = 0; i < N; ++i) id[i] = table[min(j0 + 32 * i + (N == 2 ? 8 : 16) * wave, last) >> shift];
-        kid = table[min(j0 + 8 * (int)(threadIdx.x & 7), last) >> shift];
     }
     __device__ __forceinline__ void load(const AttnArgs &a, int shift, int h, int j0) {
         const int tid = threadIdx.x, wave = uniform(tid >> 6);
@@ -80,9 +76,9 @@ struct Loader {
             const int64_t from = ((at << shift) + slot) * D;
             k[i] = *reinterpret_cast<const u32x4_t *>(a.kc + from + 16 * (tid & 63));
             v[i] = *reinterpret_cast<const u32x4_t *>(a.vc + from + 16 * (tid & 63));
-            scale[i] = a.vs[at];
+            kscale[i] = a.ks[at];
+            vscale[i] = a.vs[at];
         }
-        if (wave == 0) kscale = a.ks[block(kid)];
     }
     // In a chunk that not every row of the tile (positions p_min to p_max) sees
     // whole, tokens that no row sees can hold anything: their codes become zero
@@ -98,7 +94,7 @@ struct Loader {
                 const uint32_t bits = any_sees8(a, p_min, p_max, j0 + 8 * (tid / (D / 2) + 4 * i));
                 const uint32_t m0 = spread4(bits), m1 = spread4(bits >> 4);
                 v[i] &= u32x4_t{m0, m1, m0, m1};
-                if (bits == 0) scale[i] = 127;
+                if (bits == 0) vscale[i] = 127;
                 const u32x4_t bad = nan_bytes(v[i]);
                 v[i] &= ~bad;
                 const u32x4_t four = ((bad & 0x08040201u) * 0x01010101u) >> 24;      // a bit a byte
@@ -111,19 +107,20 @@ struct Loader {
         if ((tid & 63) == 0) lds.odd[buf][tid >> 6] = odd;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            *reinterpret_cast<u32x4_t *>(&lds.k[buf][k_slot<D>(tid / (D / 16) + 32 * i, tid % (D / 16))]) = k[i];
-            const float s = scale_of(scale[i]);
-            u32x4_t *to = reinterpret_cast<u32x4_t *>(&lds.v[buf][16 * (tid + 256 * i)]);
-            to[0] = widen8(v[i].x, v[i].y, s);
-            to[1] = widen8(v[i].z, v[i].w, s);
+            const float ks = scale_of(kscale[i]), vs = scale_of(vscale[i]);
+            uint16_t *kt = &lds.k[buf][2 * (tid % (D / 16)) * TileLds<D>::kRow + 8 * (tid / (D / 16) + 32 * i)];
+            *reinterpret_cast<u32x4_t *>(kt) = widen8(k[i].x, k[i].y, ks);
+            *reinterpret_cast<u32x4_t *>(kt + TileLds<D>::kRow) = widen8(k[i].z, k[i].w, ks);
+            u32x4_t *vt = reinterpret_cast<u32x4_t *>(&lds.v[buf][16 * (tid + 256 * i)]);
+            vt[0] = widen8(v[i].x, v[i].y, vs);
+            vt[1] = widen8(v[i].z, v[i].w, vs);
         }
-        if (tid < 8) lds.ks[buf][tid] = (int)kscale;
     }
 };
 
 template <int D>
 struct Rows32 {
-    u32x4_t q[D / 32][2];
+    u32x4_t q[D / 16];
     f32x16a_t o[D / 32];
     float m, l;      // m: of scale * log2(e) * s
     int p, p_min, p_max;
@@ -134,41 +131,46 @@ struct Rows32 {
         p = s.past + i;
         p_min = s.past + min(r0, rows - 1) / G;
         p_max = s.past + min(r0 + 31, rows - 1) / G;
-        const uint16_t *src = a.q + (int64_t)(s.first + i) * a.q_stride + (int64_t)(h * G + row - i * G) * D + 16 * (lane >> 5);
+        const uint16_t *src = a.q + (int64_t)(s.first + i) * a.q_stride + (int64_t)(h * G + row - i * G) * D + 8 * (lane >> 5);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) q[c][t] = *reinterpret_cast<const u32x4_t *>(src + 32 * c + 8 * t);
+        for (int c = 0; c < D / 16; ++c) q[c] = *reinterpret_cast<const u32x4_t *>(src + 16 * c);
 #pragma unroll
         for (int n = 0; n < D / 32; ++n) o[n] = zero16();
         m = -__builtin_inff();
         l = 0.0f;
     }
 
-    __device__ __forceinline__ void scores(const TileLds<D> &lds, int buf, f32x16a_t (&sc)[2]) const {
+    // Scores of the chunk's token tile t.
+    __device__ __forceinline__ f32x16a_t scores(const TileLds<D> &lds, int buf, int t) const {
         const int lane = threadIdx.x & 63, r = lane & 31;
         const int token = 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
+        const uint16_t *k = &lds.k[buf][(lane >> 5) * TileLds<D>::kRow + 8 * (32 * t + token)];
+        f32x16a_t sc = zero16();
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            sc[t] = zero16();
-            const float s = scale_of(lds.ks[buf][4 * t + (token >> 3)]);
+        for (int c = 0; c < D / 16; ++c)
+            sc = mfma32(*reinterpret_cast<const u32x4_t *>(k + 2 * c * TileLds<D>::kRow), q[c], sc);
+        return sc;
+    }
+
+    // Hides what a row does not see of the 32 tokens at j0.
+    __device__ __forceinline__ void hide(const AttnArgs &a, f32x16a_t &sc, int j0) const {
+        const int h = (threadIdx.x & 63) >> 5, lo = low_of(a, p);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                const u32x4_t w = *reinterpret_cast<const u32x4_t *>(&lds.k[buf][k_slot<D>(32 * t + token, 2 * c + (lane >> 5))]);
-                sc[t] = mfma32(widen8(w.x, w.y, s), q[c][0], sc[t]);
-                sc[t] = mfma32(widen8(w.z, w.w, s), q[c][1], sc[t]);
-                if (c & 1) __builtin_amdgcn_sched_barrier(0);      // bounds the registers of codes made wide
-            }
+        for (int i = 0; i < 16; ++i) {
+            const int j = j0 + 16 * (i >> 3) + 8 * h + (i & 7);
+            sc[i] = sees(a, p, lo, j) ? sc[i] : -__builtin_inff();
         }
     }
 
-    // Scores to weights (at most 2^8 times a row's present maximum's: the
-    // sums are moved to a new maximum only when it is that much larger).
-    __device__ __forceinline__ void weigh(f32x16a_t (&sc)[2], float c2, u32x4_t (&pt)[4]) {
-        float mx = fmaxf(sc[0][0], sc[1][0]);
+    __device__ __forceinline__ float top_of(const f32x16a_t &sc, float c2) const {
+        float mx = sc[0];
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, fmaxf(sc[0][i], sc[1][i]));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64)) * c2;
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
+        return fmaxf(mx, __shfl_xor(mx, 32, 64)) * c2;
+    }
+    // The sums move to a new maximum only when it is much larger (the weights
+    // stay below 2^8 of a row's present one's).
+    __device__ __forceinline__ void follow(float mx) {
         if (__ballot(mx > m + 8.0f)) {
             const float mn = fmaxf(m, mx);
             const float alpha = mn == -__builtin_inff() ? 1.0f : exp2a(m - mn);
@@ -177,36 +179,32 @@ struct Rows32 {
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) o[n] *= alpha;
         }
+    }
+    // Scores to weights, rounded to bf16 for the product (2^-8 of each at
+    // most); their sum is taken before that.
+    __device__ __forceinline__ void weigh(f32x16a_t &sc, float c2, u32x4_t (&pt)[2]) {
         const float base = m == -__builtin_inff() ? 0.0f : m;      // a row that sees nothing yet
         float sum = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sc[t][i] = exp2a(__builtin_fmaf(sc[t][i], c2, -base));
-                sum += sc[t][i];
-            }
-        l += sum;
-        // Rounded to bf16 (2^-8 of each at most); their sum l is kept as it was.
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const f32x16a_t &x = sc[c >> 1];
-            const int i = 8 * (c & 1);
-            pt[c] = u32x4_t{narrow2a(x[i], x[i + 1]), narrow2a(x[i + 2], x[i + 3]), narrow2a(x[i + 4], x[i + 5]),
-                            narrow2a(x[i + 6], x[i + 7])};
+        for (int i = 0; i < 16; ++i) {
+            sc[i] = exp2a(__builtin_fmaf(sc[i], c2, -base));
+            sum += sc[i];
         }
+        l += sum;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            pt[c] = u32x4_t{narrow2a(sc[8 * c], sc[8 * c + 1]), narrow2a(sc[8 * c + 2], sc[8 * c + 3]),
+                            narrow2a(sc[8 * c + 4], sc[8 * c + 5]), narrow2a(sc[8 * c + 6], sc[8 * c + 7])};
     }
 
-    __device__ __forceinline__ void gather(const TileLds<D> &lds, int buf, const u32x4_t (&pt)[4]) {
-        const int lane = threadIdx.x & 63, h = lane >> 5;
+    __device__ __forceinline__ void gather(const TileLds<D> &lds, int buf, int t, const u32x4_t (&pt)[2]) {
+        const int lane = threadIdx.x & 63;
+        const uint16_t *v = &lds.v[buf][8 * ((4 * t + (lane >> 5)) * D + (lane & 31))];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int n = 0; n < D / 32; ++n) {
-                const u32x4_t w = *reinterpret_cast<const u32x4_t *>(&lds.v[buf][8 * ((2 * c + h) * D + 32 * n + (lane & 31))]);
-                o[n] = mfma32(w, pt[c], o[n]);
-            }
-        }
+            for (int n = 0; n < D / 32; ++n)
+                o[n] = mfma32(*reinterpret_cast<const u32x4_t *>(v + 16 * c * D + 256 * n), pt[c], o[n]);
     }
 
     // NaN values, taken out of the product: a row that sees one gets NaN in its
@@ -228,25 +226,6 @@ struct Rows32 {
             for (int i = 0; i < 16; ++i) o[n][i] = x[i] > 0.0f ? __builtin_nanf("") : o[n][i];
             __builtin_amdgcn_sched_barrier(0);
         }
-    }
-
-    __device__ __forceinline__ void step(const AttnArgs &a, const TileLds<D> &lds, int buf, int j0, float c2) {
-        f32x16a_t sc[2];
-        u32x4_t pt[4];
-        scores(lds, buf, sc);
-        if (!all_see(a, p_min, p_max, j0)) {
-            const int h = (threadIdx.x & 63) >> 5, lo = low_of(a, p);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int j = j0 + 32 * t + 16 * (i >> 3) + 8 * h + (i & 7);
-                    sc[t][i] = sees(a, p, lo, j) ? sc[t][i] : -__builtin_inff();
-                }
-        }
-        weigh(sc, c2, pt);
-        if (lds.odd[buf][0] | lds.odd[buf][1] | lds.odd[buf][2] | lds.odd[buf][3]) mark_nan(a, lds, buf, j0);
-        gather(lds, buf, pt);
     }
 };
 
@@ -287,21 +266,50 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
     Rows32<D> w;
     w.init(a, s, h, r0 + 32 * wave, rows);
     if (c0 < c1) {
+        // Two 32-token tiles a chunk.  The scores of a tile are computed while
+        // the one before goes through its exponentials, its maximum while that
+        // one's values are gathered.
         Loader<D> ld;
         ld.look_up(table, shift, last, span.start(c0));
         ld.load(a, shift, h, span.start(c0));
         if (c0 + 1 < c1) ld.look_up(table, shift, last, span.start(c0 + 1));
         ld.store(a, lds, 0, span.start(c0), p_min, p_max);
+        if (c0 + 1 < c1) {
+            ld.load(a, shift, h, span.start(c0 + 1));
+            if (c0 + 2 < c1) ld.look_up(table, shift, last, span.start(c0 + 2));
+        }
         __syncthreads();
+        f32x16a_t s0 = w.scores(lds, 0, 0), s1;
+        bool whole = all_see(a, w.p_min, w.p_max, span.start(c0));
+        if (!whole) w.hide(a, s0, span.start(c0));
+        w.follow(w.top_of(s0, c2));
         for (int c = c0; c < c1; ++c) {
             const int buf = (c - c0) & 1, j0 = span.start(c);
-            if (c + 1 < c1) {
-                ld.load(a, shift, h, span.start(c + 1));
-                if (c + 2 < c1) ld.look_up(table, shift, last, span.start(c + 2));
+            const bool more = c + 1 < c1;
+            u32x4_t pt[2];
+            if (c > c0) __syncthreads();      // the other buffer has been read
+            if (more) {
+                ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
+                if (c + 2 < c1) {
+                    ld.load(a, shift, h, span.start(c + 2));
+                    if (c + 3 < c1) ld.look_up(table, shift, last, span.start(c + 3));
+                }
             }
-            w.step(a, lds, buf, j0, c2);
-            if (c + 1 < c1) ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
-            __syncthreads();
+            if (lds.odd[buf][0] | lds.odd[buf][1] | lds.odd[buf][2] | lds.odd[buf][3]) w.mark_nan(a, lds, buf, j0);
+            w.weigh(s0, c2, pt);
+            s1 = w.scores(lds, buf, 1);
+            if (!whole) w.hide(a, s1, j0 + 32);
+            w.gather(lds, buf, 0, pt);
+            w.follow(w.top_of(s1, c2));
+            __syncthreads();      // the next chunk is in place
+            w.weigh(s1, c2, pt);
+            if (more) {
+                s0 = w.scores(lds, buf ^ 1, 0);
+                whole = all_see(a, w.p_min, w.p_max, span.start(c + 1));
+                if (!whole) w.hide(a, s0, span.start(c + 1));
+            }
+            w.gather(lds, buf, 1, pt);
+            if (more) w.follow(w.top_of(s0, c2));
         }
     }
 
