@@ -2,17 +2,24 @@
 // (prompts and their chunks).
 //
 // A workgroup takes 128 rows of one key/value head (a wave 32) and walks the
-// 64-token chunks they see, codes staged in LDS, the next chunk's under way in
-// registers meanwhile.  As in the kernel for few rows the products are
-// S^T = K Q^T and O^T = V^T P^T, here as 32 x 32 tiles, so that a lane holds
-// successive tokens of one row (l & 31) and the weights go from the first
-// product to the second without leaving their registers:
+// 64-token chunks they see, as bf16 in LDS (each code is made wide once for the
+// 128 rows), the next chunk on its way in registers meanwhile.  As in the kernel
+// for few rows the products are S^T = K Q^T and O^T = V^T P^T, here as 32 x 32
+// tiles, so that a lane holds successive tokens of one row (l & 31) and the
+// weights go from the first product to the second without leaving their
+// registers:
 //   A row 8a + 4h + b of token tile t is token 32 t + 16 (a >> 1) + 8 h + 4 (a & 1) + b,
 //   so C register 4a + b of lane half h is that token, and registers 8c .. 8c + 7
 //   are the eight tokens 32 t + 16 c + 8 h + (0 .. 7), an operand of the second
 //   product and a group of the cache's value order.
-// Bound by the vector ALUs next to the matrix cores: the exponentials, and the
-// conversion of codes to bf16 in every wave.
+// Bound by instruction issue: per 64 tokens a wave of 128 channels issues 32
+// matrix instructions of 32 cycles and about 350 others, 32 of them exponentials
+// at a quarter of the rate.  Measured on MI355X: 920 TFLOP/s at 128 channels and
+// 744 at 64 where all tiles are alike (16384 tokens, two workgroups a CU), 815
+// TFLOP/s (211 us) for a causal prompt of 4096 tokens and 40 heads; an 8192-cubed
+// library product reaches 1232.  256 rows a workgroup: 226 us (waves of both
+// halves of a SIMD meet at one barrier); 32-token buffers with three waves a SIMD:
+// 275 us (registers spill, twice the barriers).
 #include "attn_device.h"
 
 namespace biloco {
@@ -80,6 +87,15 @@ struct Loader {
             vscale[i] = a.vs[at];
         }
     }
+    // Part i of 4 N of a chunk that all rows see whole.
+    __device__ __forceinline__ void store_part(TileLds<D> &lds, int buf, int i) const {
+        const int tid = threadIdx.x, j = i >> 2;
+        const u32x4_t w = i & 2 ? v[j] : k[j];
+        const float s = scale_of(i & 2 ? vscale[j] : kscale[j]);
+        uint16_t *to = i & 2 ? &lds.v[buf][16 * (tid + 256 * j) + 8 * (i & 1)]
+                             : &lds.k[buf][(2 * (tid % (D / 16)) + (i & 1)) * TileLds<D>::kRow + 8 * (tid / (D / 16) + 32 * j)];
+        *reinterpret_cast<u32x4_t *>(to) = i & 1 ? widen8(w.z, w.w, s) : widen8(w.x, w.y, s);
+    }
     // In a chunk that not every row of the tile (positions p_min to p_max) sees
     // whole, tokens that no row sees can hold anything: their codes become zero
     // and their scale 1.  NaN codes are taken out of the values and noted apart
@@ -106,15 +122,7 @@ struct Loader {
         }
         if ((tid & 63) == 0) lds.odd[buf][tid >> 6] = odd;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float ks = scale_of(kscale[i]), vs = scale_of(vscale[i]);
-            uint16_t *kt = &lds.k[buf][2 * (tid % (D / 16)) * TileLds<D>::kRow + 8 * (tid / (D / 16) + 32 * i)];
-            *reinterpret_cast<u32x4_t *>(kt) = widen8(k[i].x, k[i].y, ks);
-            *reinterpret_cast<u32x4_t *>(kt + TileLds<D>::kRow) = widen8(k[i].z, k[i].w, ks);
-            u32x4_t *vt = reinterpret_cast<u32x4_t *>(&lds.v[buf][16 * (tid + 256 * i)]);
-            vt[0] = widen8(v[i].x, v[i].y, vs);
-            vt[1] = widen8(v[i].z, v[i].w, vs);
-        }
+        for (int i = 0; i < 4 * N; ++i) store_part(lds, buf, i);
     }
 };
 
@@ -207,6 +215,58 @@ struct Rows32 {
                 o[n] = mfma32(*reinterpret_cast<const u32x4_t *>(v + 16 * c * D + 256 * n), pt[c], o[n]);
     }
 
+    // One tile on, in the order in which it is to be issued: between two matrix
+    // instructions as much of the vector work as fits their time.  Scores s of
+    // tile t in `buf` become weights while the next tile's scores (tile t1 in
+    // `buf1`) are computed; the values of tile t are gathered while the next
+    // scores' maximum is taken and, with `advance`, the next chunk's codes become
+    // bf16 in LDS.  Returns the next scores' maximum.
+    template <bool ADVANCE>
+    __device__ __forceinline__ float tile(TileLds<D> &lds, int buf, int t, int buf1, int t1, f32x16a_t &s, f32x16a_t &next,
+                                          float c2, const Loader<D> &ld) {
+        constexpr int M = D / 16, E = 16 / M;      // matrix instructions of each product; scores between two
+        const int lane = threadIdx.x & 63, r = lane & 31;
+        const int token = 16 * (r >> 4) + 8 * ((r >> 2) & 1) + 4 * ((r >> 3) & 1) + (r & 3);
+        const uint16_t *k = &lds.k[buf1][(lane >> 5) * TileLds<D>::kRow + 8 * (32 * t1 + token)];
+        const uint16_t *v = &lds.v[buf][8 * ((4 * t + (lane >> 5)) * D + (lane & 31))];
+        const auto key = [&](int i) { return *reinterpret_cast<const u32x4_t *>(k + 2 * i * TileLds<D>::kRow); };
+        const auto value = [&](int i) {
+            return *reinterpret_cast<const u32x4_t *>(v + 16 * (i / (D / 32)) * D + 256 * (i % (D / 32)));
+        };
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+        float sum = 0.0f;
+        u32x4_t pt[2], f[M];
+        f[0] = key(0);
+        f[1] = key(1);
+        next = zero16();
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            if (i + 2 < M) f[i + 2] = key(i + 2);
+            next = mfma32(f[i], q[i], next);
+#pragma unroll
+            for (int j = E * i; j < E * i + E; ++j) {
+                s[j] = exp2a(__builtin_fmaf(s[j], c2, -base));
+                sum += s[j];
+                if (j & 1) pt[j >> 3][(j >> 1) & 3] = narrow2a(s[j - 1], s[j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        l += sum;
+        f[0] = value(0);
+        f[1] = value(1);
+        float mx = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            if (i + 2 < M) f[i + 2] = value(i + 2);
+            o[i % (D / 32)] = mfma32(f[i], pt[i / (D / 32)], o[i % (D / 32)]);
+            if constexpr (ADVANCE) ld.store_part(lds, buf ^ 1, i);
+#pragma unroll
+            for (int j = E * i; j < E * i + E; ++j) mx = fmaxf(mx, next[j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        return fmaxf(mx, __shfl_xor(mx, 32, 64)) * c2;
+    }
+
     // NaN values, taken out of the product: a row that sees one gets NaN in its
     // channel, by a product of what is visible with what is NaN (above 0 if any).
     __device__ __forceinline__ void mark_nan(const AttnArgs &a, const TileLds<D> &lds, int buf, int j0) {
@@ -269,47 +329,58 @@ attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
         // Two 32-token tiles a chunk.  The scores of a tile are computed while
         // the one before goes through its exponentials, its maximum while that
         // one's values are gathered.
+        const auto whole = [&](int c) { return all_see(a, p_min, p_max, span.start(c)); };
         Loader<D> ld;
+        // chunk c on its way, and the pages of the one after it
+        const auto request = [&](int c) {
+            ld.load(a, shift, h, span.start(min(c, c1 - 1)));
+            ld.look_up(table, shift, last, span.start(min(c + 1, c1 - 1)));
+        };
         ld.look_up(table, shift, last, span.start(c0));
-        ld.load(a, shift, h, span.start(c0));
-        if (c0 + 1 < c1) ld.look_up(table, shift, last, span.start(c0 + 1));
+        request(c0);
         ld.store(a, lds, 0, span.start(c0), p_min, p_max);
-        if (c0 + 1 < c1) {
-            ld.load(a, shift, h, span.start(c0 + 1));
-            if (c0 + 2 < c1) ld.look_up(table, shift, last, span.start(c0 + 2));
-        }
+        request(c0 + 1);
         __syncthreads();
         f32x16a_t s0 = w.scores(lds, 0, 0), s1;
-        bool whole = all_see(a, w.p_min, w.p_max, span.start(c0));
-        if (!whole) w.hide(a, s0, span.start(c0));
+        if (!whole(c0)) w.hide(a, s0, span.start(c0));
         w.follow(w.top_of(s0, c2));
-        for (int c = c0; c < c1; ++c) {
+        int c = c0;
+        while (true) {
+            // Nothing to hide here and next.  With 64 channels the plain order below
+            // is faster: it leaves registers for three waves a SIMD instead of two
+            // (chunks of 2048 behind up to 10000 tokens: 343 us, 357 this way).
+            while (D == 128 && c + 1 < c1 && whole(c) && whole(c + 1)) {
+                const int buf = (c - c0) & 1;
+                __syncthreads();      // the other buffer has been read
+                if ((threadIdx.x & 63) == 0) lds.odd[buf ^ 1][wave] = 0;
+                w.follow(w.template tile<true>(lds, buf, 0, buf, 1, s0, s1, c2, ld));
+                request(c + 2);
+                __syncthreads();      // the next chunk is in place
+                w.follow(w.template tile<false>(lds, buf, 1, buf ^ 1, 0, s1, s0, c2, ld));
+                ++c;
+            }
             const int buf = (c - c0) & 1, j0 = span.start(c);
-            const bool more = c + 1 < c1;
             u32x4_t pt[2];
-            if (c > c0) __syncthreads();      // the other buffer has been read
-            if (more) {
+            __syncthreads();
+            if (c + 1 < c1) {
                 ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
-                if (c + 2 < c1) {
-                    ld.load(a, shift, h, span.start(c + 2));
-                    if (c + 3 < c1) ld.look_up(table, shift, last, span.start(c + 3));
-                }
+                request(c + 2);
             }
             if (lds.odd[buf][0] | lds.odd[buf][1] | lds.odd[buf][2] | lds.odd[buf][3]) w.mark_nan(a, lds, buf, j0);
             w.weigh(s0, c2, pt);
             s1 = w.scores(lds, buf, 1);
-            if (!whole) w.hide(a, s1, j0 + 32);
+            if (!all_see(a, w.p_min, w.p_max, j0)) w.hide(a, s1, j0 + 32);
             w.gather(lds, buf, 0, pt);
             w.follow(w.top_of(s1, c2));
-            __syncthreads();      // the next chunk is in place
+            __syncthreads();
             w.weigh(s1, c2, pt);
-            if (more) {
+            if (c + 1 < c1) {
                 s0 = w.scores(lds, buf ^ 1, 0);
-                whole = all_see(a, w.p_min, w.p_max, span.start(c + 1));
-                if (!whole) w.hide(a, s0, span.start(c + 1));
+                if (!all_see(a, w.p_min, w.p_max, span.start(c + 1))) w.hide(a, s0, span.start(c + 1));
             }
             w.gather(lds, buf, 1, pt);
-            if (more) w.follow(w.top_of(s0, c2));
+            if (++c == c1) break;
+            w.follow(w.top_of(s0, c2));
         }
     }
 
