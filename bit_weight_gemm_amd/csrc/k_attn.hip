@@ -25,9 +25,8 @@
 // key/value head) and join their sums in LDS at its end; where there
 // are more than 16 rows, groups of them take different rows of the same chunks
 // (the second read of a chunk is a cache hit).  A workgroup takes a whole item,
-// or, where that would leave the chip idle, an equal share of the flat list of
-// all items' chunks; items that several workgroups share are joined by a second
-// launch.
+// or, where that would leave the chip idle, a piece of one; pieces are joined by
+// a second launch.
 #include "attn_device.h"
 
 namespace biloco {
@@ -36,7 +35,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kSplitWaves = 4, kSplitGrid = 512;      // two workgroups a CU
+constexpr int kSplitWaves = 4, kPieces = 512;      // two workgroups a CU
 constexpr int kWholeWaves = 8;
 
 template <int D>
@@ -144,7 +143,7 @@ struct Rows16 {
     }
 
     // Scores to weights, relative to the running maximum.
-    __device__ __forceinline__ void weigh(const AttnArgs &a, f32x4a_t (&sc)[4], bool whole, int j0, u32x4_t (&pt)[2]) {
+    __device__ __forceinline__ void weigh(const AttnArgs &a, f32x4a_t (&sc)[4], bool whole, int j0, u32x4_t (&pt)[2][2]) {
         const int q4 = (threadIdx.x & 63) >> 4;
         const float c2 = a.scale * kLog2e;
         if (!whole) {
@@ -177,12 +176,18 @@ struct Rows16 {
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) o[n] *= alpha;
         }
-        // The weights are rounded to bf16 (at most 2^-8 of each, to either
-        // side); their sum l is kept as it was.
+        // Each weight as the sum of two bf16, its rounding and what that left
+        // (together within 2^-16 of it): the matrix cores have time for a second
+        // product here, and o then carries its own rounding only.
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-            pt[kk] = u32x4_t{narrow2a(sc[2 * kk][0], sc[2 * kk][1]), narrow2a(sc[2 * kk][2], sc[2 * kk][3]),
-                             narrow2a(sc[2 * kk + 1][0], sc[2 * kk + 1][1]), narrow2a(sc[2 * kk + 1][2], sc[2 * kk + 1][3])};
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const uint32_t w = narrow2a(sc[t][i], sc[t][i + 1]);
+                pt[t >> 1][0][2 * (t & 1) + i / 2] = w;
+                pt[t >> 1][1][2 * (t & 1) + i / 2] = narrow2a(sc[t][i] - __uint_as_float(w << 16),
+                                                              sc[t][i + 1] - __uint_as_float(w & 0xFFFF0000u));
+            }
     }
 
     // Where not every row sees the whole chunk: tokens that no row sees can
@@ -226,15 +231,19 @@ struct Rows16 {
         }
     }
 
-    __device__ __forceinline__ void gather(const Stage<D> &st, const u32x4_t (&pt)[2]) {
+    __device__ __forceinline__ void gather(const Stage<D> &st, const u32x4_t (&pt)[2][2]) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) {
                 const u32x4_t w = st.v[kk][n];
                 const float s = scale_of(st.vs[kk]);
-                o[2 * n] = mfma16(widen8(w.x, w.y, s), pt[kk], o[2 * n]);
-                o[2 * n + 1] = mfma16(widen8(w.z, w.w, s), pt[kk], o[2 * n + 1]);
+                const u32x4_t a0 = widen8(w.x, w.y, s), a1 = widen8(w.z, w.w, s);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    o[2 * n] = mfma16(a0, pt[kk][e], o[2 * n]);
+                    o[2 * n + 1] = mfma16(a1, pt[kk][e], o[2 * n + 1]);
+                }
                 if (n & 1) __builtin_amdgcn_sched_barrier(0);
             }
     }
@@ -257,7 +266,7 @@ struct Rows16 {
             const int j0 = s.c.start(c), next = c + step;
             const bool more = next < c1, whole = all_see(a, p_min, p_max, j0);
             f32x4a_t sc[4];
-            u32x4_t pt[2];
+            u32x4_t pt[2][2];
             scores(st, sc);
             if (more) w.load_k(a, st, g, s.c.start(next));
             weigh(a, sc, whole, j0, pt);
@@ -361,65 +370,51 @@ attn_whole_kernel(const AttnArgs a, int which, int row_shift) {
     finish<D, kWholeWaves>(a, s, x, lds, h, rows, 1 << row_shift, nullptr, 0);
 }
 
-// What the workgroup that begins an item leaves for the join: itself, and how
-// many workgroups share the item (1: it is done).
+// What the workgroup of an item's first piece leaves for the join: itself,
+// and how many pieces the item has (1: it is done).
 struct Begun {
     int wg, pieces;
 };
 
-// The split call's workspace: a Begun per item, then two partials a
-// workgroup, slot 0 for a piece that continues an item, slot 1 for one that
-// begins it.
+// The split call's workspace: a Begun per item, then a partial a workgroup.
 __host__ __device__ __forceinline__ int64_t part_floats(int dim, int rows) { return (int64_t)rows * (dim + 2); }
 __host__ __device__ __forceinline__ int64_t begun_slots(int64_t items) { return (items + 1) / 2 * 2; }      // 16 bytes
-__device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, int wg, int slot) {
+__device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, int wg) {
     return reinterpret_cast<float *>(static_cast<Begun *>(a.ws) + begun_slots((int64_t)a.B * a.kv_heads)) +
-           (2 * wg + slot) * part_floats(dim, rows);
+           wg * part_floats(dim, rows);
 }
 
+// A workgroup a piece of an item: equal pieces of as many units (chunks that
+// its waves take side by side) as spread all items over kPieces workgroups.  At
+// most kPieces + items pieces, the grid's size; the workgroups that are left
+// over end at once.
 template <int D>
 __global__ void __launch_bounds__(64 * kSplitWaves, 2)
-attn_split_kernel(const AttnArgs a, int which, int row_shift) {
+attn_split_kernel(const AttnArgs a, int which, int row_shift, int most_rows) {
     __shared__ JoinLds<D, kSplitWaves> lds;
-    const int most = 16 << row_shift, lanes = kSplitWaves >> row_shift;      // chunks taken side by side
-    const int wave = uniform((int)(threadIdx.x >> 6));
-    // Work is a flat list of units of `lanes` chunks, by sequence and head (a
-    // sequence with rows has at least one, to write its rows in).
-    const auto item_units = [&](const Seq &s) { return s.n > 0 ? max((s.c.nc + lanes - 1) / lanes, 1) : 0; };
-    const auto units = [&](int i) { return (int64_t)item_units(seq_of(a, i, which)) * a.kv_heads; };
+    const int lanes = kSplitWaves >> row_shift, wave = uniform((int)(threadIdx.x >> 6));
+    // a sequence with rows has at least one unit, to write its rows in
+    const auto units = [&](const Seq &s) { return s.n > 0 ? max((s.c.nc + lanes - 1) / lanes, 1) : 0; };
     int64_t total = 0, before;
-    for (int i = threadIdx.x & 63; i < a.B; i += 64) total += units(i);
-    total = uniform(wave_sum64(total));
-    const int64_t share = (total + kSplitGrid - 1) / kSplitGrid;
-    int64_t u = (int64_t)blockIdx.x * share;
-    const int64_t end = min(u + share, total);
-    if (u >= end) return;
-    int b = uniform(find_seq(a.B, u, before, units));
-    before = uniform(before);
-    Seq s = seq_uniform(a, b, which);
-    while (true) {
-        const int per = item_units(s);
-        const int h = (int)((u - before) / per), u0 = (int)(u - before - (int64_t)h * per);
-        const int u1 = (int)min((int64_t)per, u0 + (end - u));
-        const int rows = min(s.n * (a.q_heads / a.kv_heads), most);
-        const int mine = 16 * (wave & ((1 << row_shift) - 1));
-        Rows16<D> x(a, s, h, mine, rows);
-        Stage<D> st;
-        const Where w(a, b, h);
-        if (mine < rows) x.run(a, w, s, st, false, u0 * lanes + (wave >> row_shift), min(u1 * lanes, s.c.nc), lanes);
-        float *part = u0 == 0 && u1 == per ? nullptr : part_of(a, D, most, blockIdx.x, u0 == 0);
-        if (u0 == 0 && threadIdx.x == 0)
-            static_cast<Begun *>(a.ws)[b * a.kv_heads + h] =
-                Begun{(int)blockIdx.x, (int)((u + per - 1) / share) - (int)blockIdx.x + 1};
-        finish<D, kSplitWaves>(a, s, x, lds, h, rows, 1 << row_shift, part, most);
-        u += u1 - u0;
-        if (u >= end) return;
-        __syncthreads();      // lds is free again
-        while (u >= before + (int64_t)item_units(s) * a.kv_heads) {      // ends: u < total
-            before += (int64_t)item_units(s) * a.kv_heads;
-            s = seq_uniform(a, ++b, which);
-        }
-    }
+    for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(a, i, which)) * a.kv_heads;
+    const int64_t each = max((uniform(wave_sum64(total)) + kPieces - 1) / kPieces, (int64_t)1);
+    const int size = (int)min(each, (int64_t)INT32_MAX);
+    const auto pieces = [&](const Seq &s) { return (int)(((int64_t)units(s) + size - 1) / size); };
+    const int b = uniform(find_seq(a.B, blockIdx.x, before,
+                                   [&](int i) { return (int64_t)pieces(seq_of(a, i, which)) * a.kv_heads; }));
+    if (b < 0) return;
+    const Seq s = seq_uniform(a, b, which);
+    const int n = pieces(s), at = (int)(blockIdx.x - uniform(before)), h = at / n, u0 = (at - h * n) * size;
+    const int rows = min(s.n * (a.q_heads / a.kv_heads), most_rows);
+    const int mine = 16 * (wave & ((1 << row_shift) - 1));
+    const Where w(a, b, h);
+    Rows16<D> x(a, s, h, mine, rows);
+    Stage<D> st;
+    if (mine < rows)
+        x.run(a, w, s, st, false, u0 * lanes + (wave >> row_shift), min((u0 + size) * lanes, s.c.nc), lanes);
+    if (u0 == 0 && threadIdx.x == 0) static_cast<Begun *>(a.ws)[b * a.kv_heads + h] = Begun{(int)blockIdx.x, n};
+    finish<D, kSplitWaves>(a, s, x, lds, h, rows, 1 << row_shift,
+                           n == 1 ? nullptr : part_of(a, D, most_rows, blockIdx.x), most_rows);
 }
 
 // Joins the pieces of the rows of items that several workgroups shared: WAYS
@@ -427,15 +422,15 @@ attn_split_kernel(const AttnArgs a, int which, int row_shift) {
 // workgroup.
 template <int D, int WAYS>
 __global__ void __launch_bounds__(256)
-attn_join_kernel(const AttnArgs a, int which, int row_shift, int items) {
+attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
     __shared__ float lo[WAYS][D];
     __shared__ float ll[WAYS][2];
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int item = (int)(blockIdx.x % items), row = (int)(blockIdx.x / items) * (4 / WAYS) + wave / WAYS;
-    const int b = item / a.kv_heads, h = item % a.kv_heads, G = a.q_heads / a.kv_heads, most = 16 << row_shift;
+    const int b = item / a.kv_heads, h = item % a.kv_heads, G = a.q_heads / a.kv_heads;
     const Begun x = static_cast<const Begun *>(a.ws)[item];      // written if the sequence has rows
     const Seq s = seq_of(a, b, which);
-    if (row >= s.n * G || x.pieces < 2) return;      // with four ways: the whole workgroup
+    if (row >= min(s.n * G, most_rows) || x.pieces < 2) return;      // with four ways: the whole workgroup
     const int wg = uniform(x.wg), pieces = uniform(x.pieces);
     float m = -__builtin_inff(), l = 0.0f, acc[D / 64];
 #pragma unroll
@@ -446,7 +441,7 @@ attn_join_kernel(const AttnArgs a, int which, int row_shift, int items) {
         const int i = i0 + WAYS * lane, n = min((pieces - i0 + WAYS - 1) / WAYS, 64);
         float pm = -__builtin_inff(), pl = 0.0f;
         if (i < pieces) {
-            const float *ml = part_of(a, D, most, wg + i, i == 0) + most * D + 2 * row;
+            const float *ml = part_of(a, D, most_rows, wg + i) + most_rows * D + 2 * row;
             pm = ml[0];
             pl = ml[1];
         }
@@ -463,7 +458,7 @@ attn_join_kernel(const AttnArgs a, int which, int row_shift, int items) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {      // past the last one: the last one, not added
                 const int at = i0 + WAYS * min(k + e, n - 1);
-                const float *part = part_of(a, D, most, wg + at, at == 0) + row * D + (D / 64) * lane;
+                const float *part = part_of(a, D, most_rows, wg + at) + row * D + (D / 64) * lane;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) v[e][j] = part[j];
                 g[e] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), min(k + e, n - 1)));
@@ -517,7 +512,7 @@ attn_join_kernel(const AttnArgs a, int which, int row_shift, int items) {
 // whole, 21 us split.
 bool whole_items(int64_t items, int64_t chunks, int row_shift) {
     const int64_t alone = ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves;
-    const int64_t shared = ((items * chunks) << row_shift) / (kSplitGrid * kSplitWaves) + 4;
+    const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + 4;
     return alone <= (shared < 16 ? shared : 16);
 }
 
@@ -544,7 +539,7 @@ Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int ma
     const int64_t chunks = (max_kv + kChunk - 1) / kChunk;
     p.whole = whole_items(p.items, chunks, p.row_shift);
     p.rows_bytes = p.rows && !p.whole      // whatever the window
-                       ? begun_slots(p.items) * sizeof(Begun) + kSplitGrid * 2 * part_floats(dim, 16 << p.row_shift) * sizeof(float)
+                       ? begun_slots(p.items) * sizeof(Begun) + (p.items + kPieces) * part_floats(dim, p.most_rows) * sizeof(float)
                        : 0;
     if (window > 0) {
         const int64_t seen = ((int64_t)window + longest + 2 * kChunk) / kChunk + ((int64_t)sinks + kChunk - 1) / kChunk;
@@ -563,7 +558,9 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
                            p.row_shift);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((attn_split_kernel<D>), dim3(kSplitGrid), dim3(64 * kSplitWaves), 0, stream, a, which, p.row_shift);
+    if (p.items + kPieces > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((attn_split_kernel<D>), dim3((unsigned)(p.items + kPieces)), dim3(64 * kSplitWaves), 0, stream, a,
+                       which, p.row_shift, p.most_rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // few rows: four waves a row; many: a wave
@@ -571,10 +568,10 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
     const int64_t grid = p.items * ((p.most_rows + 4 / ways - 1) / (4 / ways));
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     if (ways == 4)
-        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.row_shift,
+        hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.most_rows,
                            (int)p.items);
     else
-        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.row_shift,
+        hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.most_rows,
                            (int)p.items);
     return hipGetLastError();
 }
