@@ -113,10 +113,13 @@ __device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, 
 __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int which) {
     return seq_from(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], which);
 }
-// The same for a sequence that the whole workgroup works on: held in scalar
-// registers.
+// The same for a sequence that the whole workgroup works on, through scalar
+// loads into scalar registers (b is uniform).
+__device__ __forceinline__ int scalar_load(const int *p) {
+    return *(const __attribute__((address_space(4))) int *)(uintptr_t)p;
+}
 __device__ __forceinline__ Seq seq_uniform(const AttnArgs &a, int b, int which) {
-    return seq_from(a, uniform(a.q_start[b]), uniform(a.q_start[b + 1]), uniform(a.kv_len[b]), which);
+    return seq_from(a, scalar_load(a.q_start + b), scalar_load(a.q_start + b + 1), scalar_load(a.kv_len + b), which);
 }
 
 __device__ __forceinline__ int64_t wave_sum64(int64_t v) {

@@ -47,9 +47,13 @@ biloco_status check_cache(int32_t num_pages, int32_t kv_heads, int32_t page_size
     return BILOCO_OK;
 }
 
-biloco_status check_batch(int32_t B, int32_t T, int32_t max_q_len, int32_t max_pages) {
+// Tokens of a sequence that its table row can name: positions and what is
+// added to them in the kernels stay within 32 bits.
+constexpr int64_t kMostTokens = (int64_t)1 << 30;
+
+biloco_status check_batch(int32_t B, int32_t T, int32_t max_q_len, int32_t max_pages, int32_t page_size) {
     if (B < 0 || T < 0 || max_q_len < 1 || max_pages < 1) return BILOCO_ERR_INVALID_VALUE;
-    if (B > 65535) return BILOCO_ERR_UNSUPPORTED;
+    if (B > 65535 || (int64_t)max_pages * page_size > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
     return BILOCO_OK;
 }
 
@@ -69,7 +73,7 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
                                int32_t max_q_len, uint16_t *q_out, int64_t q_out_stride,
                                hipStream_t stream) {
     biloco_status st = check_cache(num_pages, kv_heads, page_size, head_dim);
-    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, max_pages);
+    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, max_pages, page_size);
     if (st != BILOCO_OK) return st;
     if (q_heads < 0 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 != 0)
         return BILOCO_ERR_INVALID_VALUE;
@@ -135,8 +139,9 @@ biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads,
                                           int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
                                           size_t *bytes) {
     if (!bytes || max_kv_len < 0 || q_heads < 1) return BILOCO_ERR_INVALID_VALUE;
+    if (max_kv_len > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
     biloco_status st = check_cache(1, kv_heads, 16, head_dim);
-    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, 1);
+    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, 1, 1);
     if (st != BILOCO_OK) return st;
     if (q_heads % kv_heads != 0) return BILOCO_ERR_INVALID_VALUE;
     if (q_heads > 4096 || (int64_t)T * q_heads > INT32_MAX) return BILOCO_ERR_UNSUPPORTED;
@@ -155,13 +160,14 @@ biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
                                 void *workspace, size_t workspace_bytes, hipStream_t stream) {
     size_t need = 0;
     biloco_status st = check_cache(num_pages, kv_heads, page_size, head_dim);
-    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, max_pages);
+    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, max_pages, page_size);
     if (st == BILOCO_OK)
         st = biloco_attn_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len,
                                          &need);
     if (st != BILOCO_OK) return st;
     if (!(scale > 0.0f) || !isfinite(scale) || window < 0 || sinks < 0)
         return BILOCO_ERR_INVALID_VALUE;
+    if (window > kMostTokens || sinks > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
     if (!k_codes || !v_codes || !k_scales || !v_scales || !q || !q_start || !kv_len ||
         !block_table || !o || (need > 0 && !workspace))
         return BILOCO_ERR_INVALID_VALUE;

@@ -352,7 +352,6 @@ attn_whole_kernel(const AttnArgs a, int which, int row_shift) {
     const int h = (int)(blockIdx.x % a.kv_heads), b = (int)(blockIdx.x / a.kv_heads);
     const int wave = uniform((int)(threadIdx.x >> 6)), c = wave >> row_shift;
     const Where w(a, b, h);
-    const int q0 = a.q_start[b], q1 = a.q_start[b + 1], len = a.kv_len[b];
     Stage<D> st;
     const bool early = a.window == 0;
     if (early) {
@@ -361,7 +360,7 @@ attn_whole_kernel(const AttnArgs a, int which, int row_shift) {
         w.load_k(a, st, g, c * kChunk);
         w.load_v(a, st, g, c * kChunk);
     }
-    const Seq s = seq_from(a, uniform(q0), uniform(q1), uniform(len), which);
+    const Seq s = seq_uniform(a, b, which);
     if (s.n == 0) return;
     const int rows = min(s.n * (a.q_heads / a.kv_heads), 16 << row_shift);
     const int mine = 16 * (wave & ((1 << row_shift) - 1));
@@ -398,7 +397,7 @@ attn_split_kernel(const AttnArgs a, int which, int row_shift, int most_rows) {
     int64_t total = 0, before;
     for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(a, i, which)) * a.kv_heads;
     const int64_t each = max((uniform(wave_sum64(total)) + kPieces - 1) / kPieces, (int64_t)1);
-    const int size = (int)min(each, (int64_t)INT32_MAX);
+    const int size = (int)min(each, (int64_t)1 << 24);      // no item has more units
     const auto pieces = [&](const Seq &s) { return (int)(((int64_t)units(s) + size - 1) / size); };
     const int b = uniform(find_seq(a.B, blockIdx.x, before,
                                    [&](int i) { return (int64_t)pieces(seq_of(a, i, which)) * a.kv_heads; }));
@@ -435,10 +434,21 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
     float m = -__builtin_inff(), l = 0.0f, acc[D / 64];
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) acc[j] = 0.0f;
+    // o of pieces k .. k + 7 from i0 on (past the last one: the last one)
+    const auto fetch = [&](float (&v)[8][D / 64], int i0, int k, int n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float *part = part_of(a, D, most_rows, wg + i0 + WAYS * min(k + e, n - 1)) + row * D + (D / 64) * lane;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) v[e][j] = part[j];
+        }
+    };
     for (int i0 = wave % WAYS; i0 < pieces; i0 += 64 * WAYS) {
-        // up to 64 pieces: a lane each their maximum, sum and weight, then
-        // their o, whose loads wait for nothing
+        // up to 64 pieces: a lane each their maximum, sum and weight; the first
+        // eight pieces' o is on its way meanwhile
         const int i = i0 + WAYS * lane, n = min((pieces - i0 + WAYS - 1) / WAYS, 64);
+        float v[8][D / 64];
+        fetch(v, i0, 0, n);
         float pm = -__builtin_inff(), pl = 0.0f;
         if (i < pieces) {
             const float *ml = part_of(a, D, most_rows, wg + i) + most_rows * D + 2 * row;
@@ -454,19 +464,13 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) acc[j] *= f0;
         for (int k = 0; k < n; k += 8) {
-            float v[8][D / 64], g[8];
+            if (k > 0) fetch(v, i0, k, n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {      // past the last one: the last one, not added
-                const int at = i0 + WAYS * min(k + e, n - 1);
-                const float *part = part_of(a, D, most_rows, wg + at) + row * D + (D / 64) * lane;
+            for (int e = 0; e < 8; ++e) {
+                const float g = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), min(k + e, n - 1)));
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j) v[e][j] = part[j];
-                g[e] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), min(k + e, n - 1)));
+                for (int j = 0; j < D / 64; ++j) acc[j] = k + e < n ? __builtin_fmaf(g, v[e][j], acc[j]) : acc[j];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j) acc[j] = k + e < n ? __builtin_fmaf(g[e], v[e][j], acc[j]) : acc[j];
         }
     }
     if constexpr (WAYS > 1) {

@@ -405,9 +405,10 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
  *   lse = log(sum over visible j of exp(s_j))
  * A row that sees nothing (more new tokens than cached ones) gives o = 0 and
  * lse = -inf.  Tokens that a row does not see never affect it, whatever their
- * codes hold (NaN included).  Sums, maxima and o are kept in fp32; the weights
- * are rounded to bf16 for the product with v, whose codes and scales are exact
- * in bf16.
+ * codes hold (NaN included).  Codes and scales are exact in bf16; sums, maxima
+ * and o are kept in fp32.  For the product with v a weight is the sum of two
+ * bf16 (within 2^-16 of it) where a sequence has at most 64 rows (new tokens
+ * times q_heads / kv_heads), and rounded to bf16 (2^-8) where it has more.
  *   q [T][q_heads][head_dim] bf16 and o likewise, token strides in elements
  *     (multiples of 8); o must not overlap an input
  *   lse fp32 [T][q_heads] or NULL
@@ -415,8 +416,8 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
  *   max_kv_len bounds kv_len on the host; it and max_q_len shape the launch.
  *   workspace: >= biloco_attn_workspace_bytes(...) bytes, no fill needed; not
  *     shared by calls that can run at the same time.
- * q_heads must be a multiple of kv_heads.  T = 0 or B = 0 does nothing.
- * One to three launches. */
+ * q_heads must be a multiple of kv_heads; T * q_heads < 2^31; at most 2^30
+ * tokens a sequence.  T = 0 or B = 0 does nothing.  One to four launches. */
 biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
                                 const uint8_t *k_scales, const uint8_t *v_scales,
                                 int32_t num_pages, int32_t kv_heads, int32_t page_size,

@@ -199,3 +199,21 @@ def test_repeats_and_replays_are_the_same(new, kv):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 3]])
+def test_offsets_beyond_32_bits(new):
+    """The same pages at the end of a cache of more than 2^32 bytes."""
+    c = Case(new, [300, 90], 8, 8, 128, 128, seed=21, tail=False)
+    d = c.gpu()
+    o0, lse0 = c.run(d)
+    pages = 33000      # of 128 KiB each
+    big = B.biloco_kv_cache(pages, 8, 128, 128)
+    assert big[0].numel() > 1 << 32
+    n = d["cache"][0].shape[0]
+    for t, u in zip(big, d["cache"]):
+        t[-n:].copy_(u)
+    d["cache"] = big
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
+    o, lse = c.run(d)
+    assert torch.equal(o, o0) and torch.equal(lse, lse0)

@@ -236,3 +236,24 @@ def test_another_stream_and_replay():
         assert torch.equal(out, first)
         for got, ref in zip(d["cache"], want):
             np.testing.assert_array_equal(got.cpu().numpy() & 127, ref & 127)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [150, 3]])
+def test_offsets_beyond_32_bits(new):
+    """The same pages at the end of a cache of more than 2^32 bytes."""
+    b = Batch([100, 7], new, 8, 8, 128, 128, seed=21)
+    d = b.gpu()
+    pages = 33000      # of 128 KiB each
+    big = B.biloco_kv_cache(pages, 8, 128, 128)
+    assert big[0].numel() > 1 << 32
+    n = d["cache"][0].shape[0]
+    for t, u in zip(big, d["cache"]):
+        t[-n:].copy_(u)
+    q0 = b.run(d)
+    small = d["cache"]
+    d["cache"] = big
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
+    q = b.run(d)
+    assert torch.equal(q, q0)
+    for t, u in zip(big, small):
+        assert torch.equal(t[-n:], u)

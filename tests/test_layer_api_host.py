@@ -51,7 +51,7 @@ CACHE_BAD = [(dict(pages=0), BAD), (dict(hk=0), BAD), (dict(page=0), BAD), (dict
              (dict(kc=None), BAD), (dict(vc=None), BAD), (dict(ks=None), BAD), (dict(vs=None), BAD),
              (dict(kc=A + 8), BAD), (dict(vs=4 * A + 1), BAD), (dict(qs=None), BAD), (dict(kvl=None), BAD),
              (dict(bt=None), BAD), (dict(bt=12 * A + 4), BAD), (dict(mp=0), BAD), (dict(B=-1), BAD), (dict(T=-1), BAD),
-             (dict(mq=0), BAD), (dict(B=70000), UNS)]
+             (dict(mq=0), BAD), (dict(B=70000), UNS), (dict(mp=1 << 26), UNS)]
 
 
 @pytest.mark.parametrize("kw,status", CACHE_BAD)
@@ -76,7 +76,8 @@ def test_append_refuses(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(hq=0), BAD), (dict(hq=60), BAD), (dict(hq=8192, sq=1 << 20, so=1 << 20), UNS), (dict(mkv=-1), BAD),
     (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD),
-    (dict(win=-1), BAD), (dict(sinks=-1), BAD), (dict(q=None), BAD), (dict(o=None), BAD), (dict(o=13 * A + 2), BAD),
+    (dict(win=-1), BAD), (dict(sinks=-1), BAD), (dict(win=(1 << 30) + 1), UNS), (dict(mkv=(1 << 30) + 1), UNS),
+    (dict(sinks=(1 << 30) + 1), UNS), (dict(T=1 << 26), UNS), (dict(q=None), BAD), (dict(o=None), BAD), (dict(o=13 * A + 2), BAD),
     (dict(lse=14 * A + 4), BAD), (dict(sq=8190), BAD), (dict(so=8000), BAD), (dict(T=2, o=5 * A), BAD),
     (dict(T=2, o=A + 16), BAD), (dict(T=2, lse=5 * A + 32), BAD)])
 def test_attend_refuses(kw, status):
