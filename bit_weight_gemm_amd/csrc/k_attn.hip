@@ -146,7 +146,7 @@ struct Rows16 {
     __device__ __forceinline__ void weigh(const AttnArgs &a, f32x4a_t (&sc)[4], bool whole, int j0, u32x4_t (&pt)[2][2]) {
         const int q4 = (threadIdx.x & 63) >> 4;
         const float c2 = a.scale * kLog2e;
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
             const int lo = low_of(a, p);
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -196,20 +196,24 @@ struct Rows16 {
     // channel, by a product of what is visible with what is NaN (above 0 if any).
     __device__ __forceinline__ void clean(const AttnArgs &a, Stage<D> &st, int j0) {
         const int q4 = (threadIdx.x & 63) >> 4;
-        uint32_t any = 0;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             const uint32_t bits = any_sees8(a, p_min, p_max, j0 + 32 * kk + 8 * q4);
             const uint32_t m0 = spread4(bits), m1 = spread4(bits >> 4);
             if (bits == 0) st.vs[kk] = 127;
 #pragma unroll
+            for (int n = 0; n < D / 32; ++n) st.v[kk][n] &= u32x4_t{m0, m1, m0, m1};
+        }
+        if (p_min == p_max) return;      // rows of one token see the same
+        uint32_t any = 0;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
             for (int n = 0; n < D / 32; ++n) {
-                st.v[kk][n] &= u32x4_t{m0, m1, m0, m1};
                 const u32x4_t t = nan_bytes(st.v[kk][n]);
                 any |= t.x | t.y | t.z | t.w;
             }
-        }
-        if (__ballot(any != 0) == 0) return;
+        if (__builtin_expect(__ballot(any != 0) == 0, 1)) return;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             const uint32_t bits = sees8(a, p, j0 + 32 * kk + 8 * q4);
@@ -270,7 +274,7 @@ struct Rows16 {
             scores(st, sc);
             if (more) w.load_k(a, st, g, s.c.start(next));
             weigh(a, sc, whole, j0, pt);
-            if (!whole) clean(a, st, j0);
+            if (__builtin_expect(!whole, 0)) clean(a, st, j0);
             gather(st, pt);
             if (!more) return;
             w.load_v(a, st, g, s.c.start(next));
