@@ -42,7 +42,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kSplitWaves = 4, kPieces = 512;      // two workgroups a CU
+constexpr int kSplitLog = 2, kSplitWaves = 1 << kSplitLog, kPieces = 512;      // two workgroups a CU
 constexpr int kWholeWaves = 8;
 
 template <int D>
@@ -354,14 +354,24 @@ __device__ __forceinline__ void finish(const AttnArgs &a, const Seq &s, const Ro
     }
 }
 
+// Rows of a sequence, and 1 << row_shift groups of waves that take 16 of them
+// each: by the sequence's own rows, not the batch's most, so that waves which
+// would have no rows take chunks instead.
+__device__ __forceinline__ int rows_of(const AttnArgs &a, const Seq &s, int most_rows) {
+    return min(s.n * (a.q_heads / a.kv_heads), most_rows);
+}
+__host__ __device__ __forceinline__ int row_shift_of(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : 2; }
+
 // A workgroup an item.  The first chunk's pages, keys and values are asked
-// for before the sequence's length is known where it is chunk 0 on (no window).
+// for before the sequence's length is known where it is chunk 0 on (no window),
+// in the order of the batch's most rows.
 template <int D>
 __global__ void __launch_bounds__(64 * kWholeWaves, 2)
-attn_whole_kernel(const AttnArgs a, int which, int row_shift) {
+attn_whole_kernel(const AttnArgs a, int which, int most_rows) {
     __shared__ JoinLds<D, kWholeWaves> lds;
     const int h = (int)(blockIdx.x % a.kv_heads), b = (int)(blockIdx.x / a.kv_heads);
-    const int wave = uniform((int)(threadIdx.x >> 6)), c = wave >> row_shift;
+    const int wave = uniform((int)(threadIdx.x >> 6));
+    const int most_shift = row_shift_of(most_rows), c = wave >> most_shift;
     const Where w(a, b, h);
     Stage<D> st;
     const bool early = a.window == 0;
@@ -373,10 +383,11 @@ attn_whole_kernel(const AttnArgs a, int which, int row_shift) {
     }
     const Seq s = seq_uniform(a, b, which);
     if (s.n == 0) return;
-    const int rows = min(s.n * (a.q_heads / a.kv_heads), 16 << row_shift);
+    const int rows = rows_of(a, s, most_rows), row_shift = row_shift_of(rows);
     const int mine = 16 * (wave & ((1 << row_shift) - 1));
     Rows16<D> x(a, s, h, mine, rows);
-    if (mine < rows) x.run(a, w, s, st, early, c, s.c.nc, kWholeWaves >> row_shift);
+    if (mine < rows)
+        x.run(a, w, s, st, early && row_shift == most_shift, wave >> row_shift, s.c.nc, kWholeWaves >> row_shift);
     finish<D, kWholeWaves>(a, s, x, lds, h, rows, 1 << row_shift, nullptr, 0);
 }
 
@@ -400,11 +411,15 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, 
 // over end at once.
 template <int D>
 __global__ void __launch_bounds__(64 * kSplitWaves, 2)
-attn_split_kernel(const AttnArgs a, int which, int row_shift, int most_rows) {
+attn_split_kernel(const AttnArgs a, int which, int most_rows) {
     __shared__ JoinLds<D, kSplitWaves> lds;
-    const int lanes = kSplitWaves >> row_shift, wave = uniform((int)(threadIdx.x >> 6));
+    const int wave = uniform((int)(threadIdx.x >> 6));
+    const auto shift_of = [&](const Seq &s) { return row_shift_of(rows_of(a, s, most_rows)); };
     // a sequence with rows has at least one unit, to write its rows in
-    const auto units = [&](const Seq &s) { return s.n > 0 ? max((s.c.nc + lanes - 1) / lanes, 1) : 0; };
+    const auto units = [&](const Seq &s) {
+        const int by = kSplitLog - shift_of(s);      // chunks side by side, as a power of two
+        return s.n > 0 ? max((s.c.nc + (1 << by) - 1) >> by, 1) : 0;
+    };
     int64_t total = 0, before;
     for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(a, i, which)) * a.kv_heads;
     const int64_t each = max((uniform(wave_sum64(total)) + kPieces - 1) / kPieces, (int64_t)1);
@@ -415,7 +430,7 @@ attn_split_kernel(const AttnArgs a, int which, int row_shift, int most_rows) {
     if (b < 0) return;
     const Seq s = seq_uniform(a, b, which);
     const int n = pieces(s), at = (int)(blockIdx.x - uniform(before)), h = at / n, u0 = (at - h * n) * size;
-    const int rows = min(s.n * (a.q_heads / a.kv_heads), most_rows);
+    const int rows = rows_of(a, s, most_rows), row_shift = shift_of(s), lanes = kSplitWaves >> row_shift;
     const int mine = 16 * (wave & ((1 << row_shift) - 1));
     const Where w(a, b, h);
     Rows16<D> x(a, s, h, mine, rows);
@@ -548,7 +563,7 @@ Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int ma
     p.tiles = longest * G > kMostRows;
     p.rows = !p.tiles || (T - (B - 1) * longest) * G <= kMostRows;
     const int64_t rows = longest * G < kMostRows ? longest * G : kMostRows;
-    p.row_shift = rows <= 16 ? 0 : rows <= 32 ? 1 : 2;
+    p.row_shift = row_shift_of((int)rows);
     p.most_rows = (int)rows;
     p.items = (int64_t)B * kv_heads;      // at most 2^26
     const int64_t chunks = (max_kv + kChunk - 1) / kChunk;
@@ -570,12 +585,12 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
     if (p.whole) {
         if (p.items > 0x7FFFFFFF) return hipErrorInvalidValue;
         hipLaunchKernelGGL((attn_whole_kernel<D>), dim3((unsigned)p.items), dim3(64 * kWholeWaves), 0, stream, a, which,
-                           p.row_shift);
+                           p.most_rows);
         return hipGetLastError();
     }
     if (p.items + kPieces > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((attn_split_kernel<D>), dim3((unsigned)(p.items + kPieces)), dim3(64 * kSplitWaves), 0, stream, a,
-                       which, p.row_shift, p.most_rows);
+                       which, p.most_rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // few rows: four waves a row; many: a wave

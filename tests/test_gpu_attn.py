@@ -217,3 +217,12 @@ def test_offsets_beyond_32_bits(new):
     d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
     o, lse = c.run(d)
     assert torch.equal(o, o0) and torch.equal(lse, lse0)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (200, 5)])
+@pytest.mark.parametrize("max_kv", [None, 100000])      # a workgroup an item, and pieces
+def test_sequences_of_different_row_counts(dim, window, sinks, max_kv):
+    # 8 to 64 rows of a key/value head: one, two and four groups of waves in one launch
+    Case([1, 3, 8, 5, 2, 0, 4, 6], [900, 25, 777, 600, 64, 300, 1, 129], 16, 2, dim, 32, seed=dim + window).check(
+        window, sinks, max_kv=max_kv)
