@@ -42,7 +42,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kSplitLog = 2, kSplitWaves = 1 << kSplitLog, kPieces = 512;      // two workgroups a CU
+constexpr int kSplitLog = 2, kSplitWaves = 1 << kSplitLog, kPieces = 512, kSizes = 4;      // two workgroups a CU
 constexpr int kWholeWaves = 8;
 
 template <int D>
@@ -423,13 +423,28 @@ attn_split_kernel(const AttnArgs a, int which, int most_rows) {
     int64_t total = 0, before;
     for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(a, i, which)) * a.kv_heads;
     const int64_t each = max((uniform(wave_sum64(total)) + kPieces - 1) / kPieces, (int64_t)1);
-    const int size = (int)min(each, (int64_t)1 << 24);      // no item has more units
-    const auto pieces = [&](const Seq &s) { return (int)(((int64_t)units(s) + size - 1) / size); };
+    const int even = (int)min(each, (int64_t)1 << 24);      // no item has more units
+    // Each item's last piece can be short, and a workgroup above kPieces waits for
+    // another to end.  So sizes up to twice the even share: the smallest with no
+    // more pieces than that.
+    float count[kSizes] = {};      // compared with kPieces only, so exact where it matters
+    for (int i = threadIdx.x & 63; i < a.B; i += 64) {
+        const uint32_t u = (uint32_t)units(seq_of(a, i, which));
+#pragma unroll
+        for (int k = 0; k < kSizes; ++k) count[k] += (float)((u + even + k - 1) / (uint32_t)(even + k));
+    }
+    int more = 0;
+#pragma unroll
+    for (int k = kSizes - 1; k >= 0; --k)
+        if (wave_sum_dpp(count[k]) * (float)a.kv_heads <= (float)kPieces) more = k;
+    const int size = even + (uniform(more) <= even ? uniform(more) : 0);
+    const auto pieces = [&](const Seq &s) { return (int)(((uint32_t)units(s) + size - 1) / (uint32_t)size); };
     const int b = uniform(find_seq(a.B, blockIdx.x, before,
                                    [&](int i) { return (int64_t)pieces(seq_of(a, i, which)) * a.kv_heads; }));
     if (b < 0) return;
     const Seq s = seq_uniform(a, b, which);
-    const int n = pieces(s), at = (int)(blockIdx.x - uniform(before)), h = at / n, u0 = (at - h * n) * size;
+    const int n = uniform(pieces(s)), at = (int)(blockIdx.x - uniform(before));
+    const int h = uniform(at / n), u0 = uniform((at - h * n) * size);
     const int rows = rows_of(a, s, most_rows), row_shift = shift_of(s), lanes = kSplitWaves >> row_shift;
     const int mine = 16 * (wave & ((1 << row_shift) - 1));
     const Where w(a, b, h);
