@@ -406,9 +406,9 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, 
 }
 
 // A workgroup a piece of an item: equal pieces of as many units (chunks that
-// its waves take side by side) as spread all items over kPieces workgroups.  At
-// most kPieces + items pieces, the grid's size; the workgroups that are left
-// over end at once.
+// its waves take side by side) as spread all items over kPieces workgroups, or a
+// few more.  At most kPieces + items pieces, the grid's size; the workgroups that
+// are left over end at once.
 template <int D>
 __global__ void __launch_bounds__(64 * kSplitWaves, 2)
 attn_split_kernel(const AttnArgs a, int which, int most_rows) {
@@ -426,7 +426,8 @@ attn_split_kernel(const AttnArgs a, int which, int most_rows) {
     const int even = (int)min(each, (int64_t)1 << 24);      // no item has more units
     // Each item's last piece can be short, and a workgroup above kPieces waits for
     // another to end.  So sizes up to twice the even share: the smallest with no
-    // more pieces than that.
+    // more pieces than that (944 units: 528 pieces of two or 384 of three, 27.9 and
+    // 24.3 us with the join).
     float count[kSizes] = {};      // compared with kPieces only, so exact where it matters
     for (int i = threadIdx.x & 63; i < a.B; i += 64) {
         const uint32_t u = (uint32_t)units(seq_of(a, i, which));
@@ -552,9 +553,9 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
 // an even share of all chunks over the chip's 2048 waves and, for the list and
 // the join, about as long as four more chunks.  Never more than 16 in turn: the
 // host knows the longest sequence only, and the others may be short.
-// Measured (128 channels): 32 sequences of 1 to 8192 tokens, 40 heads: 93 us
-// whole, 108 + 8 us split; 16 of 1 to 4100 tokens, 40 rows, 8 heads: 74 us
-// whole, 21 us split.
+// Measured (128 channels), joins included: 32 sequences of 1 to 8192 tokens, 40
+// heads: 93 us whole, 106 split; one of 613 tokens: 8.7 and 11.3; 16 of 1 to 4100
+// tokens, up to 40 rows, 8 heads: 81 and 24.
 bool whole_items(int64_t items, int64_t chunks, int row_shift) {
     const int64_t alone = ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves;
     const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + 4;

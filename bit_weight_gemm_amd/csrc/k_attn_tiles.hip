@@ -15,8 +15,8 @@
 // Bound by instruction issue: per 64 tokens a wave of 128 channels issues 32
 // matrix instructions of 32 cycles and about 350 others, 32 of them exponentials
 // at a quarter of the rate.  Measured on MI355X: 920 TFLOP/s at 128 channels and
-// 744 at 64 where all tiles are alike (16384 tokens, two workgroups a CU), 811
-// TFLOP/s (212 us) for a causal prompt of 4096 tokens and 40 heads; an 8192-cubed
+// 744 at 64 where all tiles are alike (16384 tokens, two workgroups a CU), 782 to
+// 826 TFLOP/s (220 to 208 us) for a causal prompt of 4096 tokens and 40 heads; an 8192-cubed
 // library product reaches 1232.  256 rows a workgroup: 226 us (waves of both
 // halves of a SIMD meet at one barrier); 32-token buffers with three waves a SIMD:
 // 275 us (registers spill, twice the barriers).
