@@ -467,19 +467,21 @@ hipError_t launch(const AttnArgs &a, int which, hipStream_t stream) {
 
 }  // namespace
 
-// Tiles: every sequence ends at most one of them early.  The token axis is
-// split where the tiles alone leave CUs idle, into pieces of at least four
-// chunks.
+// Tiles: the kernel's sequences have more than kMostRows rows each, so there
+// are at most rows / (kMostRows + 1) of them, and each ends at most one tile early.
+// The token axis is split where the tiles alone leave CUs idle, into pieces of at
+// least four chunks.
 TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int max_kv) {
     TilesPlan p;
     const int64_t rows = (int64_t)T * (q_heads / kv_heads);
-    p.tiles = (int)(rows / kTileRows + B);
-    const int64_t items = (rows + kTileRows - 1) / kTileRows * kv_heads;
+    const int64_t most = rows / (kMostRows + 1), seqs = most < B ? most : B;
+    p.tiles = (int)((rows + (kTileRows - 1) * seqs) / kTileRows);
+    const int64_t items = (int64_t)p.tiles * kv_heads;
     const int pieces = (max_kv + 4 * kChunk - 1) / (4 * kChunk);
-    int64_t splits = (kWantItems + items - 1) / items;
+    int64_t splits = items > 0 ? (kWantItems + items - 1) / items : 1;
     if (splits > pieces) splits = pieces;
     p.splits = splits < 1 ? 1 : (int)splits;
-    p.ws_bytes = p.splits == 1 ? 0 : (size_t)p.tiles * kv_heads * p.splits * kTileRows * (dim + 2) * sizeof(float);
+    p.ws_bytes = p.splits == 1 ? 0 : (size_t)items * p.splits * kTileRows * (dim + 2) * sizeof(float);
     return p;
 }
 
