@@ -161,6 +161,7 @@ struct TilesPlan {
     size_t ws_bytes;
 };
 TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int max_kv);
+size_t attn_tiles_most_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_kv);
 hipError_t launch_attn_tiles(const AttnArgs &a, int which, hipStream_t stream);
 
 }  // namespace biloco

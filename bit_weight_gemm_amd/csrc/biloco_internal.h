@@ -169,7 +169,7 @@ struct AttnArgs {
     void *ws;
 };
 size_t attn_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv);
-hipError_t launch_attn(const AttnArgs &a, hipStream_t stream);
+hipError_t launch_attn(const AttnArgs &a, size_t ws_bytes, hipStream_t stream);
 
 struct NormArgs {
     const uint16_t *x;

@@ -197,7 +197,7 @@ biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
     const AttnArgs a{k_codes, v_codes, k_scales, v_scales, num_pages, kv_heads, page_size, head_dim,
                      q, q_stride, q_heads, q_start, kv_len, block_table, max_pages, B, T,
                      max_q_len, max_kv_len, scale, window, sinks, o, o_stride, lse, workspace};
-    return launch_attn(a, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
+    return launch_attn(a, workspace_bytes, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
 }
 
 biloco_status biloco_norm_gate_residual(const uint16_t *x, int64_t x_stride, const uint16_t *post_w,

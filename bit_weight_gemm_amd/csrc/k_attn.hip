@@ -556,10 +556,24 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
 // Measured (128 channels), joins included: 32 sequences of 1 to 8192 tokens, 40
 // heads: 93 us whole, 106 split; one of 613 tokens: 8.7 and 11.3; 16 of 1 to 4100
 // tokens, up to 40 rows, 8 heads: 81 and 24.
+constexpr int64_t kFreeTurns = 4, kMostTurns = 16;
+int64_t turns_of(int64_t chunks, int row_shift) { return ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves; }
 bool whole_items(int64_t items, int64_t chunks, int row_shift) {
-    const int64_t alone = ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves;
-    const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + 4;
-    return alone <= (shared < 16 ? shared : 16);
+    const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + kFreeTurns;
+    return turns_of(chunks, row_shift) <= (shared < kMostTurns ? shared : kMostTurns);
+}
+
+// The most workspace that pieces of items need, for a call of these sizes or
+// of smaller ones: up to kFreeTurns no number of items is split, up to kMostTurns only
+// fewer items than the 256 at which `shared` passes `alone`.
+size_t split_bytes(int64_t items, int dim, int rows) {
+    return begun_slots(items) * sizeof(Begun) + (items + kPieces) * part_floats(dim, rows) * sizeof(float);
+}
+size_t most_split_bytes(int64_t items, int64_t chunks, int row_shift, int dim, int rows) {
+    constexpr int64_t kShared = kPieces * kSplitWaves / kWholeWaves;
+    const int64_t turns = turns_of(chunks, row_shift);
+    if (turns <= kFreeTurns) return 0;
+    return split_bytes(turns <= kMostTurns && items >= kShared ? kShared - 1 : items, dim, rows);
 }
 
 struct Plan {
@@ -567,7 +581,8 @@ struct Plan {
     int64_t items;
     bool rows, tiles;      // which kernels the call needs
     bool whole;            // a workgroup an item
-    size_t rows_bytes, tiles_bytes;
+    size_t bytes;          // of workspace that the launches use, one after the other
+    size_t most_bytes;     // at least that, whatever the window, for this call and every smaller one
 };
 
 // What the host can know: at most this many rows, tiles and chunks.  A batch
@@ -584,14 +599,18 @@ Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int ma
     p.items = (int64_t)B * kv_heads;      // at most 2^26
     const int64_t chunks = (max_kv + kChunk - 1) / kChunk;
     p.whole = whole_items(p.items, chunks, p.row_shift);
-    p.rows_bytes = p.rows && !p.whole      // whatever the window
-                       ? begun_slots(p.items) * sizeof(Begun) + (p.items + kPieces) * part_floats(dim, p.most_rows) * sizeof(float)
-                       : 0;
+    p.most_bytes = most_split_bytes(p.items, chunks, p.row_shift, dim, p.most_rows);
     if (window > 0) {
         const int64_t seen = ((int64_t)window + longest + 2 * kChunk) / kChunk + ((int64_t)sinks + kChunk - 1) / kChunk;
         p.whole = p.whole || whole_items(p.items, seen < chunks ? seen : chunks, p.row_shift);
     }
-    p.tiles_bytes = p.tiles ? attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv).ws_bytes : 0;
+    p.bytes = p.rows && !p.whole ? split_bytes(p.items, dim, p.most_rows) : 0;
+    if (p.tiles) {
+        const size_t now = attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv).ws_bytes;
+        const size_t most = attn_tiles_most_bytes(B, T, q_heads, kv_heads, dim, max_kv);
+        p.bytes = p.bytes < now ? now : p.bytes;
+        p.most_bytes = p.most_bytes < most ? most : p.most_bytes;
+    }
     return p;
 }
 
@@ -626,16 +645,16 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
 
 size_t attn_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv) {
     if (B == 0 || T == 0) return 0;
-    const Plan p = plan_of(B, T, q_heads, kv_heads, dim, max_q, max_kv, 0, 0);
-    return p.rows_bytes + p.tiles_bytes;
+    return plan_of(B, T, q_heads, kv_heads, dim, max_q, max_kv, 0, 0).most_bytes;
 }
 
-hipError_t launch_attn(const AttnArgs &a, hipStream_t stream) {
+// The launches for many and for few rows follow one another on the stream and
+// use the same workspace.
+hipError_t launch_attn(const AttnArgs &a, size_t ws_bytes, hipStream_t stream) {
     const Plan p = plan_of(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_q, a.max_kv, a.window, a.sinks);
+    if (p.bytes > ws_bytes) return hipErrorInvalidValue;
     if (p.tiles) {      // first: the longest workgroups
-        AttnArgs t = a;
-        t.ws = static_cast<char *>(a.ws) + p.rows_bytes;
-        const hipError_t e = launch_attn_tiles(t, p.rows ? kManyRows : kAllSeqs, stream);
+        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, stream);
         if (e != hipSuccess || !p.rows) return e;
     }
     return a.dim == 64 ? launch<64>(a, p, stream) : launch<128>(a, p, stream);

@@ -485,6 +485,18 @@ TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int 
     return p;
 }
 
+// The most that a plan of these sizes or of smaller ones asks for: fewer rows can
+// have more pieces, so the plan's own bytes do not grow with the call.  Items below
+// kWantItems are split, into fewer than kWantItems + items pieces in all.
+size_t attn_tiles_most_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_kv) {
+    const TilesPlan p = attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv);
+    const int64_t all = (int64_t)p.tiles * kv_heads, items = all < kWantItems ? all : kWantItems - 1;
+    const int64_t pieces = ((int64_t)max_kv + 4 * kChunk - 1) / (4 * kChunk);
+    if (pieces <= 1) return 0;
+    const int64_t most = items * pieces < items + kWantItems - 1 ? items * pieces : items + kWantItems - 1;
+    return (size_t)most * kTileRows * (dim + 2) * sizeof(float);
+}
+
 hipError_t launch_attn_tiles(const AttnArgs &a, int which, hipStream_t stream) {
     return a.dim == 64 ? launch<64>(a, which, stream) : launch<128>(a, which, stream);
 }

@@ -54,7 +54,8 @@ class AttentionBlock:
             raise ValueError("the products' sizes do not fit the heads")
         self.qkv, self.out, self.heads, self.kv_heads, self.dim = qkv, out, heads, kv_heads, head_dim
         self.cache, self.cos_sin, self.post_w, self.next_w = cache, cos_sin, post_w, next_w
-        self.max_kv_len, self.res_scale, self.window, self.sinks, self.eps = max_kv_len, res_scale, window, sinks, eps
+        self.max_sequences, self.max_kv_len, self.res_scale, self.window, self.sinks, self.eps = (
+            max_sequences, max_kv_len, res_scale, window, sinks, eps)
         M = self.MAX_TOKENS
 
         def rows(*shape, dtype=torch.bfloat16):
@@ -67,9 +68,8 @@ class AttentionBlock:
         self._codes = rows(self.width // 2, dtype=torch.uint8)
         self._scales = rows(self.width // 16, dtype=torch.uint8)
         self._qkv_ws, self._out_ws = qkv.workspace(M, device), out.workspace(M, device)
-        # enough for every step of up to M tokens over up to max_sequences
-        need = max(B.biloco_attn_workspace_bytes(b, M, heads, kv_heads, head_dim, q, max_kv_len)
-                   for b in range(1, max_sequences + 1) for q in range(1, M + 1))
+        # that of the largest step covers every smaller one
+        need = B.biloco_attn_workspace_bytes(max_sequences, M, heads, kv_heads, head_dim, M, max_kv_len)
         self._attn_ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
     def step(self, h, codes, scales, res, positions, q_start, kv_len, block_table, max_q_len: int):
@@ -78,6 +78,8 @@ class AttentionBlock:
         T, heads, kv, d = h.shape[0], self.heads, self.kv_heads, self.dim
         if T > self.MAX_TOKENS:
             raise ValueError(f"at most {self.MAX_TOKENS} new tokens a step")
+        if kv_len.shape[0] > self.max_sequences:      # before the cache changes
+            raise ValueError(f"at most {self.max_sequences} sequences a step")
         a, o = self.qkv, self.out
         y = self._qkv[:T]
         B.biloco_gemm_lowrank(codes, scales, h, a.w_codes, a.w_scales, a.g, a.v_packed, a.u_packed, a.alpha, T, a.N,

@@ -429,8 +429,9 @@ biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
                                 float *lse, void *workspace, size_t workspace_bytes,
                                 hipStream_t stream);
 
-/* Bytes of workspace biloco_attn_paged needs for these sizes (0 is possible).
- * No HIP call. */
+/* Bytes of workspace biloco_attn_paged needs for these sizes (0 is possible),
+ * and for every call with smaller B, T, max_q_len and max_kv_len on the same heads:
+ * a workspace for a program's largest step serves all of its steps.  No HIP call. */
 biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
                                           int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
                                           size_t *bytes);
