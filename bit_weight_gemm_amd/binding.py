@@ -140,6 +140,19 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """What a call allocates by itself, from the memory of the stream it runs on:
+    a block that another stream has freed can still be in use by its pending work."""
+    if stream is None or not torch.cuda.is_initialized():
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        if stream == _raw_stream(_current_device()):
+            return torch.empty(shape, dtype=dtype, device=device)
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ok(status: int, what: str):
     if status != BILOCO_OK:
         raise BilocoError(status, what)
@@ -307,7 +320,8 @@ def biloco_schedules_for(M: int, N: int, K: int, r: int) -> list:
 # `cache` is the tuple (k_codes [pages][kv_heads][page][dim], v_codes
 # [pages][kv_heads][page/8][dim][8], k_scales [pages][kv_heads], v_scales
 # likewise), uint8, contiguous.  q, k, v and o are bf16 [tokens][heads][dim] whose
-# heads and channels are contiguous; their token strides are free.
+# heads and channels are contiguous; their token strides are free.  Outputs and
+# workspaces that are not given belong to `stream`, like any tensor made under it.
 
 def biloco_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> tuple:
     """Uninitialised cache arrays in the layouts above (plain allocation)."""
@@ -346,7 +360,7 @@ def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_
     positions int32 [axes][T]; cos_sin fp32 [n_pos][rot_dim] (None: no rotation);
     pair_axis: one byte per pair, the axis it turns by."""
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if k.shape[0] == 0:      # an empty tensor has no address
         return q_out
     st = (_layer or _ext()).kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_table, max_q_len,
@@ -368,15 +382,13 @@ def biloco_attn_paged(cache, q, q_start, kv_len, block_table, max_q_len: int, ma
                       window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of the new tokens q over the cache; returns out."""
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
     if q.shape[0] == 0:      # an empty tensor has no address
         return out
     if workspace is None:
         _, kv_heads, _, dim = cache[0].shape
         n = biloco_attn_workspace_bytes(kv_len.shape[0], q.shape[0], q.shape[1], kv_heads, dim, max_q_len, max_kv_len)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
-        if stream is not None:      # it may be given out again on its own stream
-            workspace.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        workspace = _empty(max(n, 16), torch.uint8, q.device, stream)
     st = (_layer or _ext()).attn_paged(cache, q, q_start, kv_len, block_table, max_q_len, max_kv_len, scale, window,
                                        sinks, out, lse, workspace, _stream(stream))
     if st:
@@ -391,9 +403,9 @@ def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: 
     gate [1][C] (every token) or [T][C].  a_codes and a_scales: h's FP4
     quantisation (outputs)."""
     if res_out is None:
-        res_out = torch.empty(res.shape, dtype=res.dtype, device=x.device)
+        res_out = _empty(res.shape, res.dtype, x.device, stream)
     if h is None:
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        h = _empty(x.shape, torch.bfloat16, x.device, stream)
     if x.shape[0] == 0:      # an empty tensor has no address
         return res_out, h
     st = (_layer or _ext()).norm_gate_residual(x, res, pre_w, post_w, gate, res_scale, eps, w_offset, res_out, h,
