@@ -140,6 +140,15 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _place(stream):
+    """(stream, current device) of a call that checks its tensors' device; -1 where
+    no device is in use yet, which no tensor can be on."""
+    if not torch.cuda.is_initialized():
+        return _stream(stream), -1
+    device = _current_device()
+    return (_raw_stream(device) if stream is None else _stream(stream)), device
+
+
 def _empty(shape, dtype, device, stream):
     """What a call allocates by itself, from the memory of the stream it runs on:
     a block that another stream has freed can still be in use by its pending work."""
@@ -364,7 +373,7 @@ def biloco_kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_
     if k.shape[0] == 0:      # an empty tensor has no address
         return q_out
     st = (_layer or _ext()).kv_append(cache, q, k, v, positions, cos_sin, q_start, kv_len, block_table, max_q_len,
-                                      q_out, pair_axis, interleaved, _stream(stream))
+                                      q_out, pair_axis, interleaved, *_place(stream))
     if st:
         _ok(st, "biloco_kv_append")
     return q_out
@@ -390,7 +399,7 @@ def biloco_attn_paged(cache, q, q_start, kv_len, block_table, max_q_len: int, ma
         n = biloco_attn_workspace_bytes(kv_len.shape[0], q.shape[0], q.shape[1], kv_heads, dim, max_q_len, max_kv_len)
         workspace = _empty(max(n, 16), torch.uint8, q.device, stream)
     st = (_layer or _ext()).attn_paged(cache, q, q_start, kv_len, block_table, max_q_len, max_kv_len, scale, window,
-                                       sinks, out, lse, workspace, _stream(stream))
+                                       sinks, out, lse, workspace, *_place(stream))
     if st:
         _ok(st, "biloco_attn_paged")
     return out
@@ -409,7 +418,7 @@ def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: 
     if x.shape[0] == 0:      # an empty tensor has no address
         return res_out, h
     st = (_layer or _ext()).norm_gate_residual(x, res, pre_w, post_w, gate, res_scale, eps, w_offset, res_out, h,
-                                               a_codes, a_scales, _stream(stream))
+                                               a_codes, a_scales, *_place(stream))
     if st:
         _ok(st, "biloco_norm_gate_residual")
     return res_out, h

@@ -73,9 +73,9 @@ hipStream_t stream(PyObject *o) {
     return (hipStream_t)(uintptr_t)v;
 }
 
-// The last check: every array that the kernels will touch is the GPU's, and
-// the same one's.
-void on_one_gpu(std::initializer_list<const Tensor *> all) {
+// The last check: every array that the kernels will touch is a GPU's, the same
+// one's, and that GPU is the current one, which the kernels are launched on.
+void on_one_gpu(PyObject *current, std::initializer_list<const Tensor *> all) {
     const Tensor *first = nullptr;
     for (const Tensor *t : all) {
         if (!t) continue;
@@ -83,6 +83,7 @@ void on_one_gpu(std::initializer_list<const Tensor *> all) {
         if (!t->is_cuda() || t->get_device() != first->get_device())
             throw std::invalid_argument("tensors of one GPU expected");
     }
+    if (first->get_device() != integer(current)) throw std::invalid_argument("tensors of the current GPU expected");
 }
 
 template <class... N>
@@ -199,8 +200,8 @@ Status append(PyObject *const *a) {
         so = token_stride(*out, T, heads, c.dim, "q_out");
     }
     const int64_t sk = token_stride(k, T, c.heads, c.dim, "k"), sv = token_stride(v, T, c.heads, c.dim, "v");
-    on_one_gpu({c.t[0], c.t[1], c.t[2], c.t[3], q, &k, &v, pos, cs, out, &tensor(a[6], "q_start"),
-                &tensor(a[7], "kv_len"), &tensor(a[8], "block_table")});
+    on_one_gpu(a[14], {c.t[0], c.t[1], c.t[2], c.t[3], q, &k, &v, pos, cs, out, &tensor(a[6], "q_start"),
+                       &tensor(a[7], "kv_len"), &tensor(a[8], "block_table")});
     return g_append(c.p[0], c.p[1], c.p[2], c.p[3], c.pages, c.heads, c.page, c.dim, q ? q->data_ptr() : nullptr, sq,
                     k.data_ptr(), sk, v.data_ptr(), sv, heads, positions, axes, pair_axis,
                     cs ? (const float *)cs->data_ptr() : nullptr, n_pos, rot, (int32_t)PyObject_IsTrue(a[12]), r.start,
@@ -220,8 +221,8 @@ Status attn(PyObject *const *a) {
         refuse("lse", "contiguous fp32 [tokens][heads] expected");
     if (!ws.is_contiguous()) refuse("workspace", "contiguous memory expected");
     const int64_t sq = token_stride(q, T, heads, c.dim, "q"), so = token_stride(out, T, heads, c.dim, "out");
-    on_one_gpu({c.t[0], c.t[1], c.t[2], c.t[3], &q, &out, &ws, lse, &tensor(a[2], "q_start"), &tensor(a[3], "kv_len"),
-                &tensor(a[4], "block_table")});
+    on_one_gpu(a[14], {c.t[0], c.t[1], c.t[2], c.t[3], &q, &out, &ws, lse, &tensor(a[2], "q_start"),
+                       &tensor(a[3], "kv_len"), &tensor(a[4], "block_table")});
     return g_attn(c.p[0], c.p[1], c.p[2], c.p[3], c.pages, c.heads, c.page, c.dim, q.data_ptr(), sq, heads, r.start,
                   r.len, r.table, r.max_pages, r.B, size32(T, "q"), integer32(a[5], "max_q_len"),
                   integer32(a[6], "max_kv_len"), number(a[7]), integer32(a[8], "window"), integer32(a[9], "sinks"),
@@ -248,7 +249,7 @@ Status norm(PyObject *const *a) {
                   sro = row_stride(res_out, T, C, kind, "res_out"), sh = row_stride(h, T, C, at::kBFloat16, "h");
     const void *pw = vector(post, C, "post_w"), *w = vector(&pre, C, "pre_w");
     uint8_t *pc = bytes(codes, T, C / 2, "a_codes"), *ps = bytes(scales, T, C / 16, "a_scales");
-    on_one_gpu({&x, &res, &pre, post, gate, &res_out, &h, codes, scales});
+    on_one_gpu(a[13], {&x, &res, &pre, post, gate, &res_out, &h, codes, scales});
     return g_norm(x.data_ptr(), sx, pw, gate ? gate->data_ptr() : nullptr, gate_stride, number(a[5]), res.data_ptr(),
                   sr, kind == at::kFloat, w, number(a[6]), number(a[7]), size32(T, "x"), size32(C, "x"),
                   res_out.data_ptr(), sro, h.data_ptr(), sh, pc, ps, stream(a[12]));
@@ -292,9 +293,9 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define FASTCALL(f) ((PyCFunction)(void (*)(void))(f))
 PyMethodDef methods[] = {{"bind", FASTCALL(bind), METH_FASTCALL, "addresses of the three entry points"},
-                         {"kv_append", FASTCALL((entry<append, 14>)), METH_FASTCALL, "biloco_kv_append"},
-                         {"attn_paged", FASTCALL((entry<attn, 14>)), METH_FASTCALL, "biloco_attn_paged"},
-                         {"norm_gate_residual", FASTCALL((entry<norm, 13>)), METH_FASTCALL, "biloco_norm_gate_residual"},
+                         {"kv_append", FASTCALL((entry<append, 15>)), METH_FASTCALL, "biloco_kv_append"},
+                         {"attn_paged", FASTCALL((entry<attn, 15>)), METH_FASTCALL, "biloco_attn_paged"},
+                         {"norm_gate_residual", FASTCALL((entry<norm, 14>)), METH_FASTCALL, "biloco_norm_gate_residual"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

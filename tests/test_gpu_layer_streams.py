@@ -1,6 +1,7 @@
-"""The decoder-layer calls on a stream that is not the current one: what a call
-allocates by itself comes from the stream it runs on, whose memory no other
-stream's pending work can still be using."""
+"""The decoder-layer calls on a stream that is not the current one, and with
+tensors of a GPU that is not: what a call allocates by itself comes from the stream
+it runs on, whose memory no other stream's pending work can still be using;
+tensors of another GPU than the current one are refused."""
 import pytest
 import torch
 
@@ -79,3 +80,22 @@ def test_the_current_stream_by_name(name, stream):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b) and _pool_of(a) == cur.cuda_stream
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_another_gpu_than_the_current_one_is_refused(name, monkeypatch):
+    d = _inputs()
+    cur = torch.cuda.current_stream()
+    monkeypatch.setattr(B, "_current_device", lambda: 1)      # as if GPU 1 were current
+    kw = dict(stream=cur.cuda_stream)
+    if name == "attend":
+        kw.update(out=torch.empty_like(d["q"]), workspace=torch.empty(
+            B.biloco_attn_workspace_bytes(2, 2, 16, 2, 64, 1, 3000), dtype=torch.uint8, device="cuda"))
+    elif name == "append":
+        kw.update(q_out=torch.empty_like(d["q"]))
+    else:
+        kw.update(res_out=torch.empty_like(d["x"]), h=torch.empty_like(d["x"]))
+    with pytest.raises(ValueError, match="current GPU"):
+        CALLS[name](d, **kw)
+    monkeypatch.undo()
+    CALLS[name](d, **kw)
