@@ -28,6 +28,15 @@ Span rows(const void *p, int64_t n, int64_t stride, int64_t width, size_t size) 
     return {p, n > 0 ? (size_t)((n - 1) * stride + width) * size : 0};
 }
 
+// Rows of a and of b (the same number of each, `stride` bytes apart in both)
+// that lie between one another without meeting: b's columns are within the gap
+// that follows each of a's rows.
+bool between(const void *a, size_t a_width, const void *b, size_t b_width, size_t stride) {
+    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+    const size_t at = b0 >= a0 ? (b0 - a0) % stride : (stride - (a0 - b0) % stride) % stride;
+    return at >= a_width && at + b_width <= stride;
+}
+
 // Token strides are bounded so that every byte offset fits 62 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 30;
 
@@ -118,11 +127,14 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
     for (int i = 0; i < 5; ++i) {
         for (int j = i + 1; j < 5; ++j)
             if (overlaps(out[i], out[j])) return BILOCO_ERR_INVALID_VALUE;
-        // rows of q, k and v of one product lie between one another: q_out may
-        // be q itself, and is then not compared with k's and v's spans
-        for (const Span &s : in)
-            if (!(i == 4 && q_out == q && (s.p == k || s.p == v)) && overlaps(out[i], s))
-                return BILOCO_ERR_INVALID_VALUE;
+        // rows of q, k and v of one product lie between one another, and q_out may
+        // be q itself: k's and v's columns are then not to be q's
+        for (int j = 0; j < 7; ++j) {
+            const int64_t stride = j == 0 ? k_stride : v_stride;
+            const bool apart = i == 4 && j < 2 && q_out == q && stride == q_out_stride &&
+                               between(q_out, (size_t)qw * 2, in[j].p, (size_t)kw * 2, (size_t)stride * 2);
+            if (!apart && overlaps(out[i], in[j])) return BILOCO_ERR_INVALID_VALUE;
+        }
     }
     if (q_heads > 0) {
         const Span qs = rows(q, T, q_stride, qw, 2);

@@ -136,3 +136,14 @@ def test_plain_formats():
     for amax, byte in ((448.0, 127), (448.0001, 128), (224.0, 126), (0.0, 1), (1.0, 119), (1e-45, 1)):
         assert layer.need_byte(amax) == byte
         assert amax <= 448 * 2.0 ** (byte - 127)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k=5 * A), dict(v=5 * A), dict(k=5 * A + 16), dict(v=5 * A + 2 * 8192 - 16),       # columns of q's own
+    dict(k=5 * A + 2 * 8192, sk=10248), dict(v=5 * A + 2 * 10240, sv=20480),      # other strides: rows meet q's
+    dict(k=5 * A - 2 * 1024 + 16), dict(k=5 * A + 2 * 10240 - 16),      # the last columns reach the next row's q
+    dict(k=5 * A + 2 * 10240), dict(v=5 * A + 3 * 2 * 10240 + 32)])
+def test_append_in_place_refuses_keys_within_the_queries(kw):
+    """q_out = q: k and v may be columns of the same rows, but not q's."""
+    assert append(**{**dict(T=5, qo=5 * A, sqo=10240), **kw}) == BAD
+    assert append(T=0, qo=5 * A, sqo=10240, **kw) == B.BILOCO_OK
