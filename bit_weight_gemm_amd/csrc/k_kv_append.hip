@@ -334,8 +334,9 @@ kv_append_kernel(const KvAppendArgs a, int q_blocks, int parts, int64_t items) {
     const int b = (int)(item / parts), part = (int)(item % parts);
     // the sequence's rows, kept inside the batch, and the page's share of them
     const int first = min(max(a.q_start[b], 0), a.T), last = min(max(a.q_start[b + 1], first), a.T);
-    const int n = last - first, len = a.kv_len[b];
-    const int past = max(len - n, 0);
+    // row i of n is token len - n + i; the first rows of more new tokens than
+    // the sequence has are no tokens
+    const int len = max(a.kv_len[b], 0), n = min(last - first, len), past = len - n;
     const int col = past / a.page + part;
     if (n == 0 || col >= a.max_pages) return;      // uniform over the item
     PagePart pp;
@@ -343,7 +344,7 @@ kv_append_kernel(const KvAppendArgs a, int q_blocks, int parts, int64_t items) {
     pp.lo = (int)max((int64_t)past - s0, (int64_t)0);
     pp.hi = (int)min((int64_t)past + n - s0, (int64_t)a.page);
     if (pp.lo >= pp.hi) return;
-    pp.t0 = first + (s0 + pp.lo - past);
+    pp.t0 = last - n + (s0 + pp.lo - past);
     pp.page = a.table[(int64_t)b * a.max_pages + col];
     if (pp.page < 0 || pp.page >= a.num_pages) return;
     if (which == 0) append_k<D, NW, PASSES>(a, pp, h, tid, lds);

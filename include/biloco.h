@@ -363,6 +363,8 @@ int32_t biloco_schedules_for(int32_t M, int32_t N, int32_t K, int32_t r,
  *   pair i is (x[i], x[i + R]), or (x[2i], x[2i + 1]) if interleaved != 0
  *   (a, b) -> (a c - b s, b c + a s), c = cos_sin[p][i], s = cos_sin[p][R + i],
  *   p = positions[pair_axis[i]][t]  (fp32; products and sums rounded one by one)
+ * A row at a negative place (more new tokens than kv_len) is no token: its q is
+ * rotated, nothing of it is appended.
  * Channels from rot_dim on stay as they are.  q_out is the rotated q, rounded
  * once to bf16 (it may be q itself).  The rotated k (fp32) and v are quantised:
  * a block's scale byte is the smallest b >= 1 with max|x| <= 448 * 2^(b - 127)

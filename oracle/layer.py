@@ -75,7 +75,7 @@ def append(cache, x_k, x_v, q_start, kv_len, table):
     for b in range(len(kv_len)):
         n = q_start[b + 1] - q_start[b]
         past = kv_len[b] - n
-        a = past
+        a = max(past, 0)      # rows before token 0 are no tokens
         while a < kv_len[b]:
             pg, lo = table[b, a // page], a % page
             hi = min(page, lo + kv_len[b] - a)

@@ -257,3 +257,18 @@ def test_offsets_beyond_32_bits(new):
     assert torch.equal(q, q0)
     for t, u in zip(big, small):
         assert torch.equal(t[-n:], u)
+
+
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("kv,new", [([0, 7], [1, 1]), ([3, 40, 0], [5, 2, 3]), ([0, 0, 0], [1, 1, 1]), ([20, 90], [70, 30])])
+def test_rows_before_the_first_token_are_not_appended(dim, page, kv, new):
+    """Row i of n new ones is token kv_len - n + i; where that is negative (an idle
+    slot of a padded batch, for one) its q is rotated and nothing is written, not
+    even to the pages that its table row still names."""
+    b = Batch([max(0, k - n) for k, n in zip(kv, new)], new, 4, 2, dim, page, seed=sum(kv) + page)
+    b.kv_len = np.array(kv, np.int32)
+    b.past = b.kv_len - b.new
+    b.table[:] = np.where(b.table < 0, b.table.max(), b.table)      # left from earlier sequences
+    idle = np.array(kv) == 0
+    b.table[idle] = b.table[~idle][0] if (~idle).any() else b.table[idle]
+    b.check()
