@@ -45,8 +45,10 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 _lib = None
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# the short ways, where torch has them; a torch without GPU support has neither,
+# and the calls that make no HIP call need neither
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 class BilocoError(RuntimeError):

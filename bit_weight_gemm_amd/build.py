@@ -84,13 +84,36 @@ BINDING_SRC = os.path.join(CSRC, "layer_binding.cpp")
 BINDING = os.path.join(PKG, "_layer_binding.so")
 
 
-def build_binding(verbose: bool = True) -> str:
+def binding_lacks() -> str:
+    """What this machine lacks to build the tensor binding; empty if nothing."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    header = os.path.join("torch", "csrc", "autograd", "python_variable.h")
+    if not any(os.path.exists(os.path.join(d, header)) for d in cpp_extension.include_paths()):
+        return "torch's headers"
+    return ""
+
+
+def build_binding(verbose: bool = True) -> str | None:
     """The CPython extension that marshals torch tensors for the decoder-layer
-    entry points (host code only, g++ against torch's headers)."""
+    entry points (host code only, g++ against torch's headers).  Only those calls
+    need it: without a host compiler the library is built all the same, and
+    the calls say what is missing."""
     import sysconfig
 
     import torch
     from torch.utils import cpp_extension
+    lacks = binding_lacks()
+    if lacks:
+        if os.path.exists(BINDING):      # of another source
+            os.remove(BINDING)
+        print(f"NOT built: {BINDING} (no {lacks}); the decoder-layer calls need it")
+        return None
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", BINDING_SRC, "-o", tmp,
