@@ -62,6 +62,11 @@ int32_t size32(int64_t v, const char *what) {
     if (v > INT32_MAX) refuse(what, "fewer than 2^31 rows expected");
     return (int32_t)v;
 }
+int32_t truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError();
+    return v;
+}
 float number(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw PythonError();
@@ -199,13 +204,14 @@ Status append(PyObject *const *a) {
         sq = token_stride(*q, T, heads, c.dim, "q");
         so = token_stride(*out, T, heads, c.dim, "q_out");
     }
+    const int32_t interleaved = truth(a[12]);
     const int64_t sk = token_stride(k, T, c.heads, c.dim, "k"), sv = token_stride(v, T, c.heads, c.dim, "v");
     on_one_gpu(a[14], {c.t[0], c.t[1], c.t[2], c.t[3], q, &k, &v, pos, cs, out, &tensor(a[6], "q_start"),
                        &tensor(a[7], "kv_len"), &tensor(a[8], "block_table")});
     return g_append(c.p[0], c.p[1], c.p[2], c.p[3], c.pages, c.heads, c.page, c.dim, q ? q->data_ptr() : nullptr, sq,
                     k.data_ptr(), sk, v.data_ptr(), sv, heads, positions, axes, pair_axis,
-                    cs ? (const float *)cs->data_ptr() : nullptr, n_pos, rot, (int32_t)PyObject_IsTrue(a[12]), r.start,
-                    r.len, r.table, r.max_pages, r.B, size32(T, "k"), integer32(a[9], "max_q_len"),
+                    cs ? (const float *)cs->data_ptr() : nullptr, n_pos, rot, interleaved, r.start, r.len,
+                    r.table, r.max_pages, r.B, size32(T, "k"), integer32(a[9], "max_q_len"),
                     q ? out->data_ptr() : nullptr, so, stream(a[13]));
 }
 
@@ -271,6 +277,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     } catch (const PythonError &) {
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown exception");
     }
     return nullptr;
 }

@@ -147,3 +147,16 @@ def test_append_in_place_refuses_keys_within_the_queries(kw):
     """q_out = q: k and v may be columns of the same rows, but not q's."""
     assert append(**{**dict(T=5, qo=5 * A, sqo=10240), **kw}) == BAD
     assert append(T=0, qo=5 * A, sqo=10240, **kw) == B.BILOCO_OK
+
+
+def test_append_passes_on_the_error_of_a_truth_value():
+    import torch
+
+    class Odd:
+        def __bool__(self):
+            raise KeyError("odd")
+    cache = B.biloco_kv_cache(4, 2, 16, 64, device="cpu")
+    kv = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    i32 = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(KeyError, match="odd"):
+        B.biloco_kv_append(cache, None, kv, kv, None, None, i32, i32[:1], i32[None], 1, interleaved=Odd(), stream=1)
