@@ -80,6 +80,8 @@ class AttentionBlock:
             raise ValueError(f"at most {self.MAX_TOKENS} new tokens a step")
         if kv_len.shape[0] > self.max_sequences:      # before the cache changes
             raise ValueError(f"at most {self.max_sequences} sequences a step")
+        if T == 0:
+            return self._h[:0], self._codes[:0], self._scales[:0]
         a, o = self.qkv, self.out
         y = self._qkv[:T]
         B.biloco_gemm_lowrank(codes, scales, h, a.w_codes, a.w_scales, a.g, a.v_packed, a.u_packed, a.alpha, T, a.N,
