@@ -67,6 +67,12 @@ def main():
     ap.add_argument("--kv-heads", type=int, default=8)
     ap.add_argument("--rank", type=int, default=256)
     a = ap.parse_args()
+    if not 1 <= a.sequences <= AttentionBlock.MAX_TOKENS:
+        ap.error(f"--sequences is 1 to {AttentionBlock.MAX_TOKENS}, the rows of a product")
+    if a.steps < 1:
+        ap.error("--steps is at least 1")
+    if a.prompt < 0:
+        ap.error("--prompt is at least 0")
     d, width, page = 128, a.heads * 128, 32
     batch = Batch(a.sequences, page, a.prompt + a.steps + 1)
     ones = torch.ones(width, dtype=torch.bfloat16, device="cuda")
@@ -87,7 +93,7 @@ def main():
             n = min(32, a.prompt - at)
             run([n if i == b else 0 for i in range(a.sequences)],
                 torch.randn(n, width, device="cuda").to(torch.bfloat16))
-    x = torch.randn(min(a.sequences, 32), width, device="cuda").to(torch.bfloat16)
+    x = torch.randn(a.sequences, width, device="cuda").to(torch.bfloat16)
     for _ in range(a.steps):
         h, _, _ = run([1] * a.sequences, x)
     torch.cuda.synchronize()

@@ -1,7 +1,14 @@
-"""The attention block's empty steps (no GPU)."""
+"""The attention block's empty steps, the example's refusals (no GPU)."""
+import os
+import subprocess
+import sys
+
+import pytest
 import torch
 
 from bit_weight_gemm_amd.decoder import AttentionBlock, Linear
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _block():
@@ -18,3 +25,10 @@ def test_a_step_of_no_tokens_is_empty():
     h, codes, scales = block.step(x, x[:, :128].byte(), x[:, :16].byte(), x, i32[None, :0], i32, i32[:2], i32[:2, None], 1)
     assert (tuple(h.shape), tuple(codes.shape), tuple(scales.shape)) == ((0, 256), (0, 128), (0, 16))
     assert h.dtype == torch.bfloat16 and codes.dtype == scales.dtype == torch.uint8
+
+
+@pytest.mark.parametrize("args", [["--sequences", "33"], ["--sequences", "0"], ["--steps", "0"], ["--prompt", "-5"]])
+def test_example_refuses_what_a_step_cannot_take(args):
+    p = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "decode_block.py")] + args, capture_output=True,
+                       text=True)
+    assert p.returncode == 2 and "usage" in p.stderr and args[0] in p.stderr.splitlines()[-1]
