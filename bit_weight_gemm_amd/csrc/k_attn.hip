@@ -549,23 +549,34 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
     if (a.lse && lane == 0) a.lse[t * a.q_heads + h * G + g] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// Whether a workgroup takes a whole item: `chunks` by 8 waves in turn, against
-// an even share of all chunks over the chip's 2048 waves and, for the list and
-// the join, about as long as four more chunks.  Never more than 16 in turn: the
-// host knows the longest sequence only, and the others may be short.
-// Measured (128 channels), joins included: 32 sequences of 1 to 8192 tokens, 40
-// heads: 93 us whole, 106 split; one of 613 tokens: 8.7 and 11.3; 16 of 1 to 4100
-// tokens, up to 40 rows, 8 heads: 81 and 24.
-constexpr int64_t kFreeTurns = 4, kMostTurns = 16;
+// Whether a workgroup takes a whole item: it takes `turns` of 8 waves in turn,
+// against an even share of all chunks over the chip's 2048 waves and, for the list
+// and the join, about as long as four more.  The host knows the longest sequence
+// only, and the others may be short: the longest is not to take more than eight
+// times a CU's share if all were as long (items / 256 items), or, where waves form four
+// groups that read a chunk each, twice.  Up to four turns a join costs more than it saves.
+// Measured, us whole | split, joins included, for 32 and 128 sequences (64/8 heads) and
+// 32 (40/40), lengths all of the longest (=) or spread evenly in their logarithm (~):
+//   longest   32, 64/8 (256 items)     128, 64/8 (1024)         32, 40/40 (1280)
+//    2048     = 24 | 29,  ~ 16 | 14    = 101 | 106, ~ 39 | 39   = 122 | 123, ~ 41 | 38
+//    4096     = 42 | 49,  ~ 27 | 18    = 187 | 191, ~ 43 | 44   = 227 | 230, ~ 51 | 48
+//    8192     = 95 | 101, ~ 46 | 24    = 356 | 363, ~ 69 | 67   = 441 | 449, ~ 77 | 93
+//   16384     = 182 | 191, ~ 85 | 35   = 699 | 709, ~ 139 | 126 = 881 | 897, ~ 168 | 182
+//   32768     = 358 | 366, ~ 185 | 83  = 1408 | 1421, ~ 208 | 197   = 1787 | 1823, ~ 312 | 338
+// One sequence of 613 tokens, 40/40: 8.7 | 11.3.  40 rows, 128 sequences, 64/8 heads: 2048
+// = 196 | 189, ~ 82 | 78; 8192 = 701 | 677, ~ 190 | 167.
+constexpr int64_t kFreeTurns = 4;
 int64_t turns_of(int64_t chunks, int row_shift) { return ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves; }
+int64_t items_a_turn(int row_shift) { return row_shift < 2 ? 32 : 128; }
 bool whole_items(int64_t items, int64_t chunks, int row_shift) {
+    const int64_t turns = turns_of(chunks, row_shift), most = items / items_a_turn(row_shift);
     const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + kFreeTurns;
-    return turns_of(chunks, row_shift) <= (shared < kMostTurns ? shared : kMostTurns);
+    return turns <= shared && (turns <= kFreeTurns || turns <= most);
 }
 
 // The most workspace that pieces of items need, for a call of these sizes or
-// of smaller ones: up to kFreeTurns no number of items is split, up to kMostTurns only
-// fewer items than the 256 at which `shared` passes `alone`.
+// of smaller ones: up to kFreeTurns no number of items is split; above, only fewer items
+// than the 256 at which `shared` passes `turns`, or than turns * items_a_turn.
 size_t split_bytes(int64_t items, int dim, int rows) {
     return begun_slots(items) * sizeof(Begun) + (items + kPieces) * part_floats(dim, rows) * sizeof(float);
 }
@@ -573,7 +584,9 @@ size_t most_split_bytes(int64_t items, int64_t chunks, int row_shift, int dim, i
     constexpr int64_t kShared = kPieces * kSplitWaves / kWholeWaves;
     const int64_t turns = turns_of(chunks, row_shift);
     if (turns <= kFreeTurns) return 0;
-    return split_bytes(turns <= kMostTurns && items >= kShared ? kShared - 1 : items, dim, rows);
+    int64_t most = turns * items_a_turn(row_shift);
+    if (most < kShared) most = kShared;
+    return split_bytes(items < most ? items : most - 1, dim, rows);
 }
 
 struct Plan {
