@@ -160,7 +160,7 @@ struct TilesPlan {
     int splits;       // pieces of the token axis
     size_t ws_bytes;
 };
-TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int max_kv);
+TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int max_kv, int window, int sinks);
 size_t attn_tiles_most_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_kv);
 hipError_t launch_attn_tiles(const AttnArgs &a, int which, hipStream_t stream);
 

@@ -619,7 +619,7 @@ Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int ma
     }
     p.bytes = p.rows && !p.whole ? split_bytes(p.items, dim, p.most_rows) : 0;
     if (p.tiles) {
-        const size_t now = attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv).ws_bytes;
+        const size_t now = attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv, window, sinks).ws_bytes;
         const size_t most = attn_tiles_most_bytes(B, T, q_heads, kv_heads, dim, max_kv);
         p.bytes = p.bytes < now ? now : p.bytes;
         p.most_bytes = p.most_bytes < most ? most : p.most_bytes;

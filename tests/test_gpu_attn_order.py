@@ -96,3 +96,9 @@ def test_a_prompt_of_many_chunks(dim, max_kv):
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (100, 0), (127, 70), (640, 130), (5000, 4), (3, 5000)])
 def test_window_and_sinks_at_128_channels(new, window, sinks):
     Case(new, [700, 300], 4, 2, 128, 16, seed=window + sinks).check(window, sinks)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 3), (700, 200)])
+def test_a_window_far_smaller_than_the_bound(dim, window, sinks):
+    Case([20, 9], [1500, 700], 16, 2, dim, 64, seed=window).check(window, sinks, max_kv=131072)
