@@ -551,10 +551,10 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
 
 // Whether a workgroup takes a whole item: it takes `turns` of 8 waves in turn,
 // against an even share of all chunks over the chip's 2048 waves and, for the list
-// and the join, about as long as four more.  The host knows the longest sequence
+// and the join, about as long as two more (four of 64 channels).  The host knows the longest sequence
 // only, and the others may be short: the longest is not to take more than eight
 // times a CU's share if all were as long (items / 256 items), or, where waves form four
-// groups that read a chunk each, twice.  Up to four turns a join costs more than it saves.
+// groups that read a chunk each, twice.
 // Measured, us whole | split, joins included, for 32 and 128 sequences (64/8 heads) and
 // 32 (40/40), lengths all of the longest (=) or spread evenly in their logarithm (~):
 //   longest   32, 64/8 (256 items)     128, 64/8 (1024)         32, 40/40 (1280)
@@ -563,19 +563,21 @@ attn_join_kernel(const AttnArgs a, int which, int most_rows, int items) {
 //    8192     = 95 | 101, ~ 46 | 24    = 356 | 363, ~ 69 | 67   = 441 | 449, ~ 77 | 93
 //   16384     = 182 | 191, ~ 85 | 35   = 699 | 709, ~ 139 | 126 = 881 | 897, ~ 168 | 182
 //   32768     = 358 | 366, ~ 185 | 83  = 1408 | 1421, ~ 208 | 197   = 1787 | 1823, ~ 312 | 338
-// One sequence of 613 tokens, 40/40: 8.7 | 11.3.  40 rows, 128 sequences, 64/8 heads: 2048
+// One sequence of 512, 1024, 1536 and 2048 tokens (1 to 4 turns), 40/40: 7.5 | 11.2,
+// 10.3 | 11.0, 12.8 | 11.6, 15.6 | 12.8; of 64 channels 6.0 | 9.7, 7.7 | 9.9, 8.6 | 9.9,
+// 10.2 | 11.2.  40 rows, 128 sequences, 64/8 heads: 2048
 // = 196 | 189, ~ 82 | 78; 8192 = 701 | 677, ~ 190 | 167.
-constexpr int64_t kFreeTurns = 4;
+int64_t free_turns(int dim) { return dim == 64 ? 4 : 2; }
 int64_t turns_of(int64_t chunks, int row_shift) { return ((chunks << row_shift) + kWholeWaves - 1) / kWholeWaves; }
 int64_t items_a_turn(int row_shift) { return row_shift < 2 ? 32 : 128; }
-bool whole_items(int64_t items, int64_t chunks, int row_shift) {
+bool whole_items(int64_t items, int64_t chunks, int row_shift, int dim) {
     const int64_t turns = turns_of(chunks, row_shift), most = items / items_a_turn(row_shift);
-    const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + kFreeTurns;
-    return turns <= shared && (turns <= kFreeTurns || turns <= most);
+    const int64_t shared = ((items * chunks) << row_shift) / (kPieces * kSplitWaves) + free_turns(dim);
+    return turns <= shared && (turns <= free_turns(dim) || turns <= most);
 }
 
 // The most workspace that pieces of items need, for a call of these sizes or
-// of smaller ones: up to kFreeTurns no number of items is split; above, only fewer items
+// of smaller ones: up to free_turns no number of items is split; above, only fewer items
 // than the 256 at which `shared` passes `turns`, or than turns * items_a_turn.
 size_t split_bytes(int64_t items, int dim, int rows) {
     return begun_slots(items) * sizeof(Begun) + (items + kPieces) * part_floats(dim, rows) * sizeof(float);
@@ -583,7 +585,7 @@ size_t split_bytes(int64_t items, int dim, int rows) {
 size_t most_split_bytes(int64_t items, int64_t chunks, int row_shift, int dim, int rows) {
     constexpr int64_t kShared = kPieces * kSplitWaves / kWholeWaves;
     const int64_t turns = turns_of(chunks, row_shift);
-    if (turns <= kFreeTurns) return 0;
+    if (turns <= free_turns(dim)) return 0;
     int64_t most = turns * items_a_turn(row_shift);
     if (most < kShared) most = kShared;
     return split_bytes(items < most ? items : most - 1, dim, rows);
@@ -611,11 +613,11 @@ Plan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int ma
     p.most_rows = (int)rows;
     p.items = (int64_t)B * kv_heads;      // at most 2^26
     const int64_t chunks = (max_kv + kChunk - 1) / kChunk;
-    p.whole = whole_items(p.items, chunks, p.row_shift);
+    p.whole = whole_items(p.items, chunks, p.row_shift, dim);
     p.most_bytes = most_split_bytes(p.items, chunks, p.row_shift, dim, p.most_rows);
     if (window > 0) {
         const int64_t seen = ((int64_t)window + longest + 2 * kChunk) / kChunk + ((int64_t)sinks + kChunk - 1) / kChunk;
-        p.whole = p.whole || whole_items(p.items, seen < chunks ? seen : chunks, p.row_shift);
+        p.whole = p.whole || whole_items(p.items, seen < chunks ? seen : chunks, p.row_shift, dim);
     }
     p.bytes = p.rows && !p.whole ? split_bytes(p.items, dim, p.most_rows) : 0;
     if (p.tiles) {
