@@ -29,11 +29,10 @@
 // a second launch.
 //
 // Bound by the cache's bytes where contexts are long, by the chain lookup -> load
-// -> two products -> join where they are short.  Measured on MI355X (a large copy
-// reaches 4.90 TB/s): one sequence of 131071 tokens, 64/8 heads, 55.6 us, 4.83
-// TB/s with the join; 32 sequences of 1 to 8192 tokens, 40/40 heads, 93 us, 4.04
-// TB/s (the longest items end last); one of 613 tokens, 8.6 us, of which the first
-// scores take 2.9.
+// -> two products -> join where they are short.  Measured on MI355X (a kernel that
+// only reads reaches 7.2 TB/s): one sequence of 131071 tokens, 64/8 heads, 55.7 us,
+// 4.82 TB/s with the join (5.3 before it); 32 sequences of 1 to 8192 tokens, 40/40
+// heads, 93 us, 4.03 TB/s (the longest items end last); one of 613 tokens, 8.5 us.
 #include "attn_device.h"
 
 namespace biloco {

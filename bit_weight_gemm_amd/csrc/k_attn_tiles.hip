@@ -12,14 +12,15 @@
 //   so C register 4a + b of lane half h is that token, and registers 8c .. 8c + 7
 //   are the eight tokens 32 t + 16 c + 8 h + (0 .. 7), an operand of the second
 //   product and a group of the cache's value order.
-// Bound by instruction issue: per 64 tokens a wave of 128 channels issues 32
-// matrix instructions of 32 cycles and about 350 others, 32 of them exponentials
-// at a quarter of the rate.  Measured on MI355X: 920 TFLOP/s at 128 channels and
-// 744 at 64 where all tiles are alike (16384 tokens, two workgroups a CU), 782 to
-// 826 TFLOP/s (220 to 208 us) for a causal prompt of 4096 tokens and 40 heads; an 8192-cubed
-// library product reaches 1232.  256 rows a workgroup: 226 us (waves of both
-// halves of a SIMD meet at one barrier); 32-token buffers with three waves a SIMD:
-// 275 us (registers spill, twice the barriers).
+// Per 64 tokens a wave of 128 channels issues 32 matrix instructions of 32 cycles
+// and about 410 others (227 vector ones, 32 of them exponentials at a quarter of the
+// rate, 44 of LDS, 141 scalar); no single part has been shown to bound it.  Measured on
+// MI355X: 840 to 900 TFLOP/s at 128 channels and 720 to 760 at 64 where all tiles are
+// alike (128 rows behind 16384 tokens, three or four workgroups a CU), 782 to 826
+// TFLOP/s (220 to 208 us) for a causal prompt of 4096 tokens and 40 heads; an
+// 8192-cubed library product reaches 1340 to 1430.  256 rows a workgroup: 226 us (waves
+// of both halves of a SIMD meet at one barrier); 32-token buffers with three waves a
+// SIMD: 275 us (registers spill, twice the barriers).
 #include "attn_device.h"
 
 namespace biloco {
@@ -189,7 +190,11 @@ struct Rows32 {
         }
     }
     // Scores to weights, rounded to bf16 for the product (2^-8 of each at
-    // most); their sum is taken before that.
+    // most); their sum is taken before that.  What the rounding leaves as a second
+    // term, as in the kernel for few rows, brings o's error to that of its own rounding
+    // (from 1.3 to 1.4 times that, root mean square) and takes half as many matrix
+    // instructions again, which that kernel has time for and this one has not: 259 us
+    // for 210 on a prompt of 4096 tokens, 441 for 348 on chunks of 64 channels.
     __device__ __forceinline__ void weigh(f32x16a_t &sc, float c2, u32x4_t (&pt)[2]) {
         const float base = m == -__builtin_inff() ? 0.0f : m;      // a row that sees nothing yet
         float sum = 0.0f;

@@ -16,9 +16,9 @@
 // at once.  An item is one wave where at most a few tokens are new (decode)
 // and four waves otherwise.  Bound by memory traffic: q is read and written
 // once, k and v are read once and held in registers while their maximum is
-// found.  Measured on MI355X: 13399 tokens with three axes 111 us, 4.74 TB/s (a
-// large copy reaches 4.90); 32 tokens of as many sequences, 64/8 heads, 5.1 us,
-// which is the launch.
+// found.  Measured on MI355X: 13399 tokens with three axes 111.5 us, 4.74 TB/s
+// (an addition of two large arrays reaches 6.1); 32 tokens of as many sequences, 64/8
+// heads, 5.1 to 5.8 us, which is the launch.
 #include "biloco_device.h"
 #include "biloco_internal.h"
 

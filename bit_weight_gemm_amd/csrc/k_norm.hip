@@ -9,8 +9,9 @@
 // Bound by memory traffic: each of x, gate, res is read once, r' and h are
 // written once; the row stays in registers in fp32 between the two sums.
 // Two reductions a row are the only exchange between waves.  Measured on MI355X:
-// 6001 gated rows of 8192 channels 130 us, 5.30 TB/s (a large copy reaches 4.90);
-// 32 rows of 5120 4.3 us, which is the launch.
+// 6001 gated rows of 8192 channels 129 us, 5.34 TB/s (an addition of two large
+// arrays reaches 6.1); 32 rows of 5120 4.3 us, which is the launch, 4.5 with codes.
+// Rows that are not aligned go an element a lane: 6001 of 8191 channels 348 us, 1.13 TB/s.
 #include "biloco_device.h"
 #include "biloco_internal.h"
 

@@ -407,10 +407,11 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
  *   lse = log(sum over visible j of exp(s_j))
  * A row that sees nothing (more new tokens than cached ones) gives o = 0 and
  * lse = -inf.  Tokens that a row does not see never affect it, whatever their
- * codes hold (NaN included).  Codes and scales are exact in bf16; sums, maxima
- * and o are kept in fp32.  For the product with v a weight is the sum of two
- * bf16 (within 2^-16 of it) where a sequence has at most 64 rows (new tokens
- * times q_heads / kv_heads), and rounded to bf16 (2^-8) where it has more.
+ * codes hold (NaN included).  Codes times scales are exact in bf16 from scale byte
+ * 10 on (below it values under 2^-126 can lose bits); sums, maxima and o are
+ * kept in fp32.  For the product with v a weight is the sum of two bf16 (within
+ * 2^-16 of it) where a sequence has at most 64 rows (new tokens times q_heads /
+ * kv_heads), and rounded to bf16 (2^-8) where it has more.
  *   q [T][q_heads][head_dim] bf16 and o likewise, token strides in elements
  *     (multiples of 8); o must not overlap an input
  *   lse fp32 [T][q_heads] or NULL
