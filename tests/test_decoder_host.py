@@ -1,6 +1,6 @@
 """The attention block's empty steps, the example's refusals (no GPU)."""
 import os
-import subprocess
+import runpy
 import sys
 
 import pytest
@@ -28,7 +28,10 @@ def test_a_step_of_no_tokens_is_empty():
 
 
 @pytest.mark.parametrize("args", [["--sequences", "33"], ["--sequences", "0"], ["--steps", "0"], ["--prompt", "-5"]])
-def test_example_refuses_what_a_step_cannot_take(args):
-    p = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "decode_block.py")] + args, capture_output=True,
-                       text=True)
-    assert p.returncode == 2 and "usage" in p.stderr and args[0] in p.stderr.splitlines()[-1]
+def test_example_refuses_what_a_step_cannot_take(args, monkeypatch, capsys):
+    path = os.path.join(ROOT, "examples", "decode_block.py")
+    monkeypatch.setattr(sys, "argv", [path] + args)
+    with pytest.raises(SystemExit) as e:
+        runpy.run_path(path, run_name="__main__")
+    err = capsys.readouterr().err
+    assert e.value.code == 2 and "usage" in err and args[0] in err.splitlines()[-1]
