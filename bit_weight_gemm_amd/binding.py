@@ -39,7 +39,9 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
             "biloco_quant_weight_nvfp4", "biloco_quant_weight_workspace_bytes",
             "biloco_peel_decompose", "biloco_peel_workspace_bytes", "biloco_gemm_lowrank_quant",
             "biloco_gemm_lowrank_quant_noalloc", "biloco_kv_append", "biloco_attn_paged",
-            "biloco_attn_workspace_bytes", "biloco_norm_gate_residual"]
+            "biloco_attn_workspace_bytes", "biloco_norm_gate_residual", "biloco_quant_mxfp4",
+            "biloco_dequant_mxfp4", "biloco_gemm_mxfp4", "biloco_gemm_mxfp4_quant",
+            "biloco_gemm_mxfp4_workspace_bytes"]
 
 # size of the device array biloco_gemm_lowrank_quant_noalloc works in
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -114,6 +116,16 @@ def lib() -> ctypes.CDLL:
         L.biloco_norm_gate_residual.restype = st
         L.biloco_norm_gate_residual.argtypes = [p, i64, p, p, i64, f32, p, i64, i32, p, f32, f32, i32, i32, p,
                                                 i64, p, i64, p, p, p]
+        L.biloco_quant_mxfp4.restype = st
+        L.biloco_quant_mxfp4.argtypes = [p, i64, i32, i32, i32, p, p, p]
+        L.biloco_dequant_mxfp4.restype = st
+        L.biloco_dequant_mxfp4.argtypes = [p, p, i32, i32, p, i64, i32, p]
+        L.biloco_gemm_mxfp4.restype = st
+        L.biloco_gemm_mxfp4.argtypes = [p, p, p, p, i32, i32, i32, p, i64, i32, p, sz, p]
+        L.biloco_gemm_mxfp4_quant.restype = st
+        L.biloco_gemm_mxfp4_quant.argtypes = [p, i64, p, p, i32, i32, i32, p, i64, i32, p, sz, p]
+        L.biloco_gemm_mxfp4_workspace_bytes.restype = st
+        L.biloco_gemm_mxfp4_workspace_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
         _lib = L
     return _lib
 
@@ -360,7 +372,8 @@ def _ext():
             raise RuntimeError("the tensor binding is missing: build it with "
                                "`python -m bit_weight_gemm_amd.build`") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                 for f in (L.biloco_kv_append, L.biloco_attn_paged, L.biloco_norm_gate_residual)))
+                 for f in (L.biloco_kv_append, L.biloco_attn_paged, L.biloco_norm_gate_residual, L.biloco_quant_mxfp4,
+                           L.biloco_dequant_mxfp4, L.biloco_gemm_mxfp4, L.biloco_gemm_mxfp4_quant)))
         _layer = m
     return _layer
 
@@ -424,3 +437,76 @@ def biloco_norm_gate_residual(x, res, pre_w, post_w=None, gate=None, res_scale: 
     if st:
         _ok(st, "biloco_norm_gate_residual")
     return res_out, h
+
+
+# ---------------------------------------------------------------- several answers to one prompt
+# Microscaled 4-bit rows are the pair codes uint8 [rows][K/2], scales uint8
+# [rows][K/32], contiguous.  Rows of x, y and out may lie apart (any row stride that
+# include/biloco.h allows).  Outputs and workspaces as above.
+
+def biloco_quant_mxfp4(x, codes=None, scales=None, stream=None):
+    """x bf16 or fp32 [M][K] -> (codes, scales)."""
+    M, K = x.shape
+    if codes is None:
+        codes = _empty((M, K // 2), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((M, K // 32), torch.uint8, x.device, stream)
+    if M == 0:      # an empty tensor has no address
+        return codes, scales
+    st = (_layer or _ext()).quant_mxfp4(x, codes, scales, *_place(stream))
+    if st:
+        _ok(st, "biloco_quant_mxfp4")
+    return codes, scales
+
+
+def biloco_dequant_mxfp4(codes, scales, out=None, out_dtype=torch.bfloat16, stream=None):
+    """The values that codes and scales stand for, [M][K] bf16 or fp32."""
+    if out is None:
+        out = _empty((codes.shape[0], 2 * codes.shape[1]), out_dtype, codes.device, stream)
+    if codes.shape[0] == 0:      # an empty tensor has no address
+        return out
+    st = (_layer or _ext()).dequant_mxfp4(codes, scales, out, *_place(stream))
+    if st:
+        _ok(st, "biloco_dequant_mxfp4")
+    return out
+
+
+def biloco_gemm_mxfp4_workspace_bytes(M: int, N: int, K: int) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().biloco_gemm_mxfp4_workspace_bytes(M, N, K, ctypes.byref(out)), "biloco_gemm_mxfp4_workspace_bytes")
+    return int(out.value)
+
+
+def _mx_workspace(M, w_codes, stream):
+    n = biloco_gemm_mxfp4_workspace_bytes(M, w_codes.shape[0], 2 * w_codes.shape[1])
+    return _empty(max(n, 16), torch.uint8, w_codes.device, stream)
+
+
+def biloco_gemm_mxfp4(a_codes, a_scales, w_codes, w_scales, y=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """y [M][N] = a w^T of two microscaled 4-bit matrices, bf16 or fp32."""
+    M = a_codes.shape[0]
+    if y is None:
+        y = _empty((M, w_codes.shape[0]), out_dtype, w_codes.device, stream)
+    if M == 0:      # an empty tensor has no address
+        return y
+    if workspace is None:
+        workspace = _mx_workspace(M, w_codes, stream)
+    st = (_layer or _ext()).gemm_mxfp4(a_codes, a_scales, w_codes, w_scales, y, workspace, *_place(stream))
+    if st:
+        _ok(st, "biloco_gemm_mxfp4")
+    return y
+
+
+def biloco_gemm_mxfp4_quant(x, w_codes, w_scales, y=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """y [M][N] = Q(x) w^T: x bf16 [M][K] is quantised first, into the workspace."""
+    M = x.shape[0]
+    if y is None:
+        y = _empty((M, w_codes.shape[0]), out_dtype, w_codes.device, stream)
+    if M == 0:      # an empty tensor has no address
+        return y
+    if workspace is None:
+        workspace = _mx_workspace(M, w_codes, stream)
+    st = (_layer or _ext()).gemm_mxfp4_quant(x, w_codes, w_scales, y, workspace, *_place(stream))
+    if st:
+        _ok(st, "biloco_gemm_mxfp4_quant")
+    return y

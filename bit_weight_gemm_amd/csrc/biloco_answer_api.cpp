@@ -1,0 +1,112 @@
+// C ABI layer of the operators for several answers to one prompt (microscaled 4-bit
+// products, attention over shared prefixes, sampling): argument checks (no HIP
+// call), dispatch.
+#include <stdint.h>
+
+#include "../../include/biloco.h"
+#include "api_checks.h"
+#include "biloco_internal.h"
+
+using namespace biloco;
+
+namespace {
+
+constexpr int32_t kMostK = 1 << 20;
+
+biloco_status check_k(int32_t K) {
+    if (K < 32 || K % 32 != 0) return BILOCO_ERR_INVALID_VALUE;
+    return K > kMostK ? BILOCO_ERR_UNSUPPORTED : BILOCO_OK;
+}
+biloco_status check_mx(int32_t M, int32_t K, const void *x, int64_t x_stride, const void *codes, const void *scales) {
+    if (M < 0) return BILOCO_ERR_INVALID_VALUE;
+    const biloco_status st = check_k(K);
+    if (st != BILOCO_OK) return st;
+    if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
+        return BILOCO_ERR_INVALID_VALUE;
+    return check_stride(x_stride, K);
+}
+Span codes_span(const void *p, int64_t rows, int64_t K) { return {p, (size_t)(rows * (K / 2))}; }
+Span scales_span(const void *p, int64_t rows, int64_t K) { return {p, (size_t)(rows * (K / 32))}; }
+
+// x: rows to quantise, or NULL for a's codes and scales.
+biloco_status gemm(const uint16_t *x, int64_t x_stride, const uint8_t *a_codes, const uint8_t *a_scales,
+                   const uint8_t *w_codes, const uint8_t *w_scales, int32_t M, int32_t N, int32_t K, void *y,
+                   int64_t y_stride, int32_t y_fp32, void *workspace, size_t workspace_bytes, bool quant,
+                   hipStream_t stream) {
+    if (M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
+    biloco_status st = check_k(K);
+    if (st != BILOCO_OK) return st;
+    if ((quant ? !x : !a_codes || !a_scales) || !w_codes || !w_scales || !y) return BILOCO_ERR_INVALID_VALUE;
+    const void *ptrs[] = {x, a_codes, a_scales, w_codes, w_scales, y, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return BILOCO_ERR_INVALID_VALUE;
+    if (quant) st = check_stride(x_stride, K);
+    if (st != BILOCO_OK) return st;
+    if (y_stride < N) return BILOCO_ERR_INVALID_VALUE;
+    if (y_stride > kMaxStride) return BILOCO_ERR_UNSUPPORTED;
+    if (M == 0) return BILOCO_OK;
+    const size_t need = mxfp4_plan_bytes(M, N, K, quant);
+    if (need > 0 && !workspace) return BILOCO_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return BILOCO_ERR_WORKSPACE_TOO_SMALL;
+    const Span out[] = {rows(y, M, y_stride, N, y_fp32 ? 4 : 2), {workspace, need}};
+    const Span in[] = {rows(x, M, x_stride, K, 2), codes_span(a_codes, M, K), scales_span(a_scales, M, K),
+                       codes_span(w_codes, N, K), scales_span(w_scales, N, K)};
+    if (overlaps(out[0], out[1])) return BILOCO_ERR_INVALID_VALUE;
+    for (const Span &o : out)
+        for (const Span &i : in)
+            if (overlaps(o, i)) return BILOCO_ERR_INVALID_VALUE;
+    const MxGemmArgs a{x, x_stride, a_codes, a_scales, w_codes, w_scales, M, N, K, y, y_stride, y_fp32 != 0, workspace};
+    return launch_gemm_mxfp4(a, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+biloco_status biloco_quant_mxfp4(const void *x, int64_t x_stride, int32_t x_fp32, int32_t M, int32_t K, uint8_t *codes,
+                                 uint8_t *scales, hipStream_t stream) {
+    const biloco_status st = check_mx(M, K, x, x_stride, codes, scales);
+    if (st != BILOCO_OK) return st;
+    const Span in = rows(x, M, x_stride, K, x_fp32 ? 4 : 2), c = codes_span(codes, M, K), s = scales_span(scales, M, K);
+    if (overlaps(in, c) || overlaps(in, s) || overlaps(c, s)) return BILOCO_ERR_INVALID_VALUE;
+    if (M == 0) return BILOCO_OK;
+    return launch_quant_mxfp4(x, x_stride, x_fp32 != 0, M, K, codes, scales, stream) == hipSuccess ? BILOCO_OK
+                                                                                                 : BILOCO_ERR_HIP;
+}
+
+biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int32_t M, int32_t K, void *out,
+                                   int64_t out_stride, int32_t out_fp32, hipStream_t stream) {
+    const biloco_status st = check_mx(M, K, out, out_stride, codes, scales);
+    if (st != BILOCO_OK) return st;
+    const Span o = rows(out, M, out_stride, K, out_fp32 ? 4 : 2);
+    if (overlaps(o, codes_span(codes, M, K)) || overlaps(o, scales_span(scales, M, K))) return BILOCO_ERR_INVALID_VALUE;
+    if (M == 0) return BILOCO_OK;
+    return launch_dequant_mxfp4(codes, scales, M, K, out, out_stride, out_fp32 != 0, stream) == hipSuccess
+               ? BILOCO_OK
+               : BILOCO_ERR_HIP;
+}
+
+biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t *bytes) {
+    if (!bytes || M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
+    const biloco_status st = check_k(K);
+    if (st != BILOCO_OK) return st;
+    *bytes = M == 0 ? 0 : mxfp4_ws_bytes(M, N, K);
+    return BILOCO_OK;
+}
+
+biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales, const uint8_t *w_codes,
+                                const uint8_t *w_scales, int32_t M, int32_t N, int32_t K, void *y, int64_t y_stride,
+                                int32_t y_fp32, void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    return gemm(nullptr, 0, a_codes, a_scales, w_codes, w_scales, M, N, K, y, y_stride, y_fp32, workspace,
+                workspace_bytes, false, stream);
+}
+
+biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const uint8_t *w_codes,
+                                      const uint8_t *w_scales, int32_t M, int32_t N, int32_t K, void *y,
+                                      int64_t y_stride, int32_t y_fp32, void *workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+    return gemm(x, x_stride, nullptr, nullptr, w_codes, w_scales, M, N, K, y, y_stride, y_fp32, workspace,
+                workspace_bytes, true, stream);
+}
+
+}  // extern "C"

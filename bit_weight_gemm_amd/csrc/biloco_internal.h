@@ -191,4 +191,24 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
 
+// ---------------------------------------------------------------- several answers to one prompt
+hipError_t launch_quant_mxfp4(const void *x, int64_t stride, bool fp32, int64_t M, int64_t K, uint8_t *codes,
+                              uint8_t *scales, hipStream_t stream);
+hipError_t launch_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K, void *out,
+                                int64_t stride, bool fp32, hipStream_t stream);
+
+struct MxGemmArgs {
+    const uint16_t *x;      // rows to quantise into the workspace, or NULL: a_codes and a_scales
+    int64_t x_stride;
+    const uint8_t *a_codes, *a_scales, *w_codes, *w_scales;
+    int M, N, K;
+    void *y;
+    int64_t y_stride;
+    bool y_fp32;
+    void *ws;
+};
+size_t mxfp4_plan_bytes(int M, int N, int K, bool quant);      // what this call uses
+size_t mxfp4_ws_bytes(int M, int N, int K);                    // what every call of up to M rows uses
+hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream);
+
 }  // namespace biloco

@@ -1,4 +1,5 @@
-// Python marshalling of the decoder-layer entry points: checks the tensors'
+// Python marshalling of the decoder-layer entry points and of those for several
+// answers to one prompt: checks the tensors'
 // types, shapes and strides and calls the C ABI with their addresses.  A
 // CPython extension because a decode step makes these calls every few
 // microseconds: an append of one token (40 heads) takes 5.2 us a call this way,
@@ -27,12 +28,22 @@ using AttnFn = Status (*)(const uint8_t *, const uint8_t *, const uint8_t *, con
 using NormFn = Status (*)(const void *, int64_t, const void *, const void *, int64_t, float, const void *, int64_t,
                           int32_t, const void *, float, float, int32_t, int32_t, void *, int64_t, void *, int64_t,
                           uint8_t *, uint8_t *, hipStream_t);
+using QuantMxFn = Status (*)(const void *, int64_t, int32_t, int32_t, int32_t, uint8_t *, uint8_t *, hipStream_t);
+using DequantMxFn = Status (*)(const uint8_t *, const uint8_t *, int32_t, int32_t, void *, int64_t, int32_t, hipStream_t);
+using GemmMxFn = Status (*)(const uint8_t *, const uint8_t *, const uint8_t *, const uint8_t *, int32_t, int32_t, int32_t,
+                            void *, int64_t, int32_t, void *, size_t, hipStream_t);
+using GemmMxQuantFn = Status (*)(const void *, int64_t, const uint8_t *, const uint8_t *, int32_t, int32_t, int32_t,
+                                 void *, int64_t, int32_t, void *, size_t, hipStream_t);
 
 namespace {
 
 AppendFn g_append;
 AttnFn g_attn;
 NormFn g_norm;
+QuantMxFn g_quant_mx;
+DequantMxFn g_dequant_mx;
+GemmMxFn g_gemm_mx;
+GemmMxQuantFn g_gemm_mx_quant;
 
 using at::Tensor;
 
@@ -261,6 +272,79 @@ Status norm(PyObject *const *a) {
                   res_out.data_ptr(), sro, h.data_ptr(), sh, pc, ps, stream(a[12]));
 }
 
+// Rows of bf16 or fp32 with any row stride.
+struct RowsOf {
+    void *p;
+    int64_t n, width, stride;
+    int32_t fp32;
+};
+RowsOf float_rows(const Tensor &t, const char *what) {
+    const auto kind = t.scalar_type();
+    if (t.dim() != 2 || (kind != at::kFloat && kind != at::kBFloat16)) refuse(what, "bf16 or fp32 [rows][columns] expected");
+    return {t.data_ptr(), t.size(0), t.size(1), row_stride(t, t.size(0), t.size(1), kind, what), kind == at::kFloat};
+}
+// Codes and scales of `rows` rows of K.
+struct MxRows {
+    const Tensor *c, *s;
+    uint8_t *codes, *scales;
+    int64_t n, K;
+};
+MxRows mx_rows(PyObject *codes, PyObject *scales, const char *what_c, const char *what_s) {
+    MxRows m{&tensor(codes, what_c), &tensor(scales, what_s), nullptr, nullptr, 0, 0};
+    if (m.c->dim() != 2) refuse(what_c, "uint8 [rows][K/2] expected");
+    m.n = m.c->size(0);
+    m.K = 2 * m.c->size(1);
+    m.codes = bytes(m.c, m.n, m.K / 2, what_c);
+    m.scales = bytes(m.s, m.n, m.K / 32, what_s);
+    return m;
+}
+const Tensor &space(PyObject *o) {
+    const Tensor &t = tensor(o, "workspace");
+    if (!t.is_contiguous()) refuse("workspace", "contiguous memory expected");
+    return t;
+}
+
+Status quant_mx(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x");
+    const RowsOf r = float_rows(x, "x");
+    const MxRows m = mx_rows(a[1], a[2], "codes", "scales");
+    if (m.n != r.n || m.K != r.width) refuse("codes", "uint8 [rows][K/2] of x's rows expected");
+    on_one_gpu(a[4], {&x, m.c, m.s});
+    return g_quant_mx(r.p, r.stride, r.fp32, size32(r.n, "x"), size32(r.width, "x"), m.codes, m.scales, stream(a[3]));
+}
+
+Status dequant_mx(PyObject *const *a) {
+    const MxRows m = mx_rows(a[0], a[1], "codes", "scales");
+    const Tensor &out = tensor(a[2], "out");
+    const RowsOf r = float_rows(out, "out");
+    if (m.n != r.n || m.K != r.width) refuse("out", "[rows][K] of the codes' rows expected");
+    on_one_gpu(a[4], {m.c, m.s, &out});
+    return g_dequant_mx(m.codes, m.scales, size32(m.n, "codes"), size32(m.K, "codes"), r.p, r.stride, r.fp32, stream(a[3]));
+}
+
+Status gemm_mx(PyObject *const *a) {
+    const MxRows x = mx_rows(a[0], a[1], "a_codes", "a_scales"), w = mx_rows(a[2], a[3], "w_codes", "w_scales");
+    const Tensor &y = tensor(a[4], "y"), &ws = space(a[5]);
+    const RowsOf r = float_rows(y, "y");
+    if (x.K != w.K) refuse("w_codes", "the rows' K expected");
+    if (r.n != x.n || r.width != w.n) refuse("y", "[rows of a][rows of w] expected");
+    on_one_gpu(a[7], {x.c, x.s, w.c, w.s, &y, &ws});
+    return g_gemm_mx(x.codes, x.scales, w.codes, w.scales, size32(x.n, "a_codes"), size32(w.n, "w_codes"),
+                     size32(w.K, "w_codes"), r.p, r.stride, r.fp32, ws.data_ptr(), ws.nbytes(), stream(a[6]));
+}
+
+Status gemm_mx_quant(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "x"), &y = tensor(a[3], "y"), &ws = space(a[4]);
+    if (x.dim() != 2) refuse("x", "bf16 [rows][K] expected");
+    const MxRows w = mx_rows(a[1], a[2], "w_codes", "w_scales");
+    const int64_t M = x.size(0), sx = row_stride(x, M, w.K, at::kBFloat16, "x");
+    const RowsOf r = float_rows(y, "y");
+    if (r.n != M || r.width != w.n) refuse("y", "[rows of x][rows of w] expected");
+    on_one_gpu(a[6], {&x, w.c, w.s, &y, &ws});
+    return g_gemm_mx_quant(x.data_ptr(), sx, w.codes, w.scales, size32(M, "x"), size32(w.n, "w_codes"),
+                           size32(w.K, "w_codes"), r.p, r.stride, r.fp32, ws.data_ptr(), ws.nbytes(), stream(a[5]));
+}
+
 // Calls f with `want` positional arguments; returns the status.
 template <Status (*F)(PyObject *const *), int WANT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -268,7 +352,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
         PyErr_Format(PyExc_TypeError, "%d arguments expected", WANT);
         return nullptr;
     }
-    if (!g_append || !g_attn || !g_norm) {
+    if (!g_append) {
         PyErr_SetString(PyExc_RuntimeError, "bind() has not been called");
         return nullptr;
     }
@@ -284,26 +368,35 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != 3) {
-        PyErr_SetString(PyExc_TypeError, "three addresses expected");
+    constexpr int kEntries = 7;
+    if (n != kEntries) {
+        PyErr_Format(PyExc_TypeError, "%d addresses expected", kEntries);
         return nullptr;
     }
-    void *p[3];
-    for (int i = 0; i < 3; ++i) {
+    void *p[kEntries];
+    for (int i = 0; i < kEntries; ++i) {
         p[i] = PyLong_AsVoidPtr(args[i]);
         if (PyErr_Occurred()) return nullptr;
     }
-    g_append = (AppendFn)p[0];
     g_attn = (AttnFn)p[1];
     g_norm = (NormFn)p[2];
+    g_quant_mx = (QuantMxFn)p[3];
+    g_dequant_mx = (DequantMxFn)p[4];
+    g_gemm_mx = (GemmMxFn)p[5];
+    g_gemm_mx_quant = (GemmMxQuantFn)p[6];
+    g_append = (AppendFn)p[0];
     Py_RETURN_NONE;
 }
 
 #define FASTCALL(f) ((PyCFunction)(void (*)(void))(f))
-PyMethodDef methods[] = {{"bind", FASTCALL(bind), METH_FASTCALL, "addresses of the three entry points"},
+PyMethodDef methods[] = {{"bind", FASTCALL(bind), METH_FASTCALL, "addresses of the entry points"},
                          {"kv_append", FASTCALL((entry<append, 15>)), METH_FASTCALL, "biloco_kv_append"},
                          {"attn_paged", FASTCALL((entry<attn, 15>)), METH_FASTCALL, "biloco_attn_paged"},
                          {"norm_gate_residual", FASTCALL((entry<norm, 14>)), METH_FASTCALL, "biloco_norm_gate_residual"},
+                         {"quant_mxfp4", FASTCALL((entry<quant_mx, 5>)), METH_FASTCALL, "biloco_quant_mxfp4"},
+                         {"dequant_mxfp4", FASTCALL((entry<dequant_mx, 5>)), METH_FASTCALL, "biloco_dequant_mxfp4"},
+                         {"gemm_mxfp4", FASTCALL((entry<gemm_mx, 8>)), METH_FASTCALL, "biloco_gemm_mxfp4"},
+                         {"gemm_mxfp4_quant", FASTCALL((entry<gemm_mx_quant, 7>)), METH_FASTCALL, "biloco_gemm_mxfp4_quant"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -463,6 +463,62 @@ biloco_status biloco_norm_gate_residual(const uint16_t *x, int64_t x_stride,
                                         int64_t res_out_stride, uint16_t *h, int64_t h_stride,
                                         uint8_t *a_codes, uint8_t *a_scales, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Several answers to one prompt: products with microscaled 4-bit weights for
+ * any number of rows, attention over a cache whose first pages sequences
+ * share, and the choice of a token from logits.  Serving only (no gradients).
+ *
+ * Microscaled 4-bit floats (OCP MXFP4): E2M1 codes, two per byte, the even k
+ * in the low nibble, and one scale byte b per 32 consecutive k that stands for
+ * 2^(b - 127); b = 255 is NaN, and so is every value of its block.
+ *   codes [rows][K/2], scales [rows][K/32], K % 32 == 0, 32 <= K <= 2^20 */
+
+/* Rows to microscaled 4-bit floats.  Per block of 32, with a = max |x|:
+ *   scale byte = max(0, floor(log2 a) + 125), 0 for a block of zeros
+ *   code = E2M1(x / 2^(byte - 127)), to nearest, ties to the even code, sign
+ *     kept; magnitudes above 6 become 6 (a's own lies in [4, 8))
+ * A block that holds a NaN or an infinity gets scale byte 255 and zero codes.
+ *   x [M][K] bf16, or fp32 if x_fp32 != 0; x_stride in elements, a multiple of
+ *     8, at least K
+ * M = 0 does nothing.  One launch.  Bit-exact. */
+biloco_status biloco_quant_mxfp4(const void *x, int64_t x_stride, int32_t x_fp32, int32_t M,
+                                 int32_t K, uint8_t *codes, uint8_t *scales, hipStream_t stream);
+
+/* The values that codes and scales stand for, as bf16 (exact while finite), or
+ * fp32 if out_fp32 != 0; magnitudes past the type's range become infinities.
+ * out_stride in elements, a multiple of 8, at least K.  M = 0 does nothing.
+ * One launch. */
+biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int32_t M,
+                                   int32_t K, void *out, int64_t out_stride, int32_t out_fp32,
+                                   hipStream_t stream);
+
+/* The product of two microscaled 4-bit matrices:
+ *   y[m][n] = sum_k a[m][k] w[n][k]
+ * in fp32, rounded once to y's type.  A NaN block of a row makes that row of y
+ * NaN, one of w that column.  Products below 2^-126 may be flushed to zero.
+ *   a_codes, a_scales: M rows; w_codes, w_scales: N rows (biloco_quant_mxfp4)
+ *   y [M][N] bf16, or fp32 if y_fp32 != 0; y_stride in elements, at least N
+ *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
+ *     not shared by calls that can run at the same time.
+ * M >= 0 (0 does nothing), N >= 1.  The result does not depend on what else
+ * runs: sums are taken in a fixed order.  One or two launches. */
+biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
+                                const uint8_t *w_codes, const uint8_t *w_scales, int32_t M,
+                                int32_t N, int32_t K, void *y, int64_t y_stride, int32_t y_fp32,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The same for rows that are quantised first, as biloco_quant_mxfp4 does:
+ * x [M][K] bf16, x_stride in elements, a multiple of 8, at least K.  The codes
+ * stay in the workspace.  One to three launches. */
+biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const uint8_t *w_codes,
+                                      const uint8_t *w_scales, int32_t M, int32_t N, int32_t K,
+                                      void *y, int64_t y_stride, int32_t y_fp32, void *workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace that the two calls above need for these sizes and for every
+ * smaller M with the same N and K (0 is possible).  No HIP call. */
+biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif
