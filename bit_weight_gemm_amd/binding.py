@@ -41,7 +41,7 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
             "biloco_gemm_lowrank_quant_noalloc", "biloco_kv_append", "biloco_attn_paged",
             "biloco_attn_workspace_bytes", "biloco_norm_gate_residual", "biloco_quant_mxfp4",
             "biloco_dequant_mxfp4", "biloco_gemm_mxfp4", "biloco_gemm_mxfp4_quant",
-            "biloco_gemm_mxfp4_workspace_bytes"]
+            "biloco_gemm_mxfp4_workspace_bytes", "biloco_sample", "biloco_sample_workspace_bytes"]
 
 # size of the device array biloco_gemm_lowrank_quant_noalloc works in
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -126,6 +126,10 @@ def lib() -> ctypes.CDLL:
         L.biloco_gemm_mxfp4_quant.argtypes = [p, i64, p, p, i32, i32, i32, p, i64, i32, p, sz, p]
         L.biloco_gemm_mxfp4_workspace_bytes.restype = st
         L.biloco_gemm_mxfp4_workspace_bytes.argtypes = [i32, i32, i32, ctypes.POINTER(sz)]
+        L.biloco_sample.restype = st
+        L.biloco_sample.argtypes = [p, i64, i32, i32, i32, p, p, p, p, p, p, p, p, sz, p]
+        L.biloco_sample_workspace_bytes.restype = st
+        L.biloco_sample_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
         _lib = L
     return _lib
 
@@ -373,7 +377,8 @@ def _ext():
                                "`python -m bit_weight_gemm_amd.build`") from e
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (L.biloco_kv_append, L.biloco_attn_paged, L.biloco_norm_gate_residual, L.biloco_quant_mxfp4,
-                           L.biloco_dequant_mxfp4, L.biloco_gemm_mxfp4, L.biloco_gemm_mxfp4_quant)))
+                           L.biloco_dequant_mxfp4, L.biloco_gemm_mxfp4, L.biloco_gemm_mxfp4_quant,
+                           L.biloco_sample)))
         _layer = m
     return _layer
 
@@ -510,3 +515,27 @@ def biloco_gemm_mxfp4_quant(x, w_codes, w_scales, y=None, out_dtype=torch.bfloat
     if st:
         _ok(st, "biloco_gemm_mxfp4_quant")
     return y
+
+
+def biloco_sample_workspace_bytes(rows: int, V: int) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().biloco_sample_workspace_bytes(rows, V, ctypes.byref(out)), "biloco_sample_workspace_bytes")
+    return int(out.value)
+
+
+def biloco_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, logprob=None,
+                  workspace=None, stream=None):
+    """A token (int32) for each row of logits bf16 or fp32 [rows][V], drawn with u fp32
+    [rows]; temperature, top_p and min_p fp32 [rows], top_k int32 [rows], or None.
+    logprob fp32 [rows] is written if given.  Rows may be one row (logits.expand)."""
+    rows, V = logits.shape
+    if token is None:
+        token = _empty((rows,), torch.int32, logits.device, stream)
+    if rows == 0:      # an empty tensor has no address
+        return token
+    if workspace is None:
+        workspace = _empty(max(biloco_sample_workspace_bytes(rows, V), 16), torch.uint8, logits.device, stream)
+    st = (_layer or _ext()).sample(logits, u, temperature, top_k, top_p, min_p, token, logprob, workspace, *_place(stream))
+    if st:
+        _ok(st, "biloco_sample")
+    return token

@@ -12,6 +12,7 @@ using namespace biloco;
 namespace {
 
 constexpr int32_t kMostK = 1 << 20;
+constexpr int32_t kMostLogits = 1 << 20;      // of weights up to 2^44, whose sums are to fit 64 bits
 
 biloco_status check_k(int32_t K) {
     if (K < 32 || K % 32 != 0) return BILOCO_ERR_INVALID_VALUE;
@@ -107,6 +108,42 @@ biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const
                                       hipStream_t stream) {
     return gemm(x, x_stride, nullptr, nullptr, w_codes, w_scales, M, N, K, y, y_stride, y_fp32, workspace,
                 workspace_bytes, true, stream);
+}
+
+biloco_status biloco_sample_workspace_bytes(int32_t rows, int32_t V, size_t *bytes) {
+    if (!bytes || rows < 0 || V < 1) return BILOCO_ERR_INVALID_VALUE;
+    if (V >= kMostLogits) return BILOCO_ERR_UNSUPPORTED;
+    *bytes = rows == 0 ? 0 : sample_ws_bytes(rows, V);
+    return BILOCO_OK;
+}
+
+biloco_status biloco_sample(const void *logits, int64_t stride, int32_t fp32, int32_t n, int32_t V,
+                            const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                            const float *u, int32_t *token, float *logprob, void *workspace, size_t workspace_bytes,
+                            hipStream_t stream) {
+    size_t need = 0;
+    const biloco_status st = biloco_sample_workspace_bytes(n, V, &need);
+    if (st != BILOCO_OK) return st;
+    if (stride < 0) return BILOCO_ERR_INVALID_VALUE;
+    if (stride > kMaxStride) return BILOCO_ERR_UNSUPPORTED;
+    if (!logits || !u || !token || (need > 0 && !workspace)) return BILOCO_ERR_INVALID_VALUE;
+    const void *ptrs[] = {logits, temperature, top_k, top_p, min_p, u, token, logprob, workspace};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return BILOCO_ERR_INVALID_VALUE;
+    if (workspace_bytes < need) return BILOCO_ERR_WORKSPACE_TOO_SMALL;
+    const size_t per_row = (size_t)n * 4;
+    const Span out[] = {{token, per_row}, {logprob, per_row}, {workspace, need}};
+    const Span in[] = {rows(logits, n, stride, V, fp32 ? 4 : 2), {temperature, per_row}, {top_k, per_row},
+                       {top_p, per_row}, {min_p, per_row}, {u, per_row}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(out[i], out[j])) return BILOCO_ERR_INVALID_VALUE;
+        for (const Span &s : in)
+            if (overlaps(out[i], s)) return BILOCO_ERR_INVALID_VALUE;
+    }
+    if (n == 0) return BILOCO_OK;
+    const SampleArgs a{logits, stride, fp32 != 0, n, V, temperature, top_k, top_p, min_p, u, token, logprob, workspace};
+    return launch_sample(a, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
 }
 
 }  // extern "C"

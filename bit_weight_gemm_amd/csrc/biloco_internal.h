@@ -211,4 +211,19 @@ size_t mxfp4_plan_bytes(int M, int N, int K, bool quant);      // what this call
 size_t mxfp4_ws_bytes(int M, int N, int K);                    // what every call of up to M rows uses
 hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream);
 
+struct SampleArgs {
+    const void *logits;
+    int64_t stride;
+    bool fp32;
+    int rows, V;
+    const float *temperature;
+    const int *top_k;
+    const float *top_p, *min_p, *u;
+    int *token;
+    float *logprob;
+    void *ws;
+};
+size_t sample_ws_bytes(int rows, int V);
+hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
+
 }  // namespace biloco

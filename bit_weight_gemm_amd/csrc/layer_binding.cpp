@@ -34,6 +34,9 @@ using GemmMxFn = Status (*)(const uint8_t *, const uint8_t *, const uint8_t *, c
                             void *, int64_t, int32_t, void *, size_t, hipStream_t);
 using GemmMxQuantFn = Status (*)(const void *, int64_t, const uint8_t *, const uint8_t *, int32_t, int32_t, int32_t,
                                  void *, int64_t, int32_t, void *, size_t, hipStream_t);
+using SampleFn = Status (*)(const void *, int64_t, int32_t, int32_t, int32_t, const float *, const int32_t *,
+                            const float *, const float *, const float *, int32_t *, float *, void *, size_t,
+                            hipStream_t);
 
 namespace {
 
@@ -44,6 +47,7 @@ QuantMxFn g_quant_mx;
 DequantMxFn g_dequant_mx;
 GemmMxFn g_gemm_mx;
 GemmMxQuantFn g_gemm_mx_quant;
+SampleFn g_sample;
 
 using at::Tensor;
 
@@ -345,6 +349,29 @@ Status gemm_mx_quant(PyObject *const *a) {
                            size32(w.K, "w_codes"), r.p, r.stride, r.fp32, ws.data_ptr(), ws.nbytes(), stream(a[5]));
 }
 
+// One number a row, or nothing.
+void *per_row(const Tensor *t, int64_t n, at::ScalarType type, const char *what) {
+    if (!t) return nullptr;
+    if (t->scalar_type() != type || !shaped(*t, n) || !t->is_contiguous())
+        refuse(what, type == at::kInt ? "contiguous int32 [rows] expected" : "contiguous fp32 [rows] expected");
+    return t->data_ptr();
+}
+
+Status sample(PyObject *const *a) {
+    const Tensor &x = tensor(a[0], "logits"), &u = tensor(a[1], "u"), &token = tensor(a[6], "token"), &ws = space(a[8]);
+    const RowsOf r = float_rows(x, "logits");
+    const Tensor *t = maybe(a[2], "temperature"), *k = maybe(a[3], "top_k"), *p = maybe(a[4], "top_p"),
+                 *m = maybe(a[5], "min_p"), *lp = maybe(a[7], "logprob");
+    const void *pu = per_row(&u, r.n, at::kFloat, "u"), *pt = per_row(t, r.n, at::kFloat, "temperature"),
+               *pk = per_row(k, r.n, at::kInt, "top_k"), *pp = per_row(p, r.n, at::kFloat, "top_p"),
+               *pm = per_row(m, r.n, at::kFloat, "min_p");
+    void *out = per_row(&token, r.n, at::kInt, "token"), *plp = per_row(lp, r.n, at::kFloat, "logprob");
+    on_one_gpu(a[10], {&x, &u, t, k, p, m, &token, lp, &ws});
+    return g_sample(r.p, r.stride, r.fp32, size32(r.n, "logits"), size32(r.width, "logits"), (const float *)pt,
+                    (const int32_t *)pk, (const float *)pp, (const float *)pm, (const float *)pu, (int32_t *)out,
+                    (float *)plp, ws.data_ptr(), ws.nbytes(), stream(a[9]));
+}
+
 // Calls f with `want` positional arguments; returns the status.
 template <Status (*F)(PyObject *const *), int WANT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -368,7 +395,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    constexpr int kEntries = 7;
+    constexpr int kEntries = 8;
     if (n != kEntries) {
         PyErr_Format(PyExc_TypeError, "%d addresses expected", kEntries);
         return nullptr;
@@ -384,6 +411,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     g_dequant_mx = (DequantMxFn)p[4];
     g_gemm_mx = (GemmMxFn)p[5];
     g_gemm_mx_quant = (GemmMxQuantFn)p[6];
+    g_sample = (SampleFn)p[7];
     g_append = (AppendFn)p[0];
     Py_RETURN_NONE;
 }
@@ -397,6 +425,7 @@ PyMethodDef methods[] = {{"bind", FASTCALL(bind), METH_FASTCALL, "addresses of t
                          {"dequant_mxfp4", FASTCALL((entry<dequant_mx, 5>)), METH_FASTCALL, "biloco_dequant_mxfp4"},
                          {"gemm_mxfp4", FASTCALL((entry<gemm_mx, 8>)), METH_FASTCALL, "biloco_gemm_mxfp4"},
                          {"gemm_mxfp4_quant", FASTCALL((entry<gemm_mx_quant, 7>)), METH_FASTCALL, "biloco_gemm_mxfp4_quant"},
+                         {"sample", FASTCALL((entry<sample, 11>)), METH_FASTCALL, "biloco_sample"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

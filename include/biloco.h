@@ -519,6 +519,40 @@ biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const
  * smaller M with the same N and K (0 is possible).  No HIP call. */
 biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t *bytes);
 
+/* A token for each of `rows` rows of V logits x, drawn with a given number u of
+ * [0, 1).  For a row with temperature T, top_k k, top_p p and min_p m:
+ *   w_i = exp((x_i - max x) / T), in steps of 2^-44
+ *   order: x descending, equal ones by index
+ *   kept: the first k in that order (k < 1: all); of these the fewest first ones
+ *     whose w sum to at least p of all theirs (p >= 1: all); of these the ones
+ *     with w_i >= m (m <= 0: all).  The first in that order is always kept.
+ *   token: the smallest kept i at which the sum of kept w_j, j <= i, passes u
+ *     times their sum over the row (u >= 1: the last kept one with w_i > 0)
+ *   logprob: log of w_i over the sum of w over the whole row
+ * T <= 0: the first in that order (the greedy choice), logprob at T = 1.  NaN
+ * logits count as -inf, which is never chosen; a row of nothing else gives
+ * token -1 and logprob -inf.  Where some logits are +inf only they have weight.
+ * NaN parameters: T as 0, p as 1, m as 0, u as 0.
+ * Weights are 64-bit whole numbers: the token does not depend on the order in which
+ * sums are taken, and the order's borders are exact.
+ *   logits bf16, or fp32 if fp32 != 0; row r begins stride * r elements on
+ *     (any stride >= 0; 0: every row is the same)
+ *   temperature, top_p, min_p fp32 [rows], top_k int32 [rows], or NULL: T = 1,
+ *     no cut
+ *   u fp32 [rows]; token int32 [rows]; logprob fp32 [rows] or NULL
+ *   workspace: >= biloco_sample_workspace_bytes(...) bytes, no fill needed; not
+ *     shared by calls that can run at the same time.
+ * 1 <= V < 2^20.  rows = 0 does nothing.  One to three launches. */
+biloco_status biloco_sample(const void *logits, int64_t stride, int32_t fp32, int32_t rows,
+                            int32_t V, const float *temperature, const int32_t *top_k,
+                            const float *top_p, const float *min_p, const float *u,
+                            int32_t *token, float *logprob, void *workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace biloco_sample needs for these sizes and for every smaller
+ * number of rows with the same V (0 is possible).  No HIP call. */
+biloco_status biloco_sample_workspace_bytes(int32_t rows, int32_t V, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

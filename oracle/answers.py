@@ -39,3 +39,42 @@ def gemm_mxfp4(a, w):
     """a and w: (codes, scales).  y, and the sums of the terms' magnitudes."""
     a, w = values_mxfp4(*a), values_mxfp4(*w)
     return a @ w.T, np.abs(a) @ np.abs(w).T
+
+
+def sample(x, u, t=1.0, k=0, p=1.0, m=0.0):
+    """One row: (token, log-probability, how near the nearest other outcome is, as a share of the sums compared)."""
+    x = np.asarray(x, np.float64)
+    x = np.where(np.isnan(x), -np.inf, x)
+    t, p, m, u = (off if np.isnan(v) else v for v, off in ((t, 0.0), (p, 1.0), (m, 0.0), (u, 0.0)))
+    top = x.max()
+    if top == -np.inf:
+        return -1, -np.inf, 1.0
+    if t <= 0:
+        t, k, p, m = 1.0, 1, 1.0, 0.0
+    with np.errstate(invalid="ignore", over="ignore"):
+        d = np.where(x == top, 0.0, (x - top) / t)
+    d = np.where(np.isnan(d), -np.inf, d)
+    w = np.exp(d)
+    order = np.argsort(-x, kind="stable")
+    near = 1.0
+    if 0 < k < len(x):
+        order = order[:k]
+    if p < 1:
+        upto = np.cumsum(w[order])
+        target = p * upto[-1]
+        order = order[:max(1, int(np.searchsorted(upto, target, side="left")) + 1)]
+        near = min(near, np.abs(upto - target).min() / upto[-1])
+    if m > 0:
+        keep = w[order] >= min(m, 1.0)
+        near = min(near, np.abs(w[order] - min(m, 1.0))[w[order] != 1.0].min(initial=1.0))
+        order = order[keep]
+    ids = np.sort(order)
+    upto = np.cumsum(w[ids])
+    target = max(u, 0.0) * upto[-1]
+    at = int(np.searchsorted(upto, target, side="right"))
+    if at >= len(ids):
+        at = int(np.nonzero(w[ids] > 2.0 ** -45)[0][-1])
+    else:
+        near = min(near, np.abs(upto - target).min() / upto[-1])
+    token = int(ids[at])
+    return token, d[token] - np.log(w.sum()), near
