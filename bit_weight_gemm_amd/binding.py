@@ -41,7 +41,8 @@ EXPORTED = ["biloco_status_string", "biloco_pack_signs", "biloco_quant_act_fp4",
             "biloco_gemm_lowrank_quant_noalloc", "biloco_kv_append", "biloco_attn_paged",
             "biloco_attn_workspace_bytes", "biloco_norm_gate_residual", "biloco_quant_mxfp4",
             "biloco_dequant_mxfp4", "biloco_gemm_mxfp4", "biloco_gemm_mxfp4_quant",
-            "biloco_gemm_mxfp4_workspace_bytes", "biloco_sample", "biloco_sample_workspace_bytes"]
+            "biloco_gemm_mxfp4_workspace_bytes", "biloco_sample", "biloco_sample_workspace_bytes",
+            "biloco_attn_shared", "biloco_attn_shared_workspace_bytes"]
 
 # size of the device array biloco_gemm_lowrank_quant_noalloc works in
 BILOCO_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -130,6 +131,11 @@ def lib() -> ctypes.CDLL:
         L.biloco_sample.argtypes = [p, i64, i32, i32, i32, p, p, p, p, p, p, p, p, sz, p]
         L.biloco_sample_workspace_bytes.restype = st
         L.biloco_sample_workspace_bytes.argtypes = [i32, i32, ctypes.POINTER(sz)]
+        L.biloco_attn_shared.restype = st
+        L.biloco_attn_shared.argtypes = cache + [p, i64, i32] + ragged + [i32, p, p, i32, i32, f32, i32, i32, p, i64, p,
+                                                                          p, sz, p]
+        L.biloco_attn_shared_workspace_bytes.restype = st
+        L.biloco_attn_shared_workspace_bytes.argtypes = [i32] * 9 + [ctypes.POINTER(sz)]
         _lib = L
     return _lib
 
@@ -378,7 +384,7 @@ def _ext():
         m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
                  for f in (L.biloco_kv_append, L.biloco_attn_paged, L.biloco_norm_gate_residual, L.biloco_quant_mxfp4,
                            L.biloco_dequant_mxfp4, L.biloco_gemm_mxfp4, L.biloco_gemm_mxfp4_quant,
-                           L.biloco_sample)))
+                           L.biloco_sample, L.biloco_attn_shared)))
         _layer = m
     return _layer
 
@@ -515,6 +521,37 @@ def biloco_gemm_mxfp4_quant(x, w_codes, w_scales, y=None, out_dtype=torch.bfloat
     if st:
         _ok(st, "biloco_gemm_mxfp4_quant")
     return y
+
+
+def biloco_attn_shared_workspace_bytes(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int, max_q_len: int,
+                                       max_kv_len: int, n_groups: int, max_shared_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _ok(lib().biloco_attn_shared_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, n_groups,
+                                                 max_shared_len, ctypes.byref(out)),
+        "biloco_attn_shared_workspace_bytes")
+    return int(out.value)
+
+
+def biloco_attn_shared(cache, q, q_start, kv_len, block_table, group_start, shared_len, max_q_len: int, max_kv_len: int,
+                       max_shared_len: int, scale: float, window: int = 0, sinks: int = 0, out=None, lse=None,
+                       workspace=None, stream=None):
+    """biloco_attn_paged where the sequences group_start[g] .. group_start[g+1] - 1 share
+    their first shared_len[g] tokens, read through the first one's table; returns out."""
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    if q.shape[0] == 0:      # an empty tensor has no address
+        return out
+    if workspace is None:
+        _, kv_heads, _, dim = cache[0].shape
+        n = biloco_attn_shared_workspace_bytes(kv_len.shape[0], q.shape[0], q.shape[1], kv_heads, dim, max_q_len, max_kv_len,
+                                               shared_len.shape[0], max_shared_len)
+        workspace = _empty(max(n, 16), torch.uint8, q.device, stream)
+    st = (_layer or _ext()).attn_shared(cache, q, q_start, kv_len, block_table, group_start, shared_len, max_q_len,
+                                        max_kv_len, max_shared_len, scale, window, sinks, out, lse, workspace,
+                                        *_place(stream))
+    if st:
+        _ok(st, "biloco_attn_shared")
+    return out
 
 
 def biloco_sample_workspace_bytes(rows: int, V: int) -> int:

@@ -1,8 +1,12 @@
 // Argument checks that the C ABI's layers share (host only, no HIP call).
 #pragma once
+#include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/biloco.h"
+#include "biloco_internal.h"
 
 namespace biloco {
 namespace {
@@ -60,6 +64,51 @@ constexpr int64_t kMostTokens = (int64_t)1 << 30;
 inline biloco_status check_batch(int32_t B, int32_t T, int32_t max_q_len, int32_t max_pages, int32_t page_size) {
     if (B < 0 || T < 0 || max_q_len < 1 || max_pages < 1) return BILOCO_ERR_INVALID_VALUE;
     if (B > 65535 || (int64_t)max_pages * page_size > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
+    return BILOCO_OK;
+}
+
+// The sizes that shape attention's launches.
+inline biloco_status check_attn_sizes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                      int32_t max_q_len, int32_t max_kv_len) {
+    if (max_kv_len < 0 || q_heads < 1) return BILOCO_ERR_INVALID_VALUE;
+    if (max_kv_len > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
+    biloco_status st = check_cache(1, kv_heads, 16, head_dim);
+    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, 1, 1);
+    if (st != BILOCO_OK) return st;
+    if (q_heads % kv_heads != 0) return BILOCO_ERR_INVALID_VALUE;
+    if (q_heads > 4096 || (int64_t)T * q_heads > INT32_MAX) return BILOCO_ERR_UNSUPPORTED;
+    return BILOCO_OK;
+}
+
+// Everything else about a call of attention; `more`: arrays that a kind of it reads besides.
+inline biloco_status check_attn(const AttnArgs &a, size_t need, size_t workspace_bytes, std::initializer_list<Span> more) {
+    if (!(a.scale > 0.0f) || !isfinite(a.scale) || a.window < 0 || a.sinks < 0) return BILOCO_ERR_INVALID_VALUE;
+    if (a.window > kMostTokens || a.sinks > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
+    const void *needed[] = {a.kc, a.vc, a.ks, a.vs, a.q, a.q_start, a.kv_len, a.table, a.o};
+    for (const void *p : needed)
+        if (!p || !aligned16(p)) return BILOCO_ERR_INVALID_VALUE;
+    for (const Span &s : more)
+        if (!s.p || !aligned16(s.p)) return BILOCO_ERR_INVALID_VALUE;
+    if ((need > 0 && !a.ws) || !aligned16(a.lse) || !aligned16(a.ws)) return BILOCO_ERR_INVALID_VALUE;
+    const int64_t qw = (int64_t)a.q_heads * a.dim;
+    biloco_status st = check_stride(a.q_stride, qw);
+    if (st == BILOCO_OK) st = check_stride(a.o_stride, qw);
+    if (st != BILOCO_OK) return st;
+    if (workspace_bytes < need) return BILOCO_ERR_WORKSPACE_TOO_SMALL;
+    const size_t cache = (size_t)a.num_pages * a.kv_heads * a.page * a.dim;
+    const size_t nscale = (size_t)a.num_pages * a.kv_heads;
+    const Span out[] = {rows(a.o, a.T, a.o_stride, qw, 2), {a.lse, (size_t)a.T * a.q_heads * 4}, {a.ws, need}};
+    const Span in[] = {{a.kc, cache}, {a.vc, cache}, {a.ks, nscale}, {a.vs, nscale},
+                       rows(a.q, a.T, a.q_stride, qw, 2), {a.q_start, (size_t)(a.B + 1) * 4},
+                       {a.kv_len, (size_t)a.B * 4}, {a.table, (size_t)a.B * a.max_pages * 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(out[i], out[j])) return BILOCO_ERR_INVALID_VALUE;
+        for (const Span &s : in)
+            if (overlaps(out[i], s)) return BILOCO_ERR_INVALID_VALUE;
+        for (const Span &s : more)
+            if (overlaps(out[i], s)) return BILOCO_ERR_INVALID_VALUE;
+    }
     return BILOCO_OK;
 }
 

@@ -40,39 +40,58 @@ __device__ __forceinline__ float exp2a(float x) { return __builtin_amdgcn_exp2f(
 constexpr int kMostRows = 64;
 enum { kAllSeqs = 0, kFewRows = 1, kManyRows = 2 };
 
+// Attention over tokens [from, upto) of the sequences only.
+struct PartArgs : AttnArgs {
+    int from, upto;
+    __host__ __device__ PartArgs(const AttnArgs &a, int from_, int upto_) : AttnArgs(a), from(from_), upto(upto_) {}
+};
+__device__ __forceinline__ int from_of(const AttnArgs &) { return 0; }
+__device__ __forceinline__ int from_of(const PartArgs &a) { return a.from; }
+__device__ __forceinline__ int upto_of(const AttnArgs &, int hi) { return hi; }
+__device__ __forceinline__ int upto_of(const PartArgs &a, int hi) { return min(hi, a.upto); }
+__device__ __forceinline__ bool holds(const AttnArgs &, int) { return true; }
+__device__ __forceinline__ bool holds(const PartArgs &a, int j) { return (bool)((j >= a.from) & (j < a.upto)); }
+
 // The chunks of 64 tokens that the rows at positions [p_min, p_max] need:
 // `ns` chunks of first tokens, then those from `lo0` on.
 struct Span64 {
-    int lo0, ns, nc;
-    __device__ __forceinline__ int start(int c) const { return c < ns ? c * kChunk : lo0 + (c - ns) * kChunk; }
+    int s0, lo0, ns, nc;
+    __device__ __forceinline__ int start(int c) const { return c < ns ? s0 + c * kChunk : lo0 + (c - ns) * kChunk; }
 };
-__device__ __forceinline__ Span64 span_of(const AttnArgs &a, int p_min, int p_max) {
+template <class A>
+__device__ __forceinline__ Span64 span_of(const A &a, int p_min, int p_max) {
     Span64 s;
-    const int lo = a.window > 0 ? max(p_min - a.window + 1, 0) : 0;
+    const int lo = max(a.window > 0 ? max(p_min - a.window + 1, 0) : 0, from_of(a));
+    s.s0 = from_of(a) & ~(kChunk - 1);
     s.lo0 = lo & ~(kChunk - 1);
-    s.ns = (min(a.sinks, s.lo0) + kChunk - 1) / kChunk;
-    s.nc = s.ns + (max(p_max + 1 - s.lo0, 0) + kChunk - 1) / kChunk;
+    s.ns = max(upto_of(a, min(a.sinks, s.lo0)) - s.s0 + kChunk - 1, 0) / kChunk;
+    s.nc = s.ns + (max(upto_of(a, p_max + 1) - s.lo0, 0) + kChunk - 1) / kChunk;
     return s;
 }
 // What a row at position pos sees; lo = low_of(pos).  No branches.
 __device__ __forceinline__ int low_of(const AttnArgs &a, int pos) { return a.window > 0 ? pos - a.window + 1 : 0; }
-__device__ __forceinline__ bool sees(const AttnArgs &a, int pos, int lo, int j) {
-    return (bool)((j <= pos) & ((j >= lo) | (j < a.sinks)));
+template <class A>
+__device__ __forceinline__ bool sees(const A &a, int pos, int lo, int j) {
+    return (bool)((j <= pos) & ((j >= lo) | (j < a.sinks)) & holds(a, j));
 }
 // Bit j: some row at a position of [p_min, p_max] sees token t0 + j.
-__device__ __forceinline__ uint32_t any_sees8(const AttnArgs &a, int p_min, int p_max, int t0) {
+template <class A>
+__device__ __forceinline__ uint32_t any_sees8(const A &a, int p_min, int p_max, int t0) {
     const int lo = low_of(a, p_min);
     uint32_t bits = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) bits |= (uint32_t)sees(a, p_max, lo, t0 + j) << j;
     return bits;
 }
-__device__ __forceinline__ uint32_t sees8(const AttnArgs &a, int pos, int t0) {
+template <class A>
+__device__ __forceinline__ uint32_t sees8(const A &a, int pos, int t0) {
     return any_sees8(a, pos, pos, t0);
 }
 // Every row at a position of [p_min, p_max] sees all of the chunk at j0.
-__device__ __forceinline__ bool all_see(const AttnArgs &a, int p_min, int p_max, int j0) {
-    return j0 + kChunk - 1 <= p_min && (a.window == 0 || p_max - j0 < a.window || j0 + kChunk <= a.sinks);
+template <class A>
+__device__ __forceinline__ bool all_see(const A &a, int p_min, int p_max, int j0) {
+    return j0 + kChunk - 1 <= p_min && (a.window == 0 || p_max - j0 < a.window || j0 + kChunk <= a.sinks) && holds(a, j0) &&
+           holds(a, j0 + kChunk - 1);
 }
 constexpr uint32_t kOnes = 0x38383838u;      // the code of 1, four times
 // 0xFF for each NaN code (0x7F or 0xFF), else 0x00.
@@ -98,7 +117,8 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int stop, int kv_len, int which) {
+template <class A>
+__device__ __forceinline__ Seq seq_from(const A &a, int start, int stop, int kv_len, int which) {
     Seq s;
     s.first = min(max(start, 0), a.T);
     s.n = min(max(stop, s.first), a.T) - s.first;

@@ -110,6 +110,42 @@ biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const
                 workspace_bytes, true, stream);
 }
 
+biloco_status biloco_attn_shared_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
+                                                 int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
+                                                 int32_t n_groups, int32_t max_shared_len, size_t *bytes) {
+    if (!bytes || n_groups < 1 || max_shared_len < 0) return BILOCO_ERR_INVALID_VALUE;
+    if (n_groups > 65535 || max_shared_len > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
+    const biloco_status st = check_attn_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
+    if (st != BILOCO_OK) return st;
+    *bytes = attn_shared_ws_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, n_groups, max_shared_len);
+    return BILOCO_OK;
+}
+
+biloco_status biloco_attn_shared(const uint8_t *k_codes, const uint8_t *v_codes, const uint8_t *k_scales,
+                                 const uint8_t *v_scales, int32_t num_pages, int32_t kv_heads, int32_t page_size,
+                                 int32_t head_dim, const uint16_t *q, int64_t q_stride, int32_t q_heads,
+                                 const int32_t *q_start, const int32_t *kv_len, const int32_t *block_table,
+                                 int32_t max_pages, int32_t B, int32_t T, int32_t max_q_len, int32_t max_kv_len,
+                                 const int32_t *group_start, const int32_t *shared_len, int32_t n_groups,
+                                 int32_t max_shared_len, float scale, int32_t window, int32_t sinks, uint16_t *o,
+                                 int64_t o_stride, float *lse, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+    size_t need = 0;
+    biloco_status st = check_cache(num_pages, kv_heads, page_size, head_dim);
+    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, max_pages, page_size);
+    if (st == BILOCO_OK)
+        st = biloco_attn_shared_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, n_groups,
+                                                max_shared_len, &need);
+    if (st != BILOCO_OK) return st;
+    const AttnArgs a{k_codes, v_codes, k_scales, v_scales, num_pages, kv_heads, page_size, head_dim,
+                     q, q_stride, q_heads, q_start, kv_len, block_table, max_pages, B, T,
+                     max_q_len, max_kv_len, scale, window, sinks, o, o_stride, lse, workspace};
+    st = check_attn(a, need, workspace_bytes, {{group_start, (size_t)(n_groups + 1) * 4}, {shared_len, (size_t)n_groups * 4}});
+    if (st != BILOCO_OK || B == 0 || T == 0) return st;
+    const SharedAttnArgs s{group_start, shared_len, n_groups, max_shared_len, nullptr, nullptr};
+    return launch_attn_shared(a, s, workspace_bytes, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
+}
+
 biloco_status biloco_sample_workspace_bytes(int32_t rows, int32_t V, size_t *bytes) {
     if (!bytes || rows < 0 || V < 1) return BILOCO_ERR_INVALID_VALUE;
     if (V >= kMostLogits) return BILOCO_ERR_UNSUPPORTED;

@@ -226,4 +226,14 @@ struct SampleArgs {
 size_t sample_ws_bytes(int rows, int V);
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream);
 
+// What attention over shared first tokens takes beyond AttnArgs.
+struct SharedAttnArgs {
+    const int *group_start, *shared_len;
+    int groups, max_shared;
+    void *tables, *parts;      // in the workspace
+};
+size_t attn_shared_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups,
+                            int max_shared);
+hipError_t launch_attn_shared(const AttnArgs &a, const SharedAttnArgs &s, size_t ws_bytes, hipStream_t stream);
+
 }  // namespace biloco

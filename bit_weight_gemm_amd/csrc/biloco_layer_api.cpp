@@ -91,13 +91,9 @@ biloco_status biloco_kv_append(uint8_t *k_codes, uint8_t *v_codes, uint8_t *k_sc
 biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads, int32_t kv_heads,
                                           int32_t head_dim, int32_t max_q_len, int32_t max_kv_len,
                                           size_t *bytes) {
-    if (!bytes || max_kv_len < 0 || q_heads < 1) return BILOCO_ERR_INVALID_VALUE;
-    if (max_kv_len > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
-    biloco_status st = check_cache(1, kv_heads, 16, head_dim);
-    if (st == BILOCO_OK) st = check_batch(B, T, max_q_len, 1, 1);
+    if (!bytes) return BILOCO_ERR_INVALID_VALUE;
+    const biloco_status st = check_attn_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
     if (st != BILOCO_OK) return st;
-    if (q_heads % kv_heads != 0) return BILOCO_ERR_INVALID_VALUE;
-    if (q_heads > 4096 || (int64_t)T * q_heads > INT32_MAX) return BILOCO_ERR_UNSUPPORTED;
     *bytes = attn_ws_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
     return BILOCO_OK;
 }
@@ -118,38 +114,11 @@ biloco_status biloco_attn_paged(const uint8_t *k_codes, const uint8_t *v_codes,
         st = biloco_attn_workspace_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len,
                                          &need);
     if (st != BILOCO_OK) return st;
-    if (!(scale > 0.0f) || !isfinite(scale) || window < 0 || sinks < 0)
-        return BILOCO_ERR_INVALID_VALUE;
-    if (window > kMostTokens || sinks > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
-    if (!k_codes || !v_codes || !k_scales || !v_scales || !q || !q_start || !kv_len ||
-        !block_table || !o || (need > 0 && !workspace))
-        return BILOCO_ERR_INVALID_VALUE;
-    const void *ptrs[] = {k_codes, v_codes, k_scales, v_scales, q, q_start, kv_len, block_table,
-                          o, lse, workspace};
-    for (const void *p : ptrs)
-        if (p && !aligned16(p)) return BILOCO_ERR_INVALID_VALUE;
-    const int64_t qw = (int64_t)q_heads * head_dim;
-    st = check_stride(q_stride, qw);
-    if (st == BILOCO_OK) st = check_stride(o_stride, qw);
-    if (st != BILOCO_OK) return st;
-    if (workspace_bytes < need) return BILOCO_ERR_WORKSPACE_TOO_SMALL;
-    const size_t cache = (size_t)num_pages * kv_heads * page_size * head_dim;
-    const size_t nscale = (size_t)num_pages * kv_heads;
-    const Span out[] = {rows(o, T, o_stride, qw, 2), {lse, (size_t)T * q_heads * 4},
-                        {workspace, need}};
-    const Span in[] = {{k_codes, cache}, {v_codes, cache}, {k_scales, nscale}, {v_scales, nscale},
-                       rows(q, T, q_stride, qw, 2), {q_start, (size_t)(B + 1) * 4},
-                       {kv_len, (size_t)B * 4}, {block_table, (size_t)B * max_pages * 4}};
-    for (int i = 0; i < 3; ++i) {
-        for (int j = i + 1; j < 3; ++j)
-            if (overlaps(out[i], out[j])) return BILOCO_ERR_INVALID_VALUE;
-        for (const Span &s : in)
-            if (overlaps(out[i], s)) return BILOCO_ERR_INVALID_VALUE;
-    }
-    if (B == 0 || T == 0) return BILOCO_OK;
     const AttnArgs a{k_codes, v_codes, k_scales, v_scales, num_pages, kv_heads, page_size, head_dim,
                      q, q_stride, q_heads, q_start, kv_len, block_table, max_pages, B, T,
                      max_q_len, max_kv_len, scale, window, sinks, o, o_stride, lse, workspace};
+    st = check_attn(a, need, workspace_bytes, {});
+    if (st != BILOCO_OK || B == 0 || T == 0) return st;
     return launch_attn(a, workspace_bytes, stream) == hipSuccess ? BILOCO_OK : BILOCO_ERR_HIP;
 }
 

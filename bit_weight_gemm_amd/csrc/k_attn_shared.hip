@@ -1,0 +1,338 @@
+// Attention over the paged 8-bit cache for a batch whose sequences share their first
+// tokens in groups.
+//
+// A row's softmax over all its tokens is joined from two parts, o = sum_i e^(m_i - m) o_i
+// over the same of l_i: the group's shared tokens, and the sequence's own ones.
+//   shared  a workgroup takes 128 rows of a group (rows of several sequences) and walks
+//           the shared tokens' chunks as the kernel for many rows does, so that a
+//           shared token is read and made wide once for 128 rows, not once a sequence
+//   own     the kernel for few rows, from the first own token on
+// A row's position is its own sequence's, so that masks by position (causality, window,
+// first tokens) hold in both parts.  Sequences of more than kMostRows rows fill tiles by
+// themselves and share nothing: the kernel for many rows takes them whole.
+#include "attn_rows.h"
+#include "attn_tiles.h"
+
+namespace biloco {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kWantItems = 512;      // workgroups that fill the chip (two a CU)
+
+// Where the sequences' rows lie in the groups' tiles; made by one workgroup first.
+struct Tables {
+    int *before;      // [B + 1] new tokens of the sequences before (of few rows)
+    int *tile;        // [groups + 1] tiles of the groups before
+    int *from;        // [B] the first own token
+    int *row;         // [B] the first row among the tiles' rows, or -1: nothing is shared
+};
+__host__ __device__ __forceinline__ size_t table_ints(int64_t B, int64_t groups) {
+    return (size_t)((3 * B + groups + 2 + 3) / 4 * 4);
+}
+__device__ __forceinline__ Tables tables_of(const SharedAttnArgs &s, int B) {
+    Tables t;
+    t.before = static_cast<int *>(s.tables);
+    t.tile = t.before + B + 1;
+    t.from = t.tile + s.groups + 1;
+    t.row = t.from + B;
+    return t;
+}
+
+struct Group {
+    int b0, b1, upto;      // its sequences, its shared tokens
+};
+__device__ __forceinline__ Group group_at(const AttnArgs &a, const SharedAttnArgs &s, int g) {
+    Group x;
+    x.b0 = min(max(s.group_start[g], 0), a.B);
+    x.b1 = min(max(s.group_start[g + 1], x.b0), a.B);
+    x.upto = (int)min((int64_t)max(s.shared_len[g], 0), (int64_t)a.max_pages * a.page);
+    return x;
+}
+
+constexpr int kTableThreads = 1024;
+// Exclusive sums over the workgroup; all: the sum.
+__device__ __forceinline__ int sums_before(int v, int (&tmp)[kTableThreads / 64], int &all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int in = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int t = __shfl_up(in, o, 64);
+        if (lane >= o) in += t;
+    }
+    __syncthreads();
+    if (lane == 63) tmp[wave] = in;
+    __syncthreads();
+    int b = in - v;
+    all = 0;
+    for (int i = 0; i < kTableThreads / 64; ++i) {
+        if (i < wave) b += tmp[i];
+        all += tmp[i];
+    }
+    return b;
+}
+
+__global__ void __launch_bounds__(kTableThreads)
+attn_shared_tables_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int tiles) {
+    __shared__ int tmp[kTableThreads / 64];
+    const Tables t = tables_of(s, a.B);
+    const int G = a.q_heads / a.kv_heads;
+    int carry = 0, all;
+    for (int at = 0; at < a.B; at += kTableThreads) {
+        const int b = at + threadIdx.x, n = b < a.B ? seq_of(a, b, which).n : 0;
+        const int mine = carry + sums_before(n, tmp, all);
+        if (b < a.B) t.before[b] = mine;
+        carry += all;
+    }
+    if (threadIdx.x == 0) t.before[a.B] = carry;
+    __threadfence_block();
+    __syncthreads();
+    carry = 0;
+    for (int at = 0; at < s.groups; at += kTableThreads) {
+        const int g = at + threadIdx.x;
+        int n = 0;
+        if (g < s.groups) {
+            const Group x = group_at(a, s, g);
+            const int64_t rows = (int64_t)(t.before[x.b1] - t.before[x.b0]) * G;
+            n = x.upto > 0 ? (int)min((rows + kTileRows - 1) / kTileRows, (int64_t)tiles) : 0;
+        }
+        const int mine = min(carry + sums_before(n, tmp, all), tiles);
+        if (g < s.groups) t.tile[g] = mine;
+        carry = min(carry + all, tiles);
+    }
+    if (threadIdx.x == 0) t.tile[s.groups] = carry;
+    __threadfence_block();
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.B; b += kTableThreads) {
+        int lo = 0, hi = s.groups - 1;      // the last group that begins at or before b
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (s.group_start[mid] <= b) lo = mid;
+            else hi = mid - 1;
+        }
+        const Group x = group_at(a, s, lo);
+        const int64_t row = (int64_t)t.tile[lo] * kTileRows + (int64_t)(t.before[b] - t.before[x.b0]) * G;
+        const int64_t end = row + (int64_t)(t.before[b + 1] - t.before[b]) * G;
+        const bool in = x.upto > 0 && b >= x.b0 && b < x.b1 && end <= (int64_t)t.tile[lo + 1] * kTileRows;
+        t.from[b] = in ? x.upto : 0;
+        t.row[b] = in ? (int)row : -1;
+    }
+}
+
+template <int D>
+__device__ __forceinline__ float *shared_part(const SharedAttnArgs &s, int64_t item, int splits, int split) {
+    return static_cast<float *>(s.parts) + (item * splits + split) * kTileRows * (D + 2);
+}
+
+// Rows of a tile: the token and position of each.
+struct TileRows {
+    int token[kTileRows], pos[kTileRows];
+};
+
+template <int D>
+__global__ void __launch_bounds__(256, 2)
+attn_shared_tiles_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int splits) {
+    __shared__ TileLds<D> lds;
+    __shared__ TileRows rows_of_tile;
+    const Tables t = tables_of(s, a.B);
+    const int h = (int)(blockIdx.x % a.kv_heads), rest = (int)(blockIdx.x / a.kv_heads);
+    const int split = rest % splits, at = rest / splits;
+    if (at >= scalar_load(t.tile + s.groups)) return;
+    int g = 0, last_g = s.groups - 1;      // the last group whose tiles begin at or before this one
+    while (g < last_g) {
+        const int mid = (g + last_g + 1) / 2;
+        if (scalar_load(t.tile + mid) <= at) g = mid;
+        else last_g = mid - 1;
+    }
+    const Group x = group_at(a, s, g);
+    const int G = a.q_heads / a.kv_heads, r0 = (at - scalar_load(t.tile + g)) * kTileRows;
+    const int first = scalar_load(t.before + x.b0), rows = (scalar_load(t.before + x.b1) - first) * G;
+    const int valid = min(rows - r0, kTileRows);
+    for (int b = x.b0 + threadIdx.x; b < x.b1; b += 256) {
+        const Seq q = seq_of(a, b, which);
+        const int at0 = (t.before[b] - first) * G - r0;      // row of its first row in the tile
+        for (int r = max(at0, 0); r < min(at0 + q.n * G, kTileRows); ++r) {
+            const int i = (r - at0) / G;
+            rows_of_tile.token[r] = q.first + i;
+            rows_of_tile.pos[r] = q.past + i;
+        }
+    }
+    __syncthreads();
+    const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+    const auto lowest = [](int v) {
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
+        return uniform(v);
+    };
+    const int p0 = rows_of_tile.pos[min(lane, valid - 1)], p1 = rows_of_tile.pos[min(lane + 64, valid - 1)];
+    const int p_min = lowest(min(p0, p1)), p_max = -lowest(min(-p0, -p1));
+
+    Rows32<D> w;
+    {
+        const int slot = min(32 * wave + (lane & 31), valid - 1), gi = (r0 + slot) % G;
+        w.p = rows_of_tile.pos[slot];
+        w.p_min = lowest(w.p);
+        w.p_max = -lowest(-w.p);
+        w.start(a.q + (int64_t)rows_of_tile.token[slot] * a.q_stride + (int64_t)(h * G + gi) * D + 8 * (lane >> 5));
+    }
+    const PartArgs part(a, 0, x.upto);
+    const Span64 span = span_of(part, p_min, p_max);
+    const int each = (span.nc + splits - 1) / splits;
+    const int c0 = min(split * each, span.nc), c1 = min(c0 + each, span.nc);
+    if (c0 < c1) walk<D>(part, lds, w, a.table + (int64_t)x.b0 * a.max_pages, x.upto - 1, h, span, c0, c1, p_min, p_max);
+
+    const float l = w.l + __shfl_xor(w.l, 32, 64);
+    const int slot = 32 * wave + (lane & 31), half = lane >> 5;
+    if (slot >= valid) return;
+    float *to = shared_part<D>(s, (int64_t)at * a.kv_heads + h, splits, split);
+    float *dst = to + slot * D + 4 * half;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
+                f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
+    if (half == 0) {
+        to[kTileRows * D + 2 * slot] = w.m;
+        to[kTileRows * D + 2 * slot + 1] = l;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(64 * kSplitWaves, 2)
+attn_shared_own_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int most_rows) {
+    __shared__ JoinLds<D, kSplitWaves> lds;
+    const Tables t = tables_of(s, a.B);
+    split_piece<D>(a, [&](int b) { return PartArgs(a, t.from[b], 0x7FFFFFFF); }, which, most_rows, true, lds);
+}
+
+// Joins a row's parts: a wave a row.
+template <int D>
+__global__ void __launch_bounds__(256)
+attn_shared_join_kernel(const AttnArgs a, const SharedAttnArgs sh, int which, int most_rows, int items, int splits) {
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int item = (int)(blockIdx.x % items), row = (int)(blockIdx.x / items) * 4 + wave;
+    const int b = item / a.kv_heads, h = item % a.kv_heads, G = a.q_heads / a.kv_heads;
+    const Tables tab = tables_of(sh, a.B);
+    const Begun x = static_cast<const Begun *>(a.ws)[item];      // written if the sequence has rows
+    const Seq s = seq_of(a, b, which);
+    if (row >= min(s.n * G, most_rows)) return;
+    float m = -__builtin_inff(), l = 0.0f, acc[D / 64];
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) acc[j] = 0.0f;
+    const auto take = [&](const float *o, const float *ml) {
+        const float pm = ml[0], pl = ml[1];
+        const float top = fmaxf(m, pm), base = top == -__builtin_inff() ? 0.0f : top;
+        const float f0 = exp2a(m - base), f1 = exp2a(pm - base);
+        m = top;
+        l = l * f0 + pl * f1;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) acc[j] = acc[j] * f0 + o[(D / 64) * lane + j] * f1;
+    };
+    for (int i = 0; i < x.pieces; ++i) {
+        const float *part = part_of(a, D, most_rows, x.wg + i);
+        take(part + row * D, part + most_rows * D + 2 * row);
+    }
+    const int first = tab.row[b];
+    if (first >= 0) {
+        const int at = first + row, r = at % kTileRows;
+        for (int i = 0; i < splits; ++i) {
+            const float *part = shared_part<D>(sh, (int64_t)(at / kTileRows) * a.kv_heads + h, splits, i);
+            take(part + r * D, part + kTileRows * D + 2 * r);
+        }
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int i = row / G, g = row - i * G;
+    const int64_t t = s.first + i;
+    uint16_t *dst = a.o + t * a.o_stride + (int64_t)(h * G + g) * D + (D / 64) * lane;
+    if constexpr (D == 128) *reinterpret_cast<uint32_t *>(dst) = narrow2a(acc[0] * inv, acc[1] * inv);
+    else *dst = f32_to_bf16_rne(acc[0] * inv);
+    if (a.lse && lane == 0) a.lse[t * a.q_heads + h * G + g] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+struct SharedPlan {
+    bool rows, tiles;      // sequences of few rows; of many
+    int most_rows, shared_tiles, splits;
+    int64_t items;
+    size_t table_bytes, own_bytes;
+    size_t bytes, most_bytes;      // for this call; for it and every smaller one
+};
+
+size_t own_bytes(int64_t items, int dim, int rows) {
+    return begun_slots(items) * sizeof(Begun) + (size_t)((items + kPieces) * part_floats(dim, rows)) * sizeof(float);
+}
+
+// Sequences of many rows, if the host cannot exclude them, are taken first, in the same
+// workspace.
+SharedPlan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups, int max_shared,
+                   int window, int sinks) {
+    SharedPlan p;
+    const int64_t G = q_heads / kv_heads, longest = max_q < T ? max_q : T;
+    p.tiles = longest * G > kMostRows;
+    p.rows = !p.tiles || (T - (B - 1) * longest) * G <= kMostRows;
+    p.most_rows = (int)(longest * G < kMostRows ? longest * G : kMostRows);
+    p.items = (int64_t)B * kv_heads;
+    const int64_t parts = groups < B ? groups : B;
+    p.shared_tiles = (int)(((int64_t)T * G + (kTileRows - 1) * parts) / kTileRows);
+    const int64_t wgs = (int64_t)p.shared_tiles * kv_heads;
+    const int64_t most = ((int64_t)max_shared + 4 * kChunk - 1) / (4 * kChunk);      // pieces of at least four chunks
+    int64_t splits = wgs > 0 ? (kWantItems + wgs - 1) / wgs : 1;
+    if (splits > most) splits = most;
+    p.splits = splits < 1 ? 1 : (int)splits;
+    p.table_bytes = table_ints(B, groups) * sizeof(int);
+    p.own_bytes = own_bytes(p.items, dim, p.most_rows);
+    const size_t part = (size_t)kTileRows * (dim + 2) * sizeof(float);
+    p.bytes = p.table_bytes + p.own_bytes + (size_t)wgs * p.splits * part;
+    const int64_t cut = wgs + kWantItems - 1, all = wgs * (most < 1 ? 1 : most);
+    p.most_bytes = p.table_bytes + p.own_bytes + (size_t)(cut < all ? cut : all) * part;
+    if (p.tiles) {
+        const size_t now = attn_tiles_plan(B, T, q_heads, kv_heads, dim, max_kv, window, sinks).ws_bytes;
+        const size_t bound = attn_tiles_most_bytes(B, T, q_heads, kv_heads, dim, max_kv);
+        if (p.bytes < now) p.bytes = now;
+        if (p.most_bytes < bound) p.most_bytes = bound;
+    }
+    return p;
+}
+
+template <int D>
+hipError_t launch(const AttnArgs &a, SharedAttnArgs s, const SharedPlan &p, hipStream_t stream) {
+    const int which = p.tiles ? kFewRows : kAllSeqs;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    AttnArgs own = a;
+    s.tables = ws;
+    own.ws = ws + p.table_bytes;
+    s.parts = ws + p.table_bytes + p.own_bytes;
+    const int64_t tiles = (int64_t)p.shared_tiles * p.splits * a.kv_heads, pieces = p.items + kPieces;
+    const int64_t join = p.items * ((p.most_rows + 3) / 4);
+    if (tiles > 0x7FFFFFFF || pieces > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(attn_shared_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, own, s, which, p.shared_tiles);
+    if (tiles > 0)
+        hipLaunchKernelGGL((attn_shared_tiles_kernel<D>), dim3((unsigned)tiles), dim3(256), 0, stream, own, s, which, p.splits);
+    hipLaunchKernelGGL((attn_shared_own_kernel<D>), dim3((unsigned)pieces), dim3(64 * kSplitWaves), 0, stream, own, s, which,
+                       p.most_rows);
+    hipLaunchKernelGGL((attn_shared_join_kernel<D>), dim3((unsigned)join), dim3(256), 0, stream, own, s, which, p.most_rows,
+                       (int)p.items, p.splits);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attn_shared_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups,
+                            int max_shared) {
+    if (B == 0 || T == 0) return 0;
+    return plan_of(B, T, q_heads, kv_heads, dim, max_q, max_kv, groups, max_shared, 0, 0).most_bytes;
+}
+
+hipError_t launch_attn_shared(const AttnArgs &a, const SharedAttnArgs &s, size_t ws_bytes, hipStream_t stream) {
+    const SharedPlan p = plan_of(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_q, a.max_kv, s.groups, s.max_shared, a.window,
+                                 a.sinks);
+    if (p.bytes > ws_bytes) return hipErrorInvalidValue;
+    if (p.tiles) {
+        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, stream);
+        if (e != hipSuccess || !p.rows) return e;
+    }
+    return a.dim == 64 ? launch<64>(a, s, p, stream) : launch<128>(a, s, p, stream);
+}
+
+}  // namespace biloco

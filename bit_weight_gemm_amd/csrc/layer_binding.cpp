@@ -37,6 +37,11 @@ using GemmMxQuantFn = Status (*)(const void *, int64_t, const uint8_t *, const u
 using SampleFn = Status (*)(const void *, int64_t, int32_t, int32_t, int32_t, const float *, const int32_t *,
                             const float *, const float *, const float *, int32_t *, float *, void *, size_t,
                             hipStream_t);
+using SharedFn = Status (*)(const uint8_t *, const uint8_t *, const uint8_t *, const uint8_t *, int32_t, int32_t,
+                            int32_t, int32_t, const void *, int64_t, int32_t, const int32_t *, const int32_t *,
+                            const int32_t *, int32_t, int32_t, int32_t, int32_t, int32_t, const int32_t *,
+                            const int32_t *, int32_t, int32_t, float, int32_t, int32_t, void *, int64_t, float *,
+                            void *, size_t, hipStream_t);
 
 namespace {
 
@@ -48,6 +53,7 @@ DequantMxFn g_dequant_mx;
 GemmMxFn g_gemm_mx;
 GemmMxQuantFn g_gemm_mx_quant;
 SampleFn g_sample;
+SharedFn g_shared;
 
 using at::Tensor;
 
@@ -372,6 +378,30 @@ Status sample(PyObject *const *a) {
                     (float *)plp, ws.data_ptr(), ws.nbytes(), stream(a[9]));
 }
 
+Status shared(PyObject *const *a) {
+    const Cache c = cache(a[0]);
+    const Tensor &q = tensor(a[1], "q"), &out = tensor(a[13], "out"), &ws = space(a[15]),
+                 &groups = tensor(a[5], "group_start"), &lens = tensor(a[6], "shared_len");
+    if (q.dim() != 3) refuse("q", "[tokens][heads][dim] expected");
+    const int64_t T = q.size(0);
+    const int32_t heads = size32(q.size(1), "q");
+    const Ragged r = ragged(a[2], a[3], a[4]);
+    if (lens.dim() != 1) refuse("shared_len", "int32 [groups] expected");
+    const int32_t n = size32(lens.size(0), "shared_len");
+    const int32_t *len = ints(lens, "shared_len", n), *start = ints(groups, "group_start", n + 1);
+    const Tensor *lse = maybe(a[14], "lse");
+    if (lse && (lse->scalar_type() != at::kFloat || !shaped(*lse, T, heads) || !lse->is_contiguous()))
+        refuse("lse", "contiguous fp32 [tokens][heads] expected");
+    const int64_t sq = token_stride(q, T, heads, c.dim, "q"), so = token_stride(out, T, heads, c.dim, "out");
+    on_one_gpu(a[17], {c.t[0], c.t[1], c.t[2], c.t[3], &q, &out, &ws, lse, &groups, &lens, &tensor(a[2], "q_start"),
+                       &tensor(a[3], "kv_len"), &tensor(a[4], "block_table")});
+    return g_shared(c.p[0], c.p[1], c.p[2], c.p[3], c.pages, c.heads, c.page, c.dim, q.data_ptr(), sq, heads, r.start,
+                    r.len, r.table, r.max_pages, r.B, size32(T, "q"), integer32(a[7], "max_q_len"),
+                    integer32(a[8], "max_kv_len"), start, len, n, integer32(a[9], "max_shared_len"), number(a[10]),
+                    integer32(a[11], "window"), integer32(a[12], "sinks"), out.data_ptr(), so,
+                    lse ? (float *)lse->data_ptr() : nullptr, ws.data_ptr(), ws.nbytes(), stream(a[16]));
+}
+
 // Calls f with `want` positional arguments; returns the status.
 template <Status (*F)(PyObject *const *), int WANT>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -395,7 +425,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    constexpr int kEntries = 8;
+    constexpr int kEntries = 9;
     if (n != kEntries) {
         PyErr_Format(PyExc_TypeError, "%d addresses expected", kEntries);
         return nullptr;
@@ -412,6 +442,7 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
     g_gemm_mx = (GemmMxFn)p[5];
     g_gemm_mx_quant = (GemmMxQuantFn)p[6];
     g_sample = (SampleFn)p[7];
+    g_shared = (SharedFn)p[8];
     g_append = (AppendFn)p[0];
     Py_RETURN_NONE;
 }
@@ -426,6 +457,7 @@ PyMethodDef methods[] = {{"bind", FASTCALL(bind), METH_FASTCALL, "addresses of t
                          {"gemm_mxfp4", FASTCALL((entry<gemm_mx, 8>)), METH_FASTCALL, "biloco_gemm_mxfp4"},
                          {"gemm_mxfp4_quant", FASTCALL((entry<gemm_mx_quant, 7>)), METH_FASTCALL, "biloco_gemm_mxfp4_quant"},
                          {"sample", FASTCALL((entry<sample, 11>)), METH_FASTCALL, "biloco_sample"},
+                         {"attn_shared", FASTCALL((entry<shared, 18>)), METH_FASTCALL, "biloco_attn_shared"},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

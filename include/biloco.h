@@ -519,6 +519,50 @@ biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const
  * smaller M with the same N and K (0 is possible).  No HIP call. */
 biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K, size_t *bytes);
 
+/* biloco_attn_paged for a batch whose sequences share their first tokens in
+ * groups, which are read once for a group instead of once for a sequence:
+ *   group_start int32 [n_groups+1]: group g is sequences group_start[g] ..
+ *             group_start[g+1] - 1; group_start[0] = 0, non-decreasing,
+ *             group_start[n_groups] = B
+ *   shared_len int32 [n_groups]: tokens j < shared_len[g] of every sequence of the
+ *             group are read through the block table row of the group's first
+ *             sequence; the others through its own.  0: nothing is shared.
+ * Everything else is as there: positions, masks and results are those of
+ * biloco_attn_paged on sequences whose tables name the same pages first.
+ * shared_len may end inside a page, and may pass a sequence's kv_len (its rows then
+ * see the shared tokens up to their position).
+ * For the product with v a weight of a shared token is rounded to bf16 (2^-8);
+ * others as there.  A sequence of more than 64 rows (new tokens times q_heads /
+ * kv_heads) fills the matrix cores by itself: its tokens are read through its own
+ * table, which has to name the shared pages too.
+ * max_shared_len bounds shared_len on the host; it shapes the launch.
+ * workspace: >= biloco_attn_shared_workspace_bytes(...) bytes, no fill needed; not
+ *   shared by calls that can run at the same time.
+ * 1 <= n_groups <= 65535.  Contents that break these rules give unspecified values,
+ * but no access outside the arrays.  T = 0 or B = 0 does nothing.  Two to six
+ * launches. */
+biloco_status biloco_attn_shared(const uint8_t *k_codes, const uint8_t *v_codes,
+                                 const uint8_t *k_scales, const uint8_t *v_scales,
+                                 int32_t num_pages, int32_t kv_heads, int32_t page_size,
+                                 int32_t head_dim, const uint16_t *q, int64_t q_stride,
+                                 int32_t q_heads, const int32_t *q_start, const int32_t *kv_len,
+                                 const int32_t *block_table, int32_t max_pages, int32_t B,
+                                 int32_t T, int32_t max_q_len, int32_t max_kv_len,
+                                 const int32_t *group_start, const int32_t *shared_len,
+                                 int32_t n_groups, int32_t max_shared_len, float scale,
+                                 int32_t window, int32_t sinks, uint16_t *o, int64_t o_stride,
+                                 float *lse, void *workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
+/* Bytes of workspace biloco_attn_shared needs for these sizes, and for every call
+ * with smaller B, T, max_q_len, max_kv_len, n_groups and max_shared_len on the same
+ * heads.  No HIP call. */
+biloco_status biloco_attn_shared_workspace_bytes(int32_t B, int32_t T, int32_t q_heads,
+                                                 int32_t kv_heads, int32_t head_dim,
+                                                 int32_t max_q_len, int32_t max_kv_len,
+                                                 int32_t n_groups, int32_t max_shared_len,
+                                                 size_t *bytes);
+
 /* A token for each of `rows` rows of V logits x, drawn with a given number u of
  * [0, 1).  For a row with temperature T, top_k k, top_p p and min_p m:
  *   w_i = exp((x_i - max x) / T), in steps of 2^-44
