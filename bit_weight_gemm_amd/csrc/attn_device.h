@@ -45,10 +45,6 @@ struct PartArgs : AttnArgs {
     int from, upto;
     __host__ __device__ PartArgs(const AttnArgs &a, int from_, int upto_) : AttnArgs(a), from(from_), upto(upto_) {}
 };
-__device__ __forceinline__ int from_of(const AttnArgs &) { return 0; }
-__device__ __forceinline__ int from_of(const PartArgs &a) { return a.from; }
-__device__ __forceinline__ int upto_of(const AttnArgs &, int hi) { return hi; }
-__device__ __forceinline__ int upto_of(const PartArgs &a, int hi) { return min(hi, a.upto); }
 __device__ __forceinline__ bool holds(const AttnArgs &, int) { return true; }
 __device__ __forceinline__ bool holds(const PartArgs &a, int j) { return (bool)((j >= a.from) & (j < a.upto)); }
 
@@ -58,14 +54,22 @@ struct Span64 {
     int s0, lo0, ns, nc;
     __device__ __forceinline__ int start(int c) const { return c < ns ? s0 + c * kChunk : lo0 + (c - ns) * kChunk; }
 };
-template <class A>
-__device__ __forceinline__ Span64 span_of(const A &a, int p_min, int p_max) {
+__device__ __forceinline__ Span64 span_of(const AttnArgs &a, int p_min, int p_max) {
     Span64 s;
-    const int lo = max(a.window > 0 ? max(p_min - a.window + 1, 0) : 0, from_of(a));
-    s.s0 = from_of(a) & ~(kChunk - 1);
+    const int lo = a.window > 0 ? max(p_min - a.window + 1, 0) : 0;
+    s.s0 = 0;
     s.lo0 = lo & ~(kChunk - 1);
-    s.ns = max(upto_of(a, min(a.sinks, s.lo0)) - s.s0 + kChunk - 1, 0) / kChunk;
-    s.nc = s.ns + (max(upto_of(a, p_max + 1) - s.lo0, 0) + kChunk - 1) / kChunk;
+    s.ns = (min(a.sinks, s.lo0) + kChunk - 1) / kChunk;
+    s.nc = s.ns + (max(p_max + 1 - s.lo0, 0) + kChunk - 1) / kChunk;
+    return s;
+}
+__device__ __forceinline__ Span64 span_of(const PartArgs &a, int p_min, int p_max) {
+    Span64 s;
+    const int lo = max(a.window > 0 ? max(p_min - a.window + 1, 0) : 0, a.from);
+    s.s0 = a.from & ~(kChunk - 1);
+    s.lo0 = lo & ~(kChunk - 1);
+    s.ns = max(min(min(a.sinks, s.lo0), a.upto) - s.s0 + kChunk - 1, 0) / kChunk;
+    s.nc = s.ns + (max(min(p_max + 1, a.upto) - s.lo0, 0) + kChunk - 1) / kChunk;
     return s;
 }
 // What a row at position pos sees; lo = low_of(pos).  No branches.
@@ -130,7 +134,8 @@ __device__ __forceinline__ Seq seq_from(const A &a, int start, int stop, int kv_
     return s;
 }
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int which) {
+template <class A>
+__device__ __forceinline__ Seq seq_of(const A &a, int b, int which) {
     return seq_from(a, a.q_start[b], a.q_start[b + 1], a.kv_len[b], which);
 }
 // The same for a sequence that the whole workgroup works on, through scalar
@@ -138,7 +143,8 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, int which) {
 __device__ __forceinline__ int scalar_load(const int *p) {
     return *(const __attribute__((address_space(4))) int *)(uintptr_t)p;
 }
-__device__ __forceinline__ Seq seq_uniform(const AttnArgs &a, int b, int which) {
+template <class A>
+__device__ __forceinline__ Seq seq_uniform(const A &a, int b, int which) {
     return seq_from(a, scalar_load(a.q_start + b), scalar_load(a.q_start + b + 1), scalar_load(a.kv_len + b), which);
 }
 

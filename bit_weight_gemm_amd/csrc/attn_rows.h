@@ -346,11 +346,13 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, 
 // A workgroup a piece of an item: equal pieces of as many units (chunks that
 // its waves take side by side) as spread all items over kPieces workgroups, or a
 // few more.  At most kPieces + items pieces, the grid's size; the workgroups that
-// are left over end at once.  of(b): the call's arguments for sequence b.  An item
+// are left over end at once.  K::of(b): the call's arguments for sequence b.  An item
 // that is one piece is written as it is to be, unless it is part of a longer one.
-template <int D, class Of>
-__device__ __forceinline__ void split_piece(const AttnArgs &a, Of of, int which, int most_rows, bool part_only,
-                                            JoinLds<D, kSplitWaves> &lds) {
+template <int D, class K>
+__global__ void __launch_bounds__(64 * kSplitWaves, 2)
+attn_split_kernel(const K k, int which, int most_rows) {
+    __shared__ JoinLds<D, kSplitWaves> lds;
+    const AttnArgs &a = k.a;
     const int wave = uniform((int)(threadIdx.x >> 6));
     const auto shift_of = [&](const Seq &s) { return row_shift_of(rows_of(a, s, most_rows)); };
     // a sequence with rows has at least one unit, to write its rows in
@@ -359,7 +361,7 @@ __device__ __forceinline__ void split_piece(const AttnArgs &a, Of of, int which,
         return s.n > 0 ? max((s.c.nc + (1 << by) - 1) >> by, 1) : 0;
     };
     int64_t total = 0, before;
-    for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(of(i), i, which)) * a.kv_heads;
+    for (int i = threadIdx.x & 63; i < a.B; i += 64) total += (int64_t)units(seq_of(k.of(i), i, which)) * a.kv_heads;
     const int64_t each = max((uniform(wave_sum64(total)) + kPieces - 1) / kPieces, (int64_t)1);
     const int even = (int)min(each, (int64_t)1 << 24);      // no item has more units
     // Each item's last piece can be short, and a workgroup above kPieces waits for
@@ -368,21 +370,21 @@ __device__ __forceinline__ void split_piece(const AttnArgs &a, Of of, int which,
     // 24.3 us with the join).
     float count[kSizes] = {};      // compared with kPieces only, so exact where it matters
     for (int i = threadIdx.x & 63; i < a.B; i += 64) {
-        const uint32_t u = (uint32_t)units(seq_of(of(i), i, which));
+        const uint32_t u = (uint32_t)units(seq_of(k.of(i), i, which));
 #pragma unroll
-        for (int k = 0; k < kSizes; ++k) count[k] += (float)((u + even + k - 1) / (uint32_t)(even + k));
+        for (int z = 0; z < kSizes; ++z) count[z] += (float)((u + even + k - 1) / (uint32_t)(even + k));
     }
     int more = 0;
 #pragma unroll
-    for (int k = kSizes - 1; k >= 0; --k)
-        if (wave_sum_dpp(count[k]) * (float)a.kv_heads <= (float)kPieces) more = k;
+    for (int z = kSizes - 1; z >= 0; --z)
+        if (wave_sum_dpp(count[z]) * (float)a.kv_heads <= (float)kPieces) more = z;
     const int size = even + (uniform(more) <= even ? uniform(more) : 0);
     const auto pieces = [&](const Seq &s) { return (int)(((uint32_t)units(s) + size - 1) / (uint32_t)size); };
     const int b = uniform(find_seq(a.B, blockIdx.x, before,
-                                   [&](int i) { return (int64_t)pieces(seq_of(of(i), i, which)) * a.kv_heads; }));
+                                   [&](int i) { return (int64_t)pieces(seq_of(k.of(i), i, which)) * a.kv_heads; }));
     if (b < 0) return;
-    const auto &mine_a = of(b);
-    const Seq s = seq_uniform(mine_a, b, which);
+    const auto &part = k.of(b);
+    const Seq s = seq_uniform(part, b, which);
     const int n = uniform(pieces(s)), at = (int)(blockIdx.x - uniform(before));
     const int h = uniform(at / n), u0 = uniform((at - h * n) * size);
     const int rows = rows_of(a, s, most_rows), row_shift = shift_of(s), lanes = kSplitWaves >> row_shift;
@@ -391,10 +393,10 @@ __device__ __forceinline__ void split_piece(const AttnArgs &a, Of of, int which,
     Rows16<D> x(a, s, h, mine, rows);
     Stage<D> st;
     if (mine < rows)
-        x.run(mine_a, w, s, st, false, u0 * lanes + (wave >> row_shift), min((u0 + size) * lanes, s.c.nc), lanes);
+        x.run(part, w, s, st, false, u0 * lanes + (wave >> row_shift), min((u0 + size) * lanes, s.c.nc), lanes);
     if (u0 == 0 && threadIdx.x == 0) static_cast<Begun *>(a.ws)[b * a.kv_heads + h] = Begun{(int)blockIdx.x, n};
     finish<D, kSplitWaves>(a, s, x, lds, h, rows, 1 << row_shift,
-                           n == 1 && !part_only ? nullptr : part_of(a, D, most_rows, blockIdx.x), most_rows);
+                           n == 1 && !K::kPart ? nullptr : part_of(a, D, most_rows, blockIdx.x), most_rows);
 }
 
 }  // namespace attn

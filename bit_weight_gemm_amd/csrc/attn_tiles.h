@@ -1,5 +1,5 @@
 // The parts of attention over many query rows per key/value head (k_attn_tiles.hip says
-// how a workgroup works): chunks on their way into LDS, 32 rows a wave, the walk.
+// how a workgroup works): chunks on their way into LDS, 32 rows a wave, the walk over chunks.
 #pragma once
 #include "attn_device.h"
 
@@ -277,68 +277,112 @@ struct Rows32 {
     }
 };
 
-// A workgroup's rows over chunks [c0, c1) of its span, at least one.  Positions of its
-// rows: p_min to p_max.
-template <int D, class A>
-__device__ __forceinline__ void walk(const A &a, TileLds<D> &lds, Rows32<D> &w, const int *table, int last, int h,
-                                     const Span64 &span, int c0, int c1, int p_min, int p_max) {
+// What a workgroup works on: chunks [c0, c1) of `span`, seen by rows at positions p_min
+// to p_max, through a block table row whose last token is `last`.
+template <class A>
+struct TileWork {
+    A a;
+    const int *table;
+    int last, h, c0, c1, p_min, p_max;
+    Span64 span;
+    int at, split;      // tile, piece of its chunks
+    int r0, rows;       // first of its rows, how many there are
+    Seq s;              // the sequence, where it is one
+};
+
+// The kernel of both calls: K::begin gives a workgroup its rows and its work (false:
+// there is none), K::end takes what the rows have gathered.  In one function, since the
+// walk over chunks as a function of its own costs the compiler 32 registers' moves a
+// turn (chunks of 64 channels 356 -> 380 us).
+template <int D, class K>
+__global__ void __launch_bounds__(256, 2)
+attn_tiles_kernel(const K k, int splits) {
+    __shared__ TileLds<D> lds;
+    __shared__ typename K::Lds more;
+    Rows32<D> w;
+    TileWork<typename K::Args> t{k.args()};
+    if (!k.begin(w, t, more, splits)) return;
+    const auto &a = t.a;
+    const int *table = t.table;
+    const int last = t.last, h = t.h, c0 = t.c0, c1 = t.c1, p_min = t.p_min, p_max = t.p_max;
+    const Span64 span = t.span;
     const int shift = 31 - __clz(a.page), wave = uniform((int)(threadIdx.x >> 6));
     const float c2 = a.scale * kLog2e;
-    // Two 32-token tiles a chunk.  The scores of a tile are computed while
-    // the one before goes through its exponentials, its maximum while that
-    // one's values are gathered.
-    const auto whole = [&](int c) { return all_see(a, p_min, p_max, span.start(c)); };
-    Loader<D> ld;
-    // chunk c on its way, and the pages of the one after it
-    const auto request = [&](int c) {
-        ld.load(a, shift, h, span.start(min(c, c1 - 1)));
-        ld.look_up(table, shift, last, span.start(min(c + 1, c1 - 1)));
-    };
-    ld.look_up(table, shift, last, span.start(c0));
-    request(c0);
-    ld.store(a, lds, 0, span.start(c0), p_min, p_max);
-    request(c0 + 1);
-    __syncthreads();
-    f32x16a_t s0 = w.scores(lds, 0, 0), s1;
-    if (!whole(c0)) w.hide(a, s0, span.start(c0));
-    w.follow(w.top_of(s0, c2));
-    int c = c0;
-    while (true) {
-        // Nothing to hide here and next.  With 64 channels the plain order below
-        // is faster: it leaves registers for three waves a SIMD instead of two
-        // (chunks of 2048 behind up to 10000 tokens: 343 us, 357 this way).
-        while (D == 128 && c + 1 < c1 && whole(c) && whole(c + 1)) {
-            const int buf = (c - c0) & 1;
-            __syncthreads();      // the other buffer has been read
-            if ((threadIdx.x & 63) == 0) lds.odd[buf ^ 1][wave] = 0;
-            w.follow(w.template tile<true>(lds, buf, 0, buf, 1, s0, s1, c2, ld));
-            request(c + 2);
-            __syncthreads();      // the next chunk is in place
-            w.follow(w.template tile<false>(lds, buf, 1, buf ^ 1, 0, s1, s0, c2, ld));
-            ++c;
-        }
-        const int buf = (c - c0) & 1, j0 = span.start(c);
-        u32x4_t pt[2];
+    if (c0 < c1) {
+        // Two 32-token tiles a chunk.  The scores of a tile are computed while
+        // the one before goes through its exponentials, its maximum while that
+        // one's values are gathered.
+        const auto whole = [&](int c) { return all_see(a, p_min, p_max, span.start(c)); };
+        Loader<D> ld;
+        // chunk c on its way, and the pages of the one after it
+        const auto request = [&](int c) {
+            ld.load(a, shift, h, span.start(min(c, c1 - 1)));
+            ld.look_up(table, shift, last, span.start(min(c + 1, c1 - 1)));
+        };
+        ld.look_up(table, shift, last, span.start(c0));
+        request(c0);
+        ld.store(a, lds, 0, span.start(c0), p_min, p_max);
+        request(c0 + 1);
         __syncthreads();
-        if (c + 1 < c1) {
-            ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
-            request(c + 2);
-        }
-        if (lds.odd[buf][0] | lds.odd[buf][1] | lds.odd[buf][2] | lds.odd[buf][3]) w.mark_nan(a, lds, buf, j0);
-        w.weigh(s0, c2, pt);
-        s1 = w.scores(lds, buf, 1);
-        if (!all_see(a, w.p_min, w.p_max, j0)) w.hide(a, s1, j0 + 32);
-        w.gather(lds, buf, 0, pt);
-        w.follow(w.top_of(s1, c2));
-        __syncthreads();
-        w.weigh(s1, c2, pt);
-        if (c + 1 < c1) {
-            s0 = w.scores(lds, buf ^ 1, 0);
-            if (!all_see(a, w.p_min, w.p_max, span.start(c + 1))) w.hide(a, s0, span.start(c + 1));
-        }
-        w.gather(lds, buf, 1, pt);
-        if (++c == c1) break;
+        f32x16a_t s0 = w.scores(lds, 0, 0), s1;
+        if (!whole(c0)) w.hide(a, s0, span.start(c0));
         w.follow(w.top_of(s0, c2));
+        int c = c0;
+        while (true) {
+            // Nothing to hide here and next.  With 64 channels the plain order below
+            // is faster: it leaves registers for three waves a SIMD instead of two
+            // (chunks of 2048 behind up to 10000 tokens: 343 us, 357 this way).
+            while (D == 128 && c + 1 < c1 && whole(c) && whole(c + 1)) {
+                const int buf = (c - c0) & 1;
+                __syncthreads();      // the other buffer has been read
+                if ((threadIdx.x & 63) == 0) lds.odd[buf ^ 1][wave] = 0;
+                w.follow(w.template tile<true>(lds, buf, 0, buf, 1, s0, s1, c2, ld));
+                request(c + 2);
+                __syncthreads();      // the next chunk is in place
+                w.follow(w.template tile<false>(lds, buf, 1, buf ^ 1, 0, s1, s0, c2, ld));
+                ++c;
+            }
+            const int buf = (c - c0) & 1, j0 = span.start(c);
+            u32x4_t pt[2];
+            __syncthreads();
+            if (c + 1 < c1) {
+                ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
+                request(c + 2);
+            }
+            if (lds.odd[buf][0] | lds.odd[buf][1] | lds.odd[buf][2] | lds.odd[buf][3]) w.mark_nan(a, lds, buf, j0);
+            w.weigh(s0, c2, pt);
+            s1 = w.scores(lds, buf, 1);
+            if (!all_see(a, w.p_min, w.p_max, j0)) w.hide(a, s1, j0 + 32);
+            w.gather(lds, buf, 0, pt);
+            w.follow(w.top_of(s1, c2));
+            __syncthreads();
+            w.weigh(s1, c2, pt);
+            if (c + 1 < c1) {
+                s0 = w.scores(lds, buf ^ 1, 0);
+                if (!all_see(a, w.p_min, w.p_max, span.start(c + 1))) w.hide(a, s0, span.start(c + 1));
+            }
+            w.gather(lds, buf, 1, pt);
+            if (++c == c1) break;
+            w.follow(w.top_of(s0, c2));
+        }
+    }
+    k.end(w, t, w.l + __shfl_xor(w.l, 32, 64), splits);
+}
+
+// A row's sums as a piece of them: [kTileRows][D], then maxima and sums of the weights.
+template <int D>
+__device__ __forceinline__ void leave(const Rows32<D> &w, float l, float *part, int row) {
+    const int half = (threadIdx.x & 63) >> 5;
+    float *dst = part + row * D + 4 * half;
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
+                f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
+    if (half == 0) {
+        part[kTileRows * D + 2 * row] = w.m;
+        part[kTileRows * D + 2 * row + 1] = l;
     }
 }
 

@@ -70,12 +70,12 @@ attn_whole_kernel(const AttnArgs a, int which, int most_rows) {
     finish<D, kWholeWaves>(a, s, x, lds, h, rows, 1 << row_shift, nullptr, 0);
 }
 
-template <int D>
-__global__ void __launch_bounds__(64 * kSplitWaves, 2)
-attn_split_kernel(const AttnArgs a, int which, int most_rows) {
-    __shared__ JoinLds<D, kSplitWaves> lds;
-    split_piece<D>(a, [&](int) -> const AttnArgs & { return a; }, which, most_rows, false, lds);
-}
+// Items of the whole batch.
+struct PagedRows {
+    static constexpr bool kPart = false;
+    AttnArgs a;
+    __device__ __forceinline__ const AttnArgs &of(int) const { return a; }
+};
 
 // Joins the pieces of the rows of items that several workgroups shared: WAYS
 // waves a row, each taking every WAYS-th piece; 4 / WAYS rows of one item a
@@ -258,8 +258,8 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
         return hipGetLastError();
     }
     if (p.items + kPieces > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_split_kernel<D>), dim3((unsigned)(p.items + kPieces)), dim3(64 * kSplitWaves), 0, stream, a,
-                       which, p.most_rows);
+    hipLaunchKernelGGL((attn_split_kernel<D, PagedRows>), dim3((unsigned)(p.items + kPieces)), dim3(64 * kSplitWaves), 0,
+                       stream, PagedRows{a}, which, p.most_rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // few rows: four waves a row; many: a wave

@@ -125,87 +125,82 @@ __device__ __forceinline__ float *shared_part(const SharedAttnArgs &s, int64_t i
     return static_cast<float *>(s.parts) + (item * splits + split) * kTileRows * (D + 2);
 }
 
-// Rows of a tile: the token and position of each.
-struct TileRows {
-    int token[kTileRows], pos[kTileRows];
-};
+// A workgroup takes 128 rows of a group, whose tokens and positions it first lists.
+struct SharedTiles {
+    using Args = PartArgs;
+    struct Lds {
+        int token[kTileRows], pos[kTileRows];
+    };
+    AttnArgs a;
+    SharedAttnArgs s;
+    int which;
 
-template <int D>
-__global__ void __launch_bounds__(256, 2)
-attn_shared_tiles_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int splits) {
-    __shared__ TileLds<D> lds;
-    __shared__ TileRows rows_of_tile;
-    const Tables t = tables_of(s, a.B);
-    const int h = (int)(blockIdx.x % a.kv_heads), rest = (int)(blockIdx.x / a.kv_heads);
-    const int split = rest % splits, at = rest / splits;
-    if (at >= scalar_load(t.tile + s.groups)) return;
-    int g = 0, last_g = s.groups - 1;      // the last group whose tiles begin at or before this one
-    while (g < last_g) {
-        const int mid = (g + last_g + 1) / 2;
-        if (scalar_load(t.tile + mid) <= at) g = mid;
-        else last_g = mid - 1;
-    }
-    const Group x = group_at(a, s, g);
-    const int G = a.q_heads / a.kv_heads, r0 = (at - scalar_load(t.tile + g)) * kTileRows;
-    const int first = scalar_load(t.before + x.b0), rows = (scalar_load(t.before + x.b1) - first) * G;
-    const int valid = min(rows - r0, kTileRows);
-    for (int b = x.b0 + threadIdx.x; b < x.b1; b += 256) {
-        const Seq q = seq_of(a, b, which);
-        const int at0 = (t.before[b] - first) * G - r0;      // row of its first row in the tile
-        for (int r = max(at0, 0); r < min(at0 + q.n * G, kTileRows); ++r) {
-            const int i = (r - at0) / G;
-            rows_of_tile.token[r] = q.first + i;
-            rows_of_tile.pos[r] = q.past + i;
-        }
-    }
-    __syncthreads();
-    const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
-    const auto lowest = [](int v) {
+    __device__ __forceinline__ PartArgs args() const { return PartArgs(a, 0, 0); }
+    __device__ __forceinline__ static int lowest(int v) {
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
         return uniform(v);
-    };
-    const int p0 = rows_of_tile.pos[min(lane, valid - 1)], p1 = rows_of_tile.pos[min(lane + 64, valid - 1)];
-    const int p_min = lowest(min(p0, p1)), p_max = -lowest(min(-p0, -p1));
-
-    Rows32<D> w;
-    {
-        const int slot = min(32 * wave + (lane & 31), valid - 1), gi = (r0 + slot) % G;
-        w.p = rows_of_tile.pos[slot];
+    }
+    template <int D>
+    __device__ __forceinline__ bool begin(Rows32<D> &w, TileWork<PartArgs> &t, Lds &lds, int splits) const {
+        const Tables tab = tables_of(s, a.B);
+        t.h = (int)(blockIdx.x % a.kv_heads);
+        const int rest = (int)(blockIdx.x / a.kv_heads);
+        t.split = rest % splits;
+        t.at = rest / splits;
+        if (t.at >= scalar_load(tab.tile + s.groups)) return false;
+        int g = 0, last_g = s.groups - 1;      // the last group whose tiles begin at or before this one
+        while (g < last_g) {
+            const int mid = (g + last_g + 1) / 2;
+            if (scalar_load(tab.tile + mid) <= t.at) g = mid;
+            else last_g = mid - 1;
+        }
+        const Group x = group_at(a, s, g);
+        const int G = a.q_heads / a.kv_heads, r0 = (t.at - scalar_load(tab.tile + g)) * kTileRows;
+        const int first = scalar_load(tab.before + x.b0);
+        t.rows = min((scalar_load(tab.before + x.b1) - first) * G - r0, kTileRows);
+        for (int b = x.b0 + threadIdx.x; b < x.b1; b += 256) {
+            const Seq q = seq_of(a, b, which);
+            const int at0 = (tab.before[b] - first) * G - r0;      // row of its first row in the tile
+            for (int r = max(at0, 0); r < min(at0 + q.n * G, kTileRows); ++r) {
+                const int i = (r - at0) / G;
+                lds.token[r] = q.first + i;
+                lds.pos[r] = q.past + i;
+            }
+        }
+        __syncthreads();
+        const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+        const int p0 = lds.pos[min(lane, t.rows - 1)], p1 = lds.pos[min(lane + 64, t.rows - 1)];
+        t.p_min = lowest(min(p0, p1));
+        t.p_max = -lowest(min(-p0, -p1));
+        const int row = min(32 * wave + (lane & 31), t.rows - 1), gi = (r0 + row) % G;
+        w.p = lds.pos[row];
         w.p_min = lowest(w.p);
         w.p_max = -lowest(-w.p);
-        w.start(a.q + (int64_t)rows_of_tile.token[slot] * a.q_stride + (int64_t)(h * G + gi) * D + 8 * (lane >> 5));
+        w.start(a.q + (int64_t)lds.token[row] * a.q_stride + (int64_t)(t.h * G + gi) * D + 8 * (lane >> 5));
+        t.a.upto = x.upto;
+        t.last = x.upto - 1;
+        t.table = a.table + (int64_t)x.b0 * a.max_pages;
+        t.span = span_of(t.a, t.p_min, t.p_max);
+        const int each = (t.span.nc + splits - 1) / splits;
+        t.c0 = min(t.split * each, t.span.nc);
+        t.c1 = min(t.c0 + each, t.span.nc);
+        return true;
     }
-    const PartArgs part(a, 0, x.upto);
-    const Span64 span = span_of(part, p_min, p_max);
-    const int each = (span.nc + splits - 1) / splits;
-    const int c0 = min(split * each, span.nc), c1 = min(c0 + each, span.nc);
-    if (c0 < c1) walk<D>(part, lds, w, a.table + (int64_t)x.b0 * a.max_pages, x.upto - 1, h, span, c0, c1, p_min, p_max);
-
-    const float l = w.l + __shfl_xor(w.l, 32, 64);
-    const int slot = 32 * wave + (lane & 31), half = lane >> 5;
-    if (slot >= valid) return;
-    float *to = shared_part<D>(s, (int64_t)at * a.kv_heads + h, splits, split);
-    float *dst = to + slot * D + 4 * half;
-#pragma unroll
-    for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
-                f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
-    if (half == 0) {
-        to[kTileRows * D + 2 * slot] = w.m;
-        to[kTileRows * D + 2 * slot + 1] = l;
+    template <int D>
+    __device__ __forceinline__ void end(const Rows32<D> &w, const TileWork<PartArgs> &t, float l, int splits) const {
+        const int row = 32 * (int)(threadIdx.x >> 6) + (int)(threadIdx.x & 31);
+        if (row < t.rows) leave(w, l, shared_part<D>(s, (int64_t)t.at * a.kv_heads + t.h, splits, t.split), row);
     }
-}
+};
 
-template <int D>
-__global__ void __launch_bounds__(64 * kSplitWaves, 2)
-attn_shared_own_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int most_rows) {
-    __shared__ JoinLds<D, kSplitWaves> lds;
-    const Tables t = tables_of(s, a.B);
-    split_piece<D>(a, [&](int b) { return PartArgs(a, t.from[b], 0x7FFFFFFF); }, which, most_rows, true, lds);
-}
+// A sequence's own tokens.
+struct OwnRows {
+    static constexpr bool kPart = true;
+    AttnArgs a;
+    SharedAttnArgs s;
+    __device__ __forceinline__ PartArgs of(int b) const { return PartArgs(a, tables_of(s, a.B).from[b], 0x7FFFFFFF); }
+};
 
 // Joins a row's parts: a wave a row.
 template <int D>
@@ -308,9 +303,10 @@ hipError_t launch(const AttnArgs &a, SharedAttnArgs s, const SharedPlan &p, hipS
     if (tiles > 0x7FFFFFFF || pieces > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(attn_shared_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, own, s, which, p.shared_tiles);
     if (tiles > 0)
-        hipLaunchKernelGGL((attn_shared_tiles_kernel<D>), dim3((unsigned)tiles), dim3(256), 0, stream, own, s, which, p.splits);
-    hipLaunchKernelGGL((attn_shared_own_kernel<D>), dim3((unsigned)pieces), dim3(64 * kSplitWaves), 0, stream, own, s, which,
-                       p.most_rows);
+        hipLaunchKernelGGL((attn_tiles_kernel<D, SharedTiles>), dim3((unsigned)tiles), dim3(256), 0, stream,
+                           SharedTiles{own, s, which}, p.splits);
+    hipLaunchKernelGGL((attn_split_kernel<D, OwnRows>), dim3((unsigned)pieces), dim3(64 * kSplitWaves), 0, stream,
+                       OwnRows{own, s}, which, p.most_rows);
     hipLaunchKernelGGL((attn_shared_join_kernel<D>), dim3((unsigned)join), dim3(256), 0, stream, own, s, which, p.most_rows,
                        (int)p.items, p.splits);
     return hipGetLastError();

@@ -43,60 +43,60 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs &a, const Seq &s) {
 // Workgroups: row tile (the last first: under causality the longest),
 // split, key/value head.  Heads run fastest, so the tiles of one head meet in
 // one XCD's L2 where the number of heads is a multiple of 8.
-template <int D>
-__global__ void __launch_bounds__(256, 2)
-attn_tiles_kernel(const AttnArgs a, int which, int tiles, int splits) {
-    __shared__ TileLds<D> lds;
-    const int h = (int)(blockIdx.x % a.kv_heads), rest = (int)(blockIdx.x / a.kv_heads);
-    const int split = rest % splits, at = tiles - 1 - rest / splits;
-    int64_t before = 0;
-    const int b = uniform(find_seq(a.B, at, before, [&](int i) { return tiles_of(a, seq_of(a, i, which)); }));
-    if (b < 0) return;
-    const Seq s = seq_uniform(a, b, which);
-    const int G = a.q_heads / a.kv_heads, rows = s.n * G, r0 = (at - (int)uniform(before)) * kTileRows;
-    const int last = s.hi - 1;
-    const int *table = a.table + (int64_t)b * a.max_pages;
-    const int p_min = s.past + r0 / G, p_max = s.past + (min(r0 + kTileRows, rows) - 1) / G;
-    const Span64 span = span_of(a, p_min, p_max);
-    const int each = (span.nc + splits - 1) / splits;
-    const int c0 = min(split * each, span.nc), c1 = min(c0 + each, span.nc);
-    const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+struct PagedTiles {
+    using Args = AttnArgs;
+    struct Lds {};
+    AttnArgs a;
+    int which, tiles;
 
-    Rows32<D> w;
-    w.init(a, s, h, r0 + 32 * wave, rows);
-    if (c0 < c1) walk<D>(a, lds, w, table, last, h, span, c0, c1, p_min, p_max);
-
-    const float l = w.l + __shfl_xor(w.l, 32, 64);
-    const int row = r0 + 32 * wave + (lane & 31), half = lane >> 5;
-    if (row >= rows) return;
-    if (splits > 1) {
-        float *part = tile_part<D>(a, (int64_t)at * a.kv_heads + h, splits, split);
-        float *dst = part + (row - r0) * D + 4 * half;
+    __device__ __forceinline__ const AttnArgs &args() const { return a; }
+    template <int D>
+    __device__ __forceinline__ bool begin(Rows32<D> &w, TileWork<AttnArgs> &t, Lds &, int splits) const {
+        t.h = (int)(blockIdx.x % a.kv_heads);
+        const int rest = (int)(blockIdx.x / a.kv_heads);
+        t.split = rest % splits;
+        t.at = tiles - 1 - rest / splits;
+        int64_t before = 0;
+        const int b = uniform(find_seq(a.B, t.at, before, [&](int i) { return tiles_of(a, seq_of(a, i, which)); }));
+        if (b < 0) return false;
+        t.s = seq_uniform(a, b, which);
+        const int G = a.q_heads / a.kv_heads;
+        t.rows = t.s.n * G;
+        t.r0 = (t.at - (int)uniform(before)) * kTileRows;
+        t.last = t.s.hi - 1;
+        t.table = a.table + (int64_t)b * a.max_pages;
+        t.p_min = t.s.past + t.r0 / G;
+        t.p_max = t.s.past + (min(t.r0 + kTileRows, t.rows) - 1) / G;
+        t.span = span_of(a, t.p_min, t.p_max);
+        const int each = (t.span.nc + splits - 1) / splits;
+        t.c0 = min(t.split * each, t.span.nc);
+        t.c1 = min(t.c0 + each, t.span.nc);
+        w.init(a, t.s, t.h, t.r0 + 32 * uniform((int)(threadIdx.x >> 6)), t.rows);
+        return true;
+    }
+    template <int D>
+    __device__ __forceinline__ void end(const Rows32<D> &w, const TileWork<AttnArgs> &t, float l, int splits) const {
+        const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), G = a.q_heads / a.kv_heads;
+        const int row = t.r0 + 32 * wave + (lane & 31), half = lane >> 5;
+        if (row >= t.rows) return;
+        if (splits > 1) {
+            leave(w, l, tile_part<D>(a, (int64_t)t.at * a.kv_heads + t.h, splits, t.split), row - t.r0);
+            return;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int i = row / G, g = row - i * G;
+        const int64_t tok = t.s.first + i;
+        uint16_t *dst = a.o + tok * a.o_stride + (int64_t)(t.h * G + g) * D + 4 * half;
 #pragma unroll
         for (int n = 0; n < D / 32; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
-                    f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
-        if (half == 0) {
-            part[kTileRows * D + 2 * (row - r0)] = w.m;
-            part[kTileRows * D + 2 * (row - r0) + 1] = l;
-        }
-        return;
+                *reinterpret_cast<uint2 *>(dst + 32 * n + 8 * j) =
+                    make_uint2(narrow2a(w.o[n][4 * j] * inv, w.o[n][4 * j + 1] * inv),
+                               narrow2a(w.o[n][4 * j + 2] * inv, w.o[n][4 * j + 3] * inv));
+        if (a.lse && half == 0) a.lse[tok * a.q_heads + t.h * G + g] = (w.m + __builtin_amdgcn_logf(l)) * kLn2;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int i = row / G, g = row - i * G;
-    const int64_t t = s.first + i;
-    uint16_t *dst = a.o + t * a.o_stride + (int64_t)(h * G + g) * D + 4 * half;
-#pragma unroll
-    for (int n = 0; n < D / 32; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint2 *>(dst + 32 * n + 8 * j) =
-                make_uint2(narrow2a(w.o[n][4 * j] * inv, w.o[n][4 * j + 1] * inv),
-                           narrow2a(w.o[n][4 * j + 2] * inv, w.o[n][4 * j + 3] * inv));
-    if (a.lse && half == 0) a.lse[t * a.q_heads + h * G + g] = (w.m + __builtin_amdgcn_logf(l)) * kLn2;
-}
+};
 
 // Joins the pieces of a row: a wave a row.
 template <int D>
@@ -140,7 +140,8 @@ hipError_t launch(const AttnArgs &a, int which, hipStream_t stream) {
     const int64_t grid = (int64_t)p.tiles * p.splits * a.kv_heads;
     const int64_t join = (int64_t)p.tiles * a.kv_heads * (kTileRows / 4);
     if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((attn_tiles_kernel<D>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.tiles, p.splits);
+    const PagedTiles k{a, which, p.tiles};
+    hipLaunchKernelGGL((attn_tiles_kernel<D, PagedTiles>), dim3((unsigned)grid), dim3(256), 0, stream, k, p.splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attn_tiles_join_kernel<D>), dim3((unsigned)join), dim3(256), 0, stream, a, which, p.splits);
