@@ -372,7 +372,7 @@ attn_split_kernel(const K k, int which, int most_rows) {
     for (int i = threadIdx.x & 63; i < a.B; i += 64) {
         const uint32_t u = (uint32_t)units(seq_of(k.of(i), i, which));
 #pragma unroll
-        for (int z = 0; z < kSizes; ++z) count[z] += (float)((u + even + k - 1) / (uint32_t)(even + k));
+        for (int z = 0; z < kSizes; ++z) count[z] += (float)((u + even + z - 1) / (uint32_t)(even + z));
     }
     int more = 0;
 #pragma unroll
