@@ -51,13 +51,12 @@ __device__ __forceinline__ bool holds(const PartArgs &a, int j) { return (bool)(
 // The chunks of 64 tokens that the rows at positions [p_min, p_max] need:
 // `ns` chunks of first tokens, then those from `lo0` on.
 struct Span64 {
-    int s0, lo0, ns, nc;
-    __device__ __forceinline__ int start(int c) const { return c < ns ? s0 + c * kChunk : lo0 + (c - ns) * kChunk; }
+    int lo0, ns, nc;
+    __device__ __forceinline__ int start(int c) const { return c < ns ? c * kChunk : lo0 + (c - ns) * kChunk; }
 };
 __device__ __forceinline__ Span64 span_of(const AttnArgs &a, int p_min, int p_max) {
     Span64 s;
     const int lo = a.window > 0 ? max(p_min - a.window + 1, 0) : 0;
-    s.s0 = 0;
     s.lo0 = lo & ~(kChunk - 1);
     s.ns = (min(a.sinks, s.lo0) + kChunk - 1) / kChunk;
     s.nc = s.ns + (max(p_max + 1 - s.lo0, 0) + kChunk - 1) / kChunk;
@@ -66,9 +65,9 @@ __device__ __forceinline__ Span64 span_of(const AttnArgs &a, int p_min, int p_ma
 __device__ __forceinline__ Span64 span_of(const PartArgs &a, int p_min, int p_max) {
     Span64 s;
     const int lo = max(a.window > 0 ? max(p_min - a.window + 1, 0) : 0, a.from);
-    s.s0 = a.from & ~(kChunk - 1);
     s.lo0 = lo & ~(kChunk - 1);
-    s.ns = max(min(min(a.sinks, s.lo0), a.upto) - s.s0 + kChunk - 1, 0) / kChunk;
+    const int first = min(min(a.sinks, s.lo0), a.upto);
+    s.ns = first > a.from ? (first + kChunk - 1) / kChunk : 0;      // from chunk 0 on, also those before `from`
     s.nc = s.ns + (max(min(p_max + 1, a.upto) - s.lo0, 0) + kChunk - 1) / kChunk;
     return s;
 }
