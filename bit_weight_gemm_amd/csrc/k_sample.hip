@@ -26,6 +26,7 @@ typedef unsigned long long u64;
 
 struct Best {      // of a row or a part of it
     float top, low;      // largest and smallest above -inf; -inf and inf where there is none
+    int at;              // the first of the largest
 };
 
 struct Shared {
@@ -33,9 +34,10 @@ struct Shared {
     u64 mass[kBins];
     u64 key[kList], w[kList];
     u64 sum[kWavesS], sum2[kWavesS];
-    float f0[kWavesS], f1[kWavesS];
+    Best best[kWavesS];
     uint32_t n, pick, lo, hi;
     u64 at, upto, all;
+    double exp[64];      // 2^(j / 64)
 };
 
 // A row as 16-byte blocks: the first may begin before it, the last end behind it.
@@ -51,8 +53,8 @@ struct Row {
         before = (int)((a & 15) / sizeof(T));
         blocks = (before + V + E - 1) / E;
     }
-    // NaN is -inf, and -0 is 0.
-    __device__ __forceinline__ static float tidy(float v) { return v != v ? -__builtin_inff() : v + 0.0f; }
+    // NaN is -inf.
+    __device__ __forceinline__ static float tidy(float v) { return fmaxf(v, -__builtin_inff()); }
     // Element e of a block.
     __device__ __forceinline__ static float value(const u32x4_t &w, int e) {
         if constexpr (sizeof(T) == 4) return tidy(__uint_as_float(w[e]));
@@ -62,31 +64,50 @@ struct Row {
         if constexpr (sizeof(T) == 4) return tidy(x[i]);
         else return tidy(bf16_to_f32(x[i]));
     }
-    // f(index, value) of the elements of blocks [b0, b1), each wave a run of them.
+    __device__ __forceinline__ int index(int b, int e) const { return b * E + e - before; }
+    // Block b, with NaN for what lies outside the row.
+    __device__ __forceinline__ u32x4_t block(int b) const {
+        u32x4_t w = p[min(b, blocks - 1)];
+        if (b == 0 || b >= blocks - 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int i = index(b, e);
+                if (i >= 0 && i < V) continue;
+                if constexpr (sizeof(T) == 4) w[e] = 0x7FC00000u;
+                else w[e >> 1] = e & 1 ? w[e >> 1] | 0x7FC00000u : w[e >> 1] | 0x7FC0u;
+            }
+        }
+        return w;
+    }
+    // f(index of the first, values) of four elements at a time of blocks [b0, b1), each
+    // wave a run of them.
     template <class F>
     __device__ __forceinline__ void each(int b0, int b1, F f) const {
         const int wave = threadIdx.x >> 6, per = ((b1 - b0 + kWavesS - 1) / kWavesS + 63) & ~63;
         run(min(b0 + wave * per, b1), min(b0 + wave * per + per, b1), f);
     }
-    // The same of one wave's blocks.
+    // The same of one wave's blocks.  Elements outside the row come as -inf.
     template <class F>
     __device__ __forceinline__ void run(int b0, int b1, F f) const {
-        constexpr int U = 4;
+        constexpr int U = 2;      // loads under way beside the one in use
         const int lane = threadIdx.x & 63;
-        for (int b = b0 + lane; b - lane < b1; b += 64 * U) {
-            u32x4_t w[U];
+        u32x4_t w[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) w[k] = p[min(b + 64 * k, blocks - 1)];
+        for (int k = 0; k < U; ++k) w[k] = block(b0 + lane + 64 * k < b1 ? b0 + lane + 64 * k : blocks);
+        for (int b = b0 + lane; b - lane < b1; b += 64 * U)
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                if (b + 64 * k >= b1) continue;
+                const u32x4_t v = w[k];
+                const int next = b + 64 * (k + U);
+                if (next - lane < b1) w[k] = block(next < b1 ? next : blocks);
+                if (b + 64 * k - lane < b1)
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int i = (b + 64 * k) * E + e - before;
-                    if (i >= 0 && i < V) f(i, value(w[k], e));
-                }
+                    for (int e = 0; e < E; e += 4) {
+                        const float x[4] = {value(v, e), value(v, e + 1), value(v, e + 2), value(v, e + 3)};
+                        f(index(b + 64 * k, e), x);
+                    }
+                __builtin_amdgcn_sched_barrier(0);
             }
-        }
     }
 };
 
@@ -126,20 +147,25 @@ __device__ __forceinline__ u64 group_before(u64 v, u64 (&tmp)[kWavesS]) {
     return b;
 }
 
-__device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t u = __float_as_uint(x);
+__device__ __forceinline__ uint32_t key_of(float x) {      // -0 is 0
+    const uint32_t u = __float_as_uint(x + 0.0f);
     return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ u64 full_key(float x, int i) { return (u64)key_of(x) << 32 | (0xFFFFFFFFu - (uint32_t)i); }
 
+__device__ __forceinline__ float value_of(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 // What a request asks of a row, and the row's scale.
 struct Ask {
     double c;            // log2(e) / T
-    float top;
-    double bins;         // parts of y's range to a unit
     double p, m;         // p >= 1: no cut; m in weights
+    float top;
+    float far;           // logits further than this below the top have no weight
+    float parts;         // histogram's parts to a logit
     uint32_t k;          // 0: no cut
-    bool cut;            // by k or p: the histogram is needed
+    bool first;          // the first of the largest
 
     __device__ __forceinline__ void set(const SampleArgs &a, int row) {
         double t = a.temperature ? (double)a.temperature[row] : 1.0;
@@ -149,41 +175,57 @@ struct Ask {
         k = kk > 0 && kk < a.V ? (uint32_t)kk : 0;
         if (!(p < 1.0)) p = 1.0;
         m = (m > 0.0 ? fmin(m, 1.0) : 0.0) * (double)(1ull << kOneShift);
-        if (!(t > 0.0)) {      // the first of the largest
-            t = 1.0;
-            k = 1;
-            p = 1.0;
-            m = 0.0;
-        }
+        first = !(t > 0.0);
+        if (first) t = 1.0;
         c = kLog2eD / t;
-        cut = k > 0 || p < 1.0;
     }
+    // By k or p: the histogram is needed.
+    __device__ __forceinline__ bool cut() const { return !first && (k > 0 || p < 1.0); }
     __device__ __forceinline__ void scale(const Best &b) {
         top = b.top;
-        const double range = ((double)b.top - (double)b.low) * c;      // NaN or inf: an infinite top
-        bins = (double)(kBins - 1) / (range < kMostY ? fmax(range, 1e-30) : kMostY);
+        // Infinite at the highest temperatures; 0 where only infinite logits have weight.
+        far = b.top == __builtin_inff() ? 0.0f : (float)((kMostY + 1.0) / c);
+        parts = (float)(kBins - 1) / fmaxf(fminf(b.top - b.low, far), 1e-30f);      // inf - inf: far
     }
-    __device__ __forceinline__ double y_of(float x) const {
-        const double y = fmin(((double)top - (double)x) * c, 64.0);      // also where that is inf - inf
-        return x == top ? 0.0 : y;
+    // Whether x may have weight.
+    __device__ __forceinline__ bool near(float x) const { return x > -__builtin_inff() && !(top - x > far); }
+    __device__ __forceinline__ int bin_of(float x) const { return min((int)((top - x) * parts), kBins - 1); }
+    // 2^-y in steps of 2^-44 of N logits that are near(); of others anything.  -y = n + j / 64 + g
+    // with whole n and j, |g| <= 1/128: 2^(j / 64) from a table, 2^g by the polynomial
+    // through Chebyshev's points, within 2^-48 relative.  Several at once, since one is a
+    // chain of dependent instructions.
+    template <int N>
+    __device__ __forceinline__ void weights(const Shared &s, const float (&x)[N], u64 (&w)[N]) const {
+        constexpr double kRound = 6755399441055744.0 / 64.0;      // 1.5 2^52 / 64: sums round to 64ths
+        double d[N], t[N], g[N], v[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = fmax((double)top - (double)x[i], 0.0);      // inf - inf: 0
+#pragma unroll
+        for (int i = 0; i < N; ++i) t[i] = __builtin_fma(d[i], -c, kRound);
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = __builtin_fma(d[i], -c, kRound - t[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = 0.009618140880813336;
+            v[i] = __builtin_fma(v[i], g[i], 0.05550421039181774);
+            v[i] = __builtin_fma(v[i], g[i], 0.24022650695892073);
+            v[i] = __builtin_fma(v[i], g[i], 0.6931471805583931);
+            v[i] = __builtin_fma(v[i], g[i], 1.0);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int k = (int)(uint32_t)__builtin_bit_cast(u64, t[i]);      // 64 n + j
+            const double p = v[i] * s.exp[k & 63];
+            const u64 scaled = __builtin_bit_cast(u64, p) + ((u64)(uint32_t)((k >> 6) + kOneShift) << 52);
+            const double whole = __builtin_bit_cast(double, scaled) + 4503599627370496.0;      // 2^52: rounds
+            w[i] = __builtin_bit_cast(u64, whole) & 0xFFFFFFFFFFFFFull;
+        }
     }
-    __device__ __forceinline__ int bin_of(double y) const { return (int)fmin(y * bins, (double)(kBins - 1)); }
-    // 2^-y in steps of 2^-44, y in [0, 64]: the polynomial through Chebyshev's points of
-    // [-1/2, 1/2], within 2^-45 of 2^f relative.
-    __device__ __forceinline__ static u64 weight(double y) {
-        const double n = __builtin_rint(-y), f = -y - n;
-        double v = 1.0205905320493103e-07;
-        v = __builtin_fma(v, f, 1.3259645243929057e-06);
-        v = __builtin_fma(v, f, 1.5252672925346873e-05);
-        v = __builtin_fma(v, f, 0.00015403433751254997);
-        v = __builtin_fma(v, f, 0.0013333558200793719);
-        v = __builtin_fma(v, f, 0.009618129193934304);
-        v = __builtin_fma(v, f, 0.05550410866465168);
-        v = __builtin_fma(v, f, 0.2402265069564034);
-        v = __builtin_fma(v, f, 0.6931471805599462);
-        v = __builtin_fma(v, f, 1.0000000000000135);
-        v = __builtin_amdgcn_ldexp(v, (int)n + kOneShift) + 4503599627370496.0;      // 2^52: rounds to whole numbers
-        return __builtin_bit_cast(u64, v) & 0xFFFFFFFFFFFFFull;
+    __device__ __forceinline__ u64 weight(const Shared &s, float x) const {
+        const float one[1] = {x};
+        u64 w[1];
+        weights(s, one, w);
+        return w[0];
     }
 };
 
@@ -191,27 +233,28 @@ struct Ask {
 template <class T>
 __device__ __forceinline__ Best best_of(const Row<T> &r, int b0, int b1, Shared &s) {
     float top = -__builtin_inff(), low = __builtin_inff();
-    r.each(b0, b1, [&](int, float x) {
-        top = fmaxf(top, x);
-        low = x > -__builtin_inff() ? fminf(low, x) : low;
+    int at = 0x7FFFFFFF;
+    r.each(b0, b1, [&](int i, const float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            at = x[e] > top ? i + e : at;      // a lane's elements come in the order of their index
+            top = fmaxf(top, x[e]);
+            low = fminf(low, x[e] > -__builtin_inff() ? x[e] : low);
+        }
     });
+    const auto join = [&](float t, float l, int i) {
+        at = t > top ? i : t == top ? min(at, i) : at;
+        top = fmaxf(top, t);
+        low = fminf(low, l);
+    };
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor(top, o, 64));
-        low = fminf(low, __shfl_xor(low, o, 64));
-    }
+    for (int o = 32; o > 0; o >>= 1) join(__shfl_xor(top, o, 64), __shfl_xor(low, o, 64), __shfl_xor(at, o, 64));
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) {
-        s.f0[threadIdx.x >> 6] = top;
-        s.f1[threadIdx.x >> 6] = low;
-    }
+    if ((threadIdx.x & 63) == 0) s.best[threadIdx.x >> 6] = Best{top, low, at};
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWavesS; ++i) {
-        top = fmaxf(top, s.f0[i]);
-        low = fminf(low, s.f1[i]);
-    }
-    return Best{top, low};
+    for (int i = 0; i < kWavesS; ++i) join(s.best[i].top, s.best[i].low, s.best[i].at);
+    return Best{top, low, at};
 }
 
 __device__ __forceinline__ void clear(Shared &s) {
@@ -222,23 +265,35 @@ __device__ __forceinline__ void clear(Shared &s) {
     __syncthreads();
 }
 
-template <class T>
-__device__ __forceinline__ void histogram(const Row<T> &r, int b0, int b1, const Ask &q, Shared &s) {
-    r.each(b0, b1, [&](int, float x) {
-        const double y = q.y_of(x);
-        const int b = q.bin_of(y);
-        atomicAdd(&s.count[b], 1u);
-        atomicAdd(&s.mass[b], Ask::weight(y));
+template <class T, class Part>
+__device__ __forceinline__ void count_parts(const Row<T> &r, int b0, int b1, const Ask &q, Shared &s, Part part) {
+    r.each(b0, b1, [&](int, const float (&x)[4]) {
+        int at[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) at[e] = q.near(x[e]) ? part(x[e]) : -1;
+        if ((at[0] & at[1] & at[2] & at[3]) == -1) return;
+        u64 w[4];
+        q.weights(s, x, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at[e] >= 0) {
+                atomicAdd(&s.count[at[e]], 1u);
+                atomicAdd(&s.mass[at[e]], w[e]);
+            }
     });
     __syncthreads();
+}
+template <class T>
+__device__ __forceinline__ void histogram(const Row<T> &r, int b0, int b1, const Ask &q, Shared &s) {
+    count_parts(r, b0, b1, q, s, [&](float x) { return q.bin_of(x); });
 }
 
 struct Upto {
     uint32_t count;
     u64 mass;
 };
-// The first bin b at which reached(sums through b) holds, and the sums before it; the
-// last bin where it holds nowhere.  reached() does not go back as the sums grow.
+// The first bin b at which reached(sums through b) holds, and the sums before it; -1
+// where it holds nowhere.  reached() does not go back as the sums grow.
 template <class F>
 __device__ __forceinline__ int first_bin(Shared &s, Upto &before, F reached) {
     constexpr int N = kBins / kThreads;
@@ -252,7 +307,7 @@ __device__ __forceinline__ int first_bin(Shared &s, Upto &before, F reached) {
         ms += m[i];
     }
     u64 cb = group_before(cs, s.sum), mb = group_before(ms, s.sum2);
-    if (threadIdx.x == 0) s.pick = kBins - 1;
+    if (threadIdx.x == 0) s.pick = 0xFFFFFFFFu;
     __syncthreads();
     const bool had = threadIdx.x > 0 && reached(Upto{(uint32_t)cb, mb});
     u64 c0 = cb, m0 = mb;
@@ -260,8 +315,7 @@ __device__ __forceinline__ int first_bin(Shared &s, Upto &before, F reached) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const bool now = reached(Upto{(uint32_t)(cb + c[i]), mb + m[i]});
-        const bool last = threadIdx.x == kThreads - 1 && i == N - 1;
-        if (mine < 0 && !had && (now || last)) {
+        if (mine < 0 && !had && now) {
             mine = threadIdx.x * N + i;
             c0 = cb;
             m0 = mb;
@@ -276,13 +330,13 @@ __device__ __forceinline__ int first_bin(Shared &s, Upto &before, F reached) {
     }
     __syncthreads();
     before = Upto{s.lo, s.at};
-    const int b = s.pick;
+    const int b = (int)s.pick;
     __syncthreads();
     return b;
 }
 
-// The elements of a row for which in(key, y) holds, in the list while it has room; their
-// number, and their smallest and largest keys.
+// The elements of a row with weight for which in(x) holds, in the list while it has room;
+// their number, and their smallest and largest keys.
 template <class T, class F>
 __device__ __forceinline__ uint32_t gather(const Row<T> &r, const Ask &q, Shared &s, F in) {
     if (threadIdx.x == 0) {
@@ -292,18 +346,16 @@ __device__ __forceinline__ uint32_t gather(const Row<T> &r, const Ask &q, Shared
     }
     __syncthreads();
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    r.each(0, r.blocks, [&](int i, float x) {
-        const double y = q.y_of(x);
-        const uint32_t k = key_of(x);
-        if (in(k, y)) {
-            lo = min(lo, k);
-            hi = max(hi, k);
-            const uint32_t at = atomicAdd(&s.n, 1u);
-            if (at < kList) {
-                s.key[at] = full_key(x, i);
-                s.w[at] = Ask::weight(y);
+    r.each(0, r.blocks, [&](int i, const float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (q.near(x[e]) && in(x[e])) {
+                const uint32_t k = key_of(x[e]);
+                lo = min(lo, k);
+                hi = max(hi, k);
+                const uint32_t at = atomicAdd(&s.n, 1u);
+                if (at < kList) s.key[at] = full_key(x[e], i + e);
             }
-        }
     });
     if (hi >= lo) {
         atomicMin(&s.lo, lo);
@@ -313,24 +365,53 @@ __device__ __forceinline__ uint32_t gather(const Row<T> &r, const Ask &q, Shared
     return s.n;
 }
 
-// Of the listed elements, in order: the one at which reached(sums through it) begins to
-// hold, and the sums through it.  s.at and s.upto: its key, and the mass.
+// The workgroup's (key, w), a thread one, in descending order of the keys of the first
+// `n` threads (the others' keys are taken as 0).
+__device__ __forceinline__ void sort_down(Shared &s, uint32_t n, u64 &key, u64 &w) {
+    const int tid = threadIdx.x;
+    if (tid >= (int)n) key = 0;
+    for (int size = 2; size < 2 * (int)n; size *= 2)
+        for (int d = size / 2; d > 0; d /= 2) {
+            u64 k2, w2;
+            if (d >= 64) {
+                __syncthreads();
+                s.key[tid] = key;
+                s.w[tid] = w;
+                __syncthreads();
+                k2 = s.key[tid ^ d];
+                w2 = s.w[tid ^ d];
+            } else {
+                k2 = __shfl_xor(key, d, 64);
+                w2 = __shfl_xor(w, d, 64);
+            }
+            const bool down = (tid & size) == 0, upper = (tid & d) == 0;      // upper: keeps the larger where down
+            if ((k2 > key) == (down == upper) && k2 != key) {
+                key = k2;
+                w = w2;
+            }
+        }
+    __syncthreads();
+}
+// The listed elements in order, with their weights.
+__device__ __forceinline__ void sort_list(const Ask &q, Shared &s, uint32_t n) {
+    u64 key = threadIdx.x < n ? s.key[threadIdx.x] : 0, w = 0;
+    if (threadIdx.x < n) w = q.weight(s, value_of((uint32_t)(key >> 32)));
+    sort_down(s, n, key, w);
+    s.key[threadIdx.x] = key;
+    s.w[threadIdx.x] = w;
+    __syncthreads();
+}
+// Of the list in order, the element at which reached(sums through it) begins to hold.
+// s.at and s.upto: its key, and the mass through it; s.n: its place.
 template <class F>
 __device__ __forceinline__ void first_listed(Shared &s, uint32_t n, const Upto &base, F reached) {
-    __syncthreads();
-    if (threadIdx.x < n) {
-        const u64 k = s.key[threadIdx.x], w = s.w[threadIdx.x];
-        Upto b = base;
-        for (uint32_t j = 0; j < n; ++j)
-            if (s.key[j] > k) {
-                ++b.count;
-                b.mass += s.w[j];
-            }
-        const Upto t{b.count + 1, b.mass + w};
-        if (reached(t) && (b.count == base.count || !reached(b))) {
-            s.at = k;
-            s.upto = t.mass;
-        }
+    const uint32_t i = threadIdx.x;
+    const u64 w = i < n ? s.w[i] : 0;
+    const u64 before = base.mass + group_before(w, s.sum);
+    if (i < n && reached(Upto{base.count + i + 1, before + w}) && (i == 0 || !reached(Upto{base.count + i, before}))) {
+        s.at = s.key[i];
+        s.upto = before + w;
+        s.lo = i;
     }
     __syncthreads();
 }
@@ -340,37 +421,33 @@ __device__ __forceinline__ void first_listed(Shared &s, uint32_t n, const Upto &
 // are one key, whose elements count by index.
 template <class T, class F>
 __device__ __forceinline__ void border(const Row<T> &r, const Ask &q, Shared &s, int bin, Upto base, F reached) {
-    uint32_t n = gather(r, q, s, [&](uint32_t, double y) { return q.bin_of(y) == bin; });
+    uint32_t n = gather(r, q, s, [&](float x) { return q.bin_of(x) == bin; });
     uint32_t lo = s.lo, hi = s.hi;
     while (n > kList && lo < hi) {
         const int shift = max(32 - __clz(hi - lo) - 11, 0);      // parts below kBins
         __syncthreads();
         clear(s);
-        r.each(0, r.blocks, [&](int, float x) {
-            const double y = q.y_of(x);
+        count_parts(r, 0, r.blocks, q, s, [&](float x) {
             const uint32_t k = key_of(x);
-            if (k >= lo && k <= hi) {
-                atomicAdd(&s.count[(hi - k) >> shift], 1u);
-                atomicAdd(&s.mass[(hi - k) >> shift], Ask::weight(y));
-            }
+            return k >= lo && k <= hi ? (int)((hi - k) >> shift) : -1;
         });
-        __syncthreads();
         Upto b;
         const uint32_t part = first_bin(s, b, [&](const Upto &t) { return reached(Upto{base.count + t.count, base.mass + t.mass}); });
         base.count += b.count;
         base.mass += b.mass;
         const uint32_t top = hi - (part << shift), width = (1u << shift) - 1;
         const uint32_t bottom = max(lo, top >= width ? top - width : 0u);
-        n = gather(r, q, s, [&](uint32_t k, double) { return k >= bottom && k <= top; });
+        n = gather(r, q, s, [&](float x) { return key_of(x) >= bottom && key_of(x) <= top; });
         lo = s.lo;
         hi = s.hi;
     }
     if (n <= kList) {
+        sort_list(q, s, n);
         first_listed(s, n, base, reached);
         return;
     }
     // one key: the number of its elements that are wanted, then the last one's index
-    const u64 w = s.w[0];
+    const u64 w = q.weight(s, value_of(lo));
     uint32_t a = 1, b = n;      // the fewest for which reached() holds
     while (a < b) {
         const uint32_t mid = a + (b - a) / 2;
@@ -386,23 +463,28 @@ __device__ __forceinline__ void border(const Row<T> &r, const Ask &q, Shared &s,
             if (wave == 0) {
                 const int at = b0 + (threadIdx.x & 63);
                 uint32_t c = 0;
-                r.run(b0, b1, [&](int, float x) { c += key_of(x) == key; });
+                r.run(b0, b1, [&](int, const float (&x)[4]) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) c += key_of(x[e]) == key;
+                });
                 const uint32_t in = (uint32_t)wave_scan_u64(c);
                 if (in >= want && in - c < want) {
                     uint32_t left = want - (in - c);
-                    const u32x4_t v = r.p[at];
+                    const u32x4_t v = r.block(at);
 #pragma unroll
                     for (int e = 0; e < Row<T>::E; ++e) {
-                        const int i = at * Row<T>::E + e - r.before;
-                        if (i >= 0 && i < r.V && key_of(Row<T>::value(v, e)) == key && --left == 0)
-                            s.at = (u64)key << 32 | (0xFFFFFFFFu - (uint32_t)i);
+                        const float x = Row<T>::value(v, e);
+                        if (key_of(x) == key && --left == 0) s.at = full_key(x, r.index(at, e));
                     }
                 }
             }
             break;
         }
         u64 c = 0;
-        r.each(b0, b1, [&](int, float x) { c += key_of(x) == key; });
+        r.each(b0, b1, [&](int, const float (&x)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c += key_of(x[e]) == key;
+        });
         c = wave_sum_u64(c);
         __syncthreads();
         if ((threadIdx.x & 63) == 0) s.sum[wave] = c;
@@ -419,20 +501,30 @@ __device__ __forceinline__ void border(const Row<T> &r, const Ask &q, Shared &s,
 }
 
 // The first index at which the kept weights' sum passes u of them all: parts of the row
-// in turn, each a sixteenth of the one before.  all: the sum of every weight.
+// in turn, each a sixteenth of the one before.  s.all: the sum of every weight, where
+// nothing has been cut.
 template <class T>
 __device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, double u, u64 tau) {
     int b0 = 0, b1 = r.blocks;
     u64 before = 0;
     double target = 0.0;
+    // the least that is kept, for a test before the key's
+    const float least = tau ? value_of((uint32_t)(tau >> 32)) : -__builtin_inff();
+    const auto kept_of = [&](int i, float x, u64 w) { return full_key(x, i) >= tau && (double)w >= q.m ? w : 0ull; };
 #pragma unroll 1
     for (bool first = true; first || b1 - b0 > 64; first = false) {
         const int wave = threadIdx.x >> 6, per = ((b1 - b0 + kWavesS - 1) / kWavesS + 63) & ~63;
         u64 mine = 0, total = 0;
-        r.each(b0, b1, [&](int i, float x) {
-            const u64 w = Ask::weight(q.y_of(x));
-            total += w;
-            mine += full_key(x, i) >= tau && (double)w >= q.m ? w : 0ull;
+        r.each(b0, b1, [&](int i, const float (&x)[4]) {
+            if (!(x[0] >= least || x[1] >= least || x[2] >= least || x[3] >= least)) return;
+            u64 w[4];
+            q.weights(s, x, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = x[e] >= least && q.near(x[e]) ? w[e] : 0;
+                total += w[e];
+                mine += kept_of(i + e, x[e], w[e]);
+            }
         });
         mine = wave_sum_u64(mine);
         total = wave_sum_u64(total);
@@ -474,13 +566,11 @@ __device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, do
     if (threadIdx.x < 64) {
         const int b = b0 + threadIdx.x;
         u64 w[Row<T>::E], mine = 0;
-        const u32x4_t v = r.p[min(b, r.blocks - 1)];
+        const u32x4_t v = r.block(b < b1 ? b : r.blocks);
 #pragma unroll
         for (int e = 0; e < Row<T>::E; ++e) {
-            const int i = b * Row<T>::E + e - r.before;
             const float x = Row<T>::value(v, e);
-            const u64 t = Ask::weight(q.y_of(x));
-            w[e] = b < b1 && i >= 0 && i < r.V && full_key(x, i) >= tau && (double)t >= q.m ? t : 0ull;
+            w[e] = q.near(x) && x >= least ? kept_of(r.index(b, e), x, q.weight(s, x)) : 0ull;
             mine += w[e];
         }
         u64 at = before + wave_scan_u64(mine) - mine;
@@ -488,7 +578,7 @@ __device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, do
 #pragma unroll
         for (int e = 0; e < Row<T>::E; ++e) {
             at += w[e];
-            const int i = b * Row<T>::E + e - r.before;
+            const int i = r.index(b, e);
             if (w[e] != 0) {
                 held = i;
                 if ((double)at > target) hit = min(hit, i);
@@ -505,57 +595,66 @@ __device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, do
     return (int)s.pick;
 }
 
-// The same on the listed elements, in the order of their index.
-__device__ __forceinline__ int draw_listed(const Ask &q, Shared &s, double u, u64 tau, uint32_t n) {
-    const auto kept_of = [&](uint32_t j) { return s.key[j] >= tau && (double)s.w[j] >= q.m ? s.w[j] : 0ull; };
-    const u64 mine = threadIdx.x < n ? kept_of(threadIdx.x) : 0ull;
-    const double target = u * (double)group_sum(mine, s.sum);
+// The same on the list in order: its first `kept` elements, in the order of their index.
+__device__ __forceinline__ int draw_listed(const Ask &q, Shared &s, double u, uint32_t kept) {
+    u64 w = threadIdx.x < kept ? s.w[threadIdx.x] : 0;
+    if (!((double)w >= q.m)) w = 0;
+    const double target = u * (double)group_sum(w, s.sum);
+    u64 key = (uint32_t)s.key[threadIdx.x];      // 2^32 - 1 - index
     if (threadIdx.x == 0) {
         s.pick = 0xFFFFFFFFu;
         s.hi = 0;
     }
-    __syncthreads();
-    if (mine != 0) {
-        const uint32_t at = (uint32_t)s.key[threadIdx.x];      // 2^32 - 1 - index
-        u64 to = 0;
-        for (uint32_t j = 0; j < n; ++j) to += (uint32_t)s.key[j] >= at ? kept_of(j) : 0ull;
-        if ((double)to > target) atomicMin(&s.pick, 0xFFFFFFFFu - at);
-        atomicMax(&s.hi, 0xFFFFFFFFu - at);      // u at or above 1: the last one
+    sort_down(s, kept, key, w);
+    const u64 upto = group_before(w, s.sum) + w;
+    if (w != 0) {
+        const uint32_t i = 0xFFFFFFFFu - (uint32_t)key;
+        if ((double)upto > target) atomicMin(&s.pick, i);
+        atomicMax(&s.hi, i);      // u at or above 1: the last one
     }
     __syncthreads();
     return (int)(s.pick == 0xFFFFFFFFu ? s.hi : s.pick);
 }
 
-// The row's token, from its histogram in s where q.cut.
+// The row's token, from its histogram in s where q.cut().
 template <class T>
-__device__ __forceinline__ void choose(const SampleArgs &a, int row, const Row<T> &r, const Ask &q, Shared &s) {
+__device__ __forceinline__ void choose(const SampleArgs &a, int row, const Row<T> &r, const Ask &q, const Best &best, Shared &s) {
     const double u = a.u[row] >= 0.0f ? (double)a.u[row] : 0.0;      // NaN: 0
     u64 tau = 0, all = 0;
     uint32_t n = 0;
     bool listed = false;
-    if (q.cut) {
+    const bool cut = q.cut();
+    if (cut) {
         u64 m = 0;
         for (int i = threadIdx.x; i < kBins; i += kThreads) m += s.mass[i];
         all = group_sum(m, s.sum);
         // the border by k, then that by p of what k has left
         bool by_k = q.k > 0;
+        u64 left = all;
         double target = q.p * (double)all;
         const auto reached = [&](const Upto &t) { return by_k ? t.count >= q.k : t.count > 0 && (double)t.mass >= target; };
 #pragma unroll 1
         for (int step = 0;; ++step) {
+            int bin = 0;
             if (!listed) {
                 Upto base;
-                const int bin = first_bin(s, base, reached);
+                bin = first_bin(s, base, reached);
                 // every element up to the border's bin in the list, if it has room
-                listed = step == 0 && base.count + s.count[bin] <= kList;
-                if (listed) n = gather(r, q, s, [&](uint32_t, double y) { return q.bin_of(y) <= bin; });
-                else border(r, q, s, bin, base, reached);
+                listed = step == 0 && bin >= 0 && base.count + s.count[bin] <= kList;
+                if (listed) {
+                    n = gather(r, q, s, [&](float x) { return q.bin_of(x) <= bin; });
+                    sort_list(q, s, n);
+                } else if (bin >= 0) border(r, q, s, bin, base, reached);
             }
             if (listed) first_listed(s, n, Upto{0, 0}, reached);
-            tau = max(tau, s.at);
+            if (bin >= 0) {      // else all that have weight are kept
+                tau = max(tau, s.at);
+                left = s.upto;
+                if (listed) n = s.lo + 1;
+            }
             if (!by_k || !(q.p < 1.0)) break;
             by_k = false;
-            target = q.p * (double)s.upto;
+            target = q.p * (double)left;
             if (!listed) {      // the search for k's border has used the histogram's room
                 __syncthreads();
                 clear(s);
@@ -563,17 +662,19 @@ __device__ __forceinline__ void choose(const SampleArgs &a, int row, const Row<T
             }
         }
     }
-    int token;
+    int token = best.at;
     if (listed) {
-        token = draw_listed(q, s, u, tau, n);
-    } else {
-        token = draw(r, q, s, u, tau);
-        all = s.all;
+        token = draw_listed(q, s, u, n);
+    } else if (!q.first || a.logprob) {
+        const int drawn = draw(r, q, s, u, tau);
+        if (!q.first) token = drawn;
+        if (!cut) all = s.all;
     }
     if (threadIdx.x == 0) {
         a.token[row] = token;
         if (a.logprob) {
-            const double y = q.y_of(r.at(token));
+            const float x = r.at(token);
+            const double y = x == q.top ? 0.0 : ((double)q.top - (double)x) * q.c;
             a.logprob[row] = (float)(-y * kLn2D - log((double)all * (1.0 / (double)(1ull << kOneShift))));
         }
     }
@@ -602,11 +703,12 @@ sample_kernel(const SampleArgs a) {
     Ask q;
     q.set(a, row);
     clear(s);
+    if (threadIdx.x < 64) s.exp[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
     const Best b = best_of(r, 0, r.blocks, s);
     if (none_left(a, row, b)) return;
     q.scale(b);
-    if (q.cut) histogram(r, 0, r.blocks, q, s);
-    choose(a, row, r, q, s);
+    if (q.cut()) histogram(r, 0, r.blocks, q, s);
+    choose(a, row, r, q, b, s);
 }
 
 }  // namespace
