@@ -18,9 +18,11 @@ namespace biloco {
 
 namespace {
 
+constexpr int kMostSlices = 16;
 constexpr int kThreads = 1024, kWavesS = kThreads / 64, kBins = 2048, kList = 1024;
 constexpr int kOneShift = 44;                    // w = 1 is 1 << 44
 constexpr double kMostY = 45.0;                  // from here on a weight rounds to 0
+constexpr float kLargest = 3.402823466e38f;
 constexpr double kLog2eD = 1.4426950408889634, kLn2D = 0.6931471805599453;
 typedef unsigned long long u64;
 
@@ -37,6 +39,7 @@ struct Shared {
     Best best[kWavesS];
     uint32_t n, pick, lo, hi;
     u64 at, upto, all;
+    int first;
     double exp[64];      // 2^(j / 64)
 };
 
@@ -111,19 +114,26 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ u64 wave_sum_u64(u64 v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+// v of another lane by a data-parallel move; 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 moved(u64 v) {
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+    return (u64)hi << 32 | lo;
 }
 __device__ __forceinline__ u64 wave_scan_u64(u64 v) {      // inclusive
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const u64 t = __shfl_up(v, o, 64);
-        if (lane >= o) v += t;
-    }
+    v += moved<0x111, 0xF>(v);      // within rows of 16 lanes
+    v += moved<0x112, 0xF>(v);
+    v += moved<0x114, 0xF>(v);
+    v += moved<0x118, 0xF>(v);
+    v += moved<0x142, 0xA>(v);      // from row to row
+    v += moved<0x143, 0xC>(v);
     return v;
+}
+__device__ __forceinline__ u64 wave_sum_u64(u64 v) {
+    v = wave_scan_u64(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63), hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63);
+    return (u64)hi << 32 | lo;
 }
 // Sum over the workgroup, to every thread.
 __device__ __forceinline__ u64 group_sum(u64 v, u64 (&tmp)[kWavesS]) {
@@ -160,8 +170,10 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 // What a request asks of a row, and the row's scale.
 struct Ask {
     double c;            // log2(e) / T
-    double p, m;         // p >= 1: no cut; m in weights
+    double p;            // p >= 1: no cut
+    u64 m;               // least weight
     float top;
+    double most;         // the top, or the largest number for an infinite one
     float far;           // logits further than this below the top have no weight
     float parts;         // histogram's parts to a logit
     uint32_t k;          // 0: no cut
@@ -170,11 +182,11 @@ struct Ask {
     __device__ __forceinline__ void set(const SampleArgs &a, int row) {
         double t = a.temperature ? (double)a.temperature[row] : 1.0;
         p = a.top_p ? (double)a.top_p[row] : 1.0;
-        m = a.min_p ? (double)a.min_p[row] : 0.0;
+        const double mp = a.min_p ? (double)a.min_p[row] : 0.0;
         const int kk = a.top_k ? a.top_k[row] : 0;
         k = kk > 0 && kk < a.V ? (uint32_t)kk : 0;
         if (!(p < 1.0)) p = 1.0;
-        m = (m > 0.0 ? fmin(m, 1.0) : 0.0) * (double)(1ull << kOneShift);
+        m = (u64)ceil((mp > 0.0 ? fmin(mp, 1.0) : 0.0) * (double)(1ull << kOneShift));
         first = !(t > 0.0);
         if (first) t = 1.0;
         c = kLog2eD / t;
@@ -183,6 +195,7 @@ struct Ask {
     __device__ __forceinline__ bool cut() const { return !first && (k > 0 || p < 1.0); }
     __device__ __forceinline__ void scale(const Best &b) {
         top = b.top;
+        most = (double)fminf(top, kLargest);
         // Infinite at the highest temperatures; 0 where only infinite logits have weight.
         far = b.top == __builtin_inff() ? 0.0f : (float)((kMostY + 1.0) / c);
         parts = (float)(kBins - 1) / fmaxf(fminf(b.top - b.low, far), 1e-30f);      // inf - inf: far
@@ -199,7 +212,7 @@ struct Ask {
         constexpr double kRound = 6755399441055744.0 / 64.0;      // 1.5 2^52 / 64: sums round to 64ths
         double d[N], t[N], g[N], v[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = fmax((double)top - (double)x[i], 0.0);      // inf - inf: 0
+        for (int i = 0; i < N; ++i) d[i] = most - (double)fminf(x[i], kLargest);      // inf - inf: 0
 #pragma unroll
         for (int i = 0; i < N; ++i) t[i] = __builtin_fma(d[i], -c, kRound);
 #pragma unroll
@@ -500,50 +513,61 @@ __device__ __forceinline__ void border(const Row<T> &r, const Ask &q, Shared &s,
     __syncthreads();
 }
 
-// The first index at which the kept weights' sum passes u of them all: parts of the row
-// in turn, each a sixteenth of the one before.  s.all: the sum of every weight, where
-// nothing has been cut.
-template <class T>
-__device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, double u, u64 tau) {
-    int b0 = 0, b1 = r.blocks;
-    u64 before = 0;
-    double target = 0.0;
-    // the least that is kept, for a test before the key's
-    const float least = tau ? value_of((uint32_t)(tau >> 32)) : -__builtin_inff();
-    const auto kept_of = [&](int i, float x, u64 w) { return full_key(x, i) >= tau && (double)w >= q.m ? w : 0ull; };
-#pragma unroll 1
-    for (bool first = true; first || b1 - b0 > 64; first = false) {
-        const int wave = threadIdx.x >> 6, per = ((b1 - b0 + kWavesS - 1) / kWavesS + 63) & ~63;
-        u64 mine = 0, total = 0;
-        r.each(b0, b1, [&](int i, const float (&x)[4]) {
-            if (!(x[0] >= least || x[1] >= least || x[2] >= least || x[3] >= least)) return;
-            u64 w[4];
-            q.weights(s, x, w);
+// What is kept of a row: keys from tau on, by weight from q.m on.
+struct Kept {
+    u64 tau;
+    float least;      // the value of tau
+    __device__ __forceinline__ explicit Kept(u64 t) : tau(t), least(t ? value_of((uint32_t)(t >> 32)) : -__builtin_inff()) {}
+    __device__ __forceinline__ bool may(const Ask &q, float x) const { return x >= least && q.near(x); }
+    // of one that may be
+    __device__ __forceinline__ bool is(float x, int i) const { return x > least || (uint32_t)i <= 0xFFFFFFFFu - (uint32_t)tau || tau == 0; }
+};
+
+// Sums of the kept weights (and, with ALL, of every weight) of four elements.
+template <bool ALL>
+__device__ __forceinline__ void add_kept(const Ask &q, const Shared &s, const Kept &k, int i, const float (&x)[4], u64 &mine, u64 &total) {
+    bool may[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = x[e] >= least && q.near(x[e]) ? w[e] : 0;
-                total += w[e];
-                mine += kept_of(i + e, x[e], w[e]);
-            }
-        });
-        mine = wave_sum_u64(mine);
-        total = wave_sum_u64(total);
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) {
-            s.sum[wave] = mine;
-            s.sum2[wave] = total;
+    for (int e = 0; e < 4; ++e) may[e] = k.may(q, x[e]);
+    if (!(may[0] | may[1] | may[2] | may[3])) return;
+    u64 w[4];
+    q.weights(s, x, w);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        w[e] = may[e] ? w[e] : 0;
+        if constexpr (ALL) total += w[e];
+        mine += w[e] >= q.m && k.is(x[e], i + e) ? w[e] : 0;
+    }
+}
+
+// The sums over blocks [b0, b1), to every thread; s.sum: the kept ones of each wave's run.
+template <class T>
+__device__ __forceinline__ void masses(const Row<T> &r, const Ask &q, Shared &s, const Kept &k, int b0, int b1, u64 &kept, u64 &all) {
+    u64 mine = 0, total = 0;
+    r.each(b0, b1, [&](int i, const float (&x)[4]) { add_kept<true>(q, s, k, i, x, mine, total); });
+    all = group_sum(total, s.sum2);
+    kept = group_sum(mine, s.sum);
+}
+
+// The first index at which the kept weights' sum passes `target`, among blocks [b0, b1),
+// before which they come to `before`: parts in turn, each a sixteenth of the one before.
+// known: s.sum holds those of the first sixteen.
+template <class T>
+__device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, const Kept &k, int b0, int b1, u64 before, double target,
+                                    bool known) {
+#pragma unroll 1
+    while (b1 - b0 > kThreads) {
+        const int wave = threadIdx.x >> 6, per = ((b1 - b0 + kWavesS - 1) / kWavesS + 63) & ~63;
+        if (!known) {
+            u64 mine = 0, none = 0;
+            r.each(b0, b1, [&](int i, const float (&x)[4]) { add_kept<false>(q, s, k, i, x, mine, none); });
+            mine = wave_sum_u64(mine);
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) s.sum[wave] = mine;
+            __syncthreads();
         }
-        __syncthreads();
-        if (first) {
-            u64 kept = 0, all = 0;
-            for (int i = 0; i < kWavesS; ++i) {
-                kept += s.sum[i];
-                all += s.sum2[i];
-            }
-            target = u * (double)kept;
-            if (threadIdx.x == 0) s.all = all;
-        }
-        // the last part that holds anything where no sum passes u (u at or above 1)
+        known = false;
+        // the last part that holds anything where no sum passes the target (u at or above 1)
         int g = -1, last = 0;
         u64 at = before, last_at = before, g_at = before;
         for (int i = 0; i < kWavesS; ++i) {
@@ -562,43 +586,50 @@ __device__ __forceinline__ int draw(const Row<T> &r, const Ask &q, Shared &s, do
         b1 = min(from + per, b1);
         b0 = from;
     }
-    __syncthreads();
-    if (threadIdx.x < 64) {
-        const int b = b0 + threadIdx.x;
-        u64 w[Row<T>::E], mine = 0;
-        const u32x4_t v = r.block(b < b1 ? b : r.blocks);
+    // a block a thread
+    const int b = b0 + threadIdx.x;
+    const u32x4_t v = r.block(b < b1 ? b : r.blocks);
+    u64 w[Row<T>::E], mine = 0;
 #pragma unroll
-        for (int e = 0; e < Row<T>::E; ++e) {
-            const float x = Row<T>::value(v, e);
-            w[e] = q.near(x) && x >= least ? kept_of(r.index(b, e), x, q.weight(s, x)) : 0ull;
-            mine += w[e];
-        }
-        u64 at = before + wave_scan_u64(mine) - mine;
-        int hit = 0x7FFFFFFF, held = -1;
+    for (int e0 = 0; e0 < Row<T>::E; e0 += 4) {
+        const float x[4] = {Row<T>::value(v, e0), Row<T>::value(v, e0 + 1), Row<T>::value(v, e0 + 2), Row<T>::value(v, e0 + 3)};
+        u64 four[4];
+        q.weights(s, x, four);
 #pragma unroll
-        for (int e = 0; e < Row<T>::E; ++e) {
-            at += w[e];
-            const int i = r.index(b, e);
-            if (w[e] != 0) {
-                held = i;
-                if ((double)at > target) hit = min(hit, i);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const bool is = k.may(q, x[e]) && four[e] >= q.m && k.is(x[e], r.index(b, e0 + e));
+            w[e0 + e] = is ? four[e] : 0;
+            mine += w[e0 + e];
         }
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) {
-            hit = min(hit, __shfl_xor(hit, o, 64));
-            held = max(held, __shfl_xor(held, o, 64));
-        }
-        if (threadIdx.x == 0) s.pick = (uint32_t)(hit == 0x7FFFFFFF ? held : hit);
     }
+    if (threadIdx.x == 0) {
+        s.pick = 0xFFFFFFFFu;
+        s.hi = 0;
+    }
+    u64 at = before + group_before(mine, s.sum);
+    const bool passes = mine != 0 && (double)(at + mine) > target;
+    int hit = 0, held = 0;
+#pragma unroll
+    for (int e = 0; e < Row<T>::E; ++e) {
+        const bool was = (double)at > target;
+        at += w[e];
+        if (w[e] != 0) held = r.index(b, e);
+        if (w[e] != 0 && !was && (double)at > target) hit = r.index(b, e);
+    }
+    // the first that passes lies in the first block that does; none: the last one held
+    if (passes) atomicMin(&s.pick, (uint32_t)threadIdx.x);
+    if (mine != 0) atomicMax(&s.hi, (uint32_t)held);
     __syncthreads();
-    return (int)s.pick;
+    if (s.pick == 0xFFFFFFFFu) return (int)s.hi;
+    if (threadIdx.x == s.pick) s.lo = (uint32_t)hit;
+    __syncthreads();
+    return (int)s.lo;
 }
 
 // The same on the list in order: its first `kept` elements, in the order of their index.
 __device__ __forceinline__ int draw_listed(const Ask &q, Shared &s, double u, uint32_t kept) {
     u64 w = threadIdx.x < kept ? s.w[threadIdx.x] : 0;
-    if (!((double)w >= q.m)) w = 0;
+    if (w < q.m) w = 0;
     const double target = u * (double)group_sum(w, s.sum);
     u64 key = (uint32_t)s.key[threadIdx.x];      // 2^32 - 1 - index
     if (threadIdx.x == 0) {
@@ -616,68 +647,64 @@ __device__ __forceinline__ int draw_listed(const Ask &q, Shared &s, double u, ui
     return (int)(s.pick == 0xFFFFFFFFu ? s.hi : s.pick);
 }
 
-// The row's token, from its histogram in s where q.cut().
+__device__ __forceinline__ double number_of(const SampleArgs &a, int row) { return a.u[row] >= 0.0f ? (double)a.u[row] : 0.0; }      // NaN: 0
+
 template <class T>
-__device__ __forceinline__ void choose(const SampleArgs &a, int row, const Row<T> &r, const Ask &q, const Best &best, Shared &s) {
-    const double u = a.u[row] >= 0.0f ? (double)a.u[row] : 0.0;      // NaN: 0
-    u64 tau = 0, all = 0;
+__device__ __forceinline__ void answer(const SampleArgs &a, int row, const Row<T> &r, const Ask &q, int token, u64 all) {
+    if (threadIdx.x != 0) return;
+    a.token[row] = token;
+    if (!a.logprob) return;
+    const float x = r.at(token);
+    const double y = x == q.top ? 0.0 : ((double)q.top - (double)x) * q.c;
+    a.logprob[row] = (float)(-y * kLn2D - log((double)all * (1.0 / (double)(1ull << kOneShift))));
+}
+
+// Of a row whose histogram is in s: true if the row is answered, else the least kept key.
+// s.all: the sum of every weight.
+template <class T>
+__device__ __forceinline__ bool cut_row(const SampleArgs &a, int row, const Row<T> &r, const Ask &q, Shared &s, u64 &tau) {
+    u64 m = 0;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) m += s.mass[i];
+    m = group_sum(m, s.sum);
+    if (threadIdx.x == 0) s.all = m;
+    tau = 0;
     uint32_t n = 0;
     bool listed = false;
-    const bool cut = q.cut();
-    if (cut) {
-        u64 m = 0;
-        for (int i = threadIdx.x; i < kBins; i += kThreads) m += s.mass[i];
-        all = group_sum(m, s.sum);
-        // the border by k, then that by p of what k has left
-        bool by_k = q.k > 0;
-        u64 left = all;
-        double target = q.p * (double)all;
-        const auto reached = [&](const Upto &t) { return by_k ? t.count >= q.k : t.count > 0 && (double)t.mass >= target; };
+    // the border by k, then that by p of what k has left
+    bool by_k = q.k > 0;
+    double target = q.p * (double)m;
+    const auto reached = [&](const Upto &t) { return by_k ? t.count >= q.k : t.count > 0 && (double)t.mass >= target; };
 #pragma unroll 1
-        for (int step = 0;; ++step) {
-            int bin = 0;
-            if (!listed) {
-                Upto base;
-                bin = first_bin(s, base, reached);
-                // every element up to the border's bin in the list, if it has room
-                listed = step == 0 && bin >= 0 && base.count + s.count[bin] <= kList;
-                if (listed) {
-                    n = gather(r, q, s, [&](float x) { return q.bin_of(x) <= bin; });
-                    sort_list(q, s, n);
-                } else if (bin >= 0) border(r, q, s, bin, base, reached);
-            }
-            if (listed) first_listed(s, n, Upto{0, 0}, reached);
-            if (bin >= 0) {      // else all that have weight are kept
-                tau = max(tau, s.at);
-                left = s.upto;
-                if (listed) n = s.lo + 1;
-            }
-            if (!by_k || !(q.p < 1.0)) break;
-            by_k = false;
-            target = q.p * (double)left;
-            if (!listed) {      // the search for k's border has used the histogram's room
-                __syncthreads();
-                clear(s);
-                histogram(r, 0, r.blocks, q, s);
+    for (int step = 0;; ++step) {
+        int bin = 0;
+        if (!listed) {
+            Upto base;
+            bin = first_bin(s, base, reached);
+            // every element up to the border's bin in the list, if it has room
+            listed = step == 0 && bin >= 0 && base.count + s.count[bin] <= kList;
+            if (listed) {
+                n = gather(r, q, s, [&](float x) { return q.bin_of(x) <= bin; });
+                sort_list(q, s, n);
+            } else if (bin >= 0) {
+                border(r, q, s, bin, base, reached);
             }
         }
-    }
-    int token = best.at;
-    if (listed) {
-        token = draw_listed(q, s, u, n);
-    } else if (!q.first || a.logprob) {
-        const int drawn = draw(r, q, s, u, tau);
-        if (!q.first) token = drawn;
-        if (!cut) all = s.all;
-    }
-    if (threadIdx.x == 0) {
-        a.token[row] = token;
-        if (a.logprob) {
-            const float x = r.at(token);
-            const double y = x == q.top ? 0.0 : ((double)q.top - (double)x) * q.c;
-            a.logprob[row] = (float)(-y * kLn2D - log((double)all * (1.0 / (double)(1ull << kOneShift))));
+        if (listed) first_listed(s, n, Upto{0, 0}, reached);
+        if (bin >= 0) {      // else all that have weight are kept
+            tau = max(tau, s.at);
+            if (listed) n = s.lo + 1;
+        }
+        if (!by_k || !(q.p < 1.0)) break;
+        by_k = false;
+        target = q.p * (double)(bin >= 0 ? s.upto : s.all);
+        if (!listed) {      // the search for k's border has used the histogram's room
+            __syncthreads();
+            clear(s);
+            histogram(r, 0, r.blocks, q, s);
         }
     }
+    if (listed) answer(a, row, r, q, draw_listed(q, s, number_of(a, row), n), s.all);
+    return listed;
 }
 
 template <class T>
@@ -693,31 +720,284 @@ __device__ __forceinline__ bool none_left(const SampleArgs &a, int row, const Be
     return true;
 }
 
+__device__ __forceinline__ void fill_table(Shared &s) {
+    if (threadIdx.x < 64) s.exp[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
+}
+
 // A workgroup a row.
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-sample_kernel(const SampleArgs a) {
+sample_row_kernel(const SampleArgs a) {
     __shared__ Shared s;
     const int row = blockIdx.x;
     const Row<T> r = row_of<T>(a, row);
     Ask q;
     q.set(a, row);
+    fill_table(s);
     clear(s);
-    if (threadIdx.x < 64) s.exp[threadIdx.x] = exp2((double)threadIdx.x / 64.0);
     const Best b = best_of(r, 0, r.blocks, s);
     if (none_left(a, row, b)) return;
     q.scale(b);
-    if (q.cut()) histogram(r, 0, r.blocks, q, s);
-    choose(a, row, r, q, b, s);
+    if (q.first && !a.logprob) return answer(a, row, r, q, b.at, 0);
+    // across the passes these wait in LDS
+    if (threadIdx.x == 0) s.first = b.at;
+    u64 tau = 0;
+    if (q.cut()) {
+        histogram(r, 0, r.blocks, q, s);
+        if (cut_row(a, row, r, q, s, tau)) return;
+    }
+    const Kept k(tau);
+    u64 kept, sum;
+    masses(r, q, s, k, 0, r.blocks, kept, sum);
+    if (threadIdx.x == 0 && !q.cut()) s.all = sum;
+    const int token = q.first ? s.first : draw(r, q, s, k, 0, r.blocks, 0, number_of(a, row) * (double)kept, true);
+    answer(a, row, r, q, token, s.all);
+}
+
+// Few rows: a row in slices, a workgroup each, in up to five launches:
+//   best     largest logit of each slice
+//   sums     histogram of each slice, or where nothing is cut its sums
+//   cut      (a workgroup a row) the histogram's border; short lists are answered here
+//   keep     sums of what is kept of each slice, of rows whose list is not short
+//   pick     (a workgroup a row) the slice that holds the draw, and the token in it
+struct Slice {
+    u64 kept, all;
+    Best best;
+};
+struct RowState {
+    u64 tau, all;
+    int done;
+};
+struct Work {
+    Slice *slice;       // [rows][S]
+    RowState *row;      // [rows]
+    u64 *mass;          // [rows][S][kBins]
+    uint32_t *count;    // likewise
+};
+__host__ __device__ __forceinline__ size_t part_bytes(size_t n) { return (n + 15) / 16 * 16; }
+__host__ __device__ __forceinline__ size_t work_bytes(size_t rows, size_t slices) {
+    return part_bytes(slices * sizeof(Slice)) + part_bytes(rows * sizeof(RowState)) + slices * kBins * 12;
+}
+__device__ __forceinline__ Work work_of(const SampleArgs &a, int S) {
+    Work w;
+    uint8_t *p = static_cast<uint8_t *>(a.ws);
+    const size_t n = (size_t)a.rows * S;
+    w.slice = reinterpret_cast<Slice *>(p);
+    p += part_bytes(n * sizeof(Slice));
+    w.row = reinterpret_cast<RowState *>(p);
+    p += part_bytes(a.rows * sizeof(RowState));
+    w.mass = reinterpret_cast<u64 *>(p);
+    w.count = reinterpret_cast<uint32_t *>(w.mass + n * kBins);
+    return w;
+}
+struct Blocks {
+    int b0, b1;
+};
+__device__ __forceinline__ Blocks slice_blocks(int blocks, int i, int S) {
+    const int per = ((blocks + S - 1) / S + 63) & ~63;
+    return Blocks{min(i * per, blocks), min(i * per + per, blocks)};
+}
+// Lane l takes slice l & 15 of a row, so that their loads go out together.
+__device__ __forceinline__ Best row_best(const Slice *s, int S) {
+    const int i = threadIdx.x & (kMostSlices - 1);
+    Best b = i < S ? s[i].best : Best{-__builtin_inff(), __builtin_inff(), 0x7FFFFFFF};
+#pragma unroll
+    for (int o = kMostSlices / 2; o > 0; o >>= 1) {
+        const Best x{__shfl_xor(b.top, o, 64), __shfl_xor(b.low, o, 64), __shfl_xor(b.at, o, 64)};
+        b.at = x.top > b.top ? x.at : x.top == b.top ? min(x.at, b.at) : b.at;
+        b.top = fmaxf(b.top, x.top);
+        b.low = fminf(b.low, x.low);
+    }
+    return b;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sample_best_kernel(const SampleArgs a, int S) {
+    __shared__ Shared s;
+    const int row = blockIdx.x / S, i = blockIdx.x % S;
+    const Row<T> r = row_of<T>(a, row);
+    const Blocks x = slice_blocks(r.blocks, i, S);
+    const Best b = best_of(r, x.b0, x.b1, s);
+    if (threadIdx.x == 0) work_of(a, S).slice[blockIdx.x].best = b;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sample_sums_kernel(const SampleArgs a, int S) {
+    __shared__ Shared s;
+    const int row = blockIdx.x / S, i = blockIdx.x % S;
+    const Work w = work_of(a, S);
+    const Row<T> r = row_of<T>(a, row);
+    const Blocks x = slice_blocks(r.blocks, i, S);
+    Ask q;
+    q.set(a, row);
+    fill_table(s);
+    const Best b = row_best(w.slice + (size_t)row * S, S);
+    q.scale(b);
+    if (!(b.top > -__builtin_inff()) || (q.first && !a.logprob)) return;
+    clear(s);
+    if (q.cut()) {
+        histogram(r, x.b0, x.b1, q, s);
+        for (int k = threadIdx.x; k < kBins; k += kThreads) {
+            w.mass[(size_t)blockIdx.x * kBins + k] = s.mass[k];
+            w.count[(size_t)blockIdx.x * kBins + k] = s.count[k];
+        }
+        return;
+    }
+    u64 kept, all;
+    masses(r, q, s, Kept(0), x.b0, x.b1, kept, all);
+    if (threadIdx.x == 0) {
+        w.slice[blockIdx.x].kept = kept;
+        w.slice[blockIdx.x].all = all;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sample_cut_kernel(const SampleArgs a, int S) {
+    __shared__ Shared s;
+    const int row = blockIdx.x;
+    const Work w = work_of(a, S);
+    const Row<T> r = row_of<T>(a, row);
+    Ask q;
+    q.set(a, row);
+    fill_table(s);
+    const Best b = row_best(w.slice + (size_t)row * S, S);
+    q.scale(b);
+    u64 tau = 0;
+    bool done = true;
+    if (threadIdx.x == 0) s.all = 0;
+    if (none_left(a, row, b)) {
+    } else if (q.first && !a.logprob) {
+        answer(a, row, r, q, b.at, 0);
+    } else if (!q.cut()) {
+        done = false;
+    } else {
+        for (int k = threadIdx.x; k < kBins; k += kThreads) {
+            u64 m = 0;
+            uint32_t c = 0;
+#pragma unroll
+            for (int i0 = 0; i0 < kMostSlices; i0 += 8) {
+                if (i0 >= S) break;
+                u64 mi[8];
+                uint32_t ci[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const size_t at = ((size_t)row * S + min(i0 + i, S - 1)) * kBins + k;
+                    mi[i] = w.mass[at];
+                    ci[i] = w.count[at];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    m += i0 + i < S ? mi[i] : 0;
+                    c += i0 + i < S ? ci[i] : 0;
+                }
+            }
+            s.mass[k] = m;
+            s.count[k] = c;
+        }
+        __syncthreads();
+        done = cut_row(a, row, r, q, s, tau);
+    }
+    if (threadIdx.x == 0) w.row[row] = RowState{tau, s.all, done};      // s.all by this thread
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sample_keep_kernel(const SampleArgs a, int S) {
+    __shared__ Shared s;
+    const int row = blockIdx.x / S, i = blockIdx.x % S;
+    const Work w = work_of(a, S);
+    const RowState st = w.row[row];
+    Ask q;
+    q.set(a, row);
+    if (st.done || !q.cut()) return;
+    const Row<T> r = row_of<T>(a, row);
+    const Blocks x = slice_blocks(r.blocks, i, S);
+    fill_table(s);
+    q.scale(row_best(w.slice + (size_t)row * S, S));
+    __syncthreads();
+    u64 kept, all;
+    masses(r, q, s, Kept(st.tau), x.b0, x.b1, kept, all);
+    if (threadIdx.x == 0) w.slice[blockIdx.x].kept = kept;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+sample_pick_kernel(const SampleArgs a, int S) {
+    __shared__ Shared s;
+    const int row = blockIdx.x;
+    const Work w = work_of(a, S);
+    const Slice *x = w.slice + (size_t)row * S;
+    const int i = threadIdx.x & (kMostSlices - 1);
+    // loads first
+    const RowState st = w.row[row];
+    const u64 mine = i < S ? x[i].kept : 0, every = i < S ? x[i].all : 0;
+    const Best b = row_best(x, S);
+    const Row<T> r = row_of<T>(a, row);
+    Ask q;
+    q.set(a, row);
+    if (st.done) return;
+    fill_table(s);
+    q.scale(b);
+    __syncthreads();
+    u64 upto = mine, all = every;
+#pragma unroll
+    for (int o = 1; o < kMostSlices; o <<= 1) {
+        const u64 t = __shfl_up(upto, o, kMostSlices);
+        if (i >= o) upto += t;
+        all += __shfl_xor(all, o, 64);
+    }
+    if (q.cut()) all = st.all;
+    const double target = number_of(a, row) * (double)__shfl(upto, kMostSlices - 1, 64);
+    // the last one that holds anything where no sum passes the target (u at or above 1)
+    const uint32_t holds = (uint32_t)__ballot(mine != 0) & 0xFFFFu, past = (uint32_t)__ballot(mine != 0 && (double)upto > target) & 0xFFFFu;
+    const int slice = past ? __ffs((int)past) - 1 : 31 - __clz((int)holds);
+    const u64 before = __shfl(upto - mine, slice, 64);
+    const Blocks y = slice_blocks(r.blocks, slice, S);
+    answer(a, row, r, q, q.first ? b.at : draw(r, q, s, Kept(st.tau), y.b0, y.b1, before, target, false), all);
+}
+
+// Slices a row where the rows alone leave CUs idle: at most kMostSlices, of at least
+// kLeastSlice logits each.
+constexpr int kCUs = 256, kLeastSlice = 4096;
+int slices_of(int rows, int V) {
+    int s = kCUs / rows;
+    if (s > kMostSlices) s = kMostSlices;
+    if (s > V / kLeastSlice) s = V / kLeastSlice;
+    return s < 2 ? 1 : s;
+}
+
+template <class T>
+void launch_rows(const SampleArgs &a, int S, hipStream_t stream) {
+    const dim3 rows((unsigned)a.rows), slices((unsigned)(a.rows * S)), threads(kThreads);
+    if (S == 1) {
+        hipLaunchKernelGGL(sample_row_kernel<T>, rows, threads, 0, stream, a);
+        return;
+    }
+    hipLaunchKernelGGL(sample_best_kernel<T>, slices, threads, 0, stream, a, S);
+    hipLaunchKernelGGL(sample_sums_kernel<T>, slices, threads, 0, stream, a, S);
+    hipLaunchKernelGGL(sample_cut_kernel<T>, rows, threads, 0, stream, a, S);
+    // without k and p nothing is cut
+    if (a.top_k || a.top_p) hipLaunchKernelGGL(sample_keep_kernel<T>, slices, threads, 0, stream, a, S);
+    hipLaunchKernelGGL(sample_pick_kernel<T>, rows, threads, 0, stream, a, S);
 }
 
 }  // namespace
 
-size_t sample_ws_bytes(int, int) { return 0; }
+// For every smaller number of rows too: slices in all are at most those of as many as fit.
+size_t sample_ws_bytes(int rows, int V) {
+    int most = V / kLeastSlice < kMostSlices ? V / kLeastSlice : kMostSlices;
+    if (most < 2) return 0;
+    const int64_t all = (int64_t)rows * most;
+    return work_bytes((size_t)(rows < kCUs ? rows : kCUs), (size_t)(all < kCUs ? all : kCUs));
+}
 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t stream) {
-    if (a.fp32) hipLaunchKernelGGL(sample_kernel<float>, dim3((unsigned)a.rows), dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL(sample_kernel<uint16_t>, dim3((unsigned)a.rows), dim3(kThreads), 0, stream, a);
+    const int S = slices_of(a.rows, a.V);
+    if (a.fp32) launch_rows<float>(a, S, stream);
+    else launch_rows<uint16_t>(a, S, stream);
     return hipGetLastError();
 }
 
