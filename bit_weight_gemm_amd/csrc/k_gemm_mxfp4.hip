@@ -4,8 +4,7 @@
 //   y[m][n] = sum over blocks b of 2^(sa[m][b] + sw[n][b] - 254) sum_k a[m][k] w[n][k]
 //
 // Sums are fp32 (the instruction adds a block's exact sum).  A scale byte of 255 makes
-// its row NaN.  W is the instructions' first operand, so that a lane's results are
-// successive n of one m.
+// its row NaN.
 #include "mx_device.h"
 
 namespace biloco {
@@ -47,7 +46,8 @@ __device__ __forceinline__ T rounded(float v) {
 }
 
 // ---------------------------------------------------------------- few rows
-// A workgroup takes 16 NT rows of W and all rows of A (16 MT of them); its waves take
+// A workgroup takes 16 NT rows of W (the instructions' first operand, so that a lane's
+// results are successive n of one m) and all rows of A (16 MT of them); its waves take
 // chunks of 512 k in turn and join their sums in LDS.  In a chunk the lanes l >> 4 == g
 // take the blocks 4 g .. 4 g + 3, one a step, so that a lane's four scale bytes are one
 // dword and each step's byte is the instruction's selector.
@@ -156,9 +156,13 @@ mxfp4_rows_kernel(const Mx p) {
 // ---------------------------------------------------------------- many rows
 // A workgroup of four waves takes BM rows of A and BN of W, a wave a quarter; stages of
 // 256 k go straight from memory to LDS, the next one while this one is multiplied.
-// Rows of a stage are 128 bytes in LDS; block j of row r lies in slot j ^ (r & 7), so that
-// eight successive rows' reads of one block meet all banks.  Lanes of half h take blocks
-// 4 h .. 4 h + 3 of a stage, one a step: a lane's scales are one dword, as above.
+// Rows of a stage are 128 bytes in LDS, half of the banks; block j of row r lies in slot
+// j ^ (r >> 1 & 7), so that sixteen successive rows' reads of one block meet all banks.
+// Lanes of half h multiply blocks 4 h .. 4 h + 3 of a stage, one a step, whose four scale
+// bytes are one dword.  Four stages are taken together, 1024 k: stage s has blocks 4 s ..
+// of the first 16 for h = 0 and of the others for h = 1, so that a lane's scales of four
+// stages are 16 bytes.  (A load of a dword a row costs as many requests to L2 as a stage's
+// codes: with one a stage 249 us for 4096 rows of 8192 to 8192.)
 template <int BM, int BN>
 struct StageLds {
     alignas(16) uint8_t x[(BM + BN) * 128];
@@ -167,11 +171,14 @@ struct StageLds {
 template <int BM, int BN>
 struct Tile {
     static constexpr int MT = BM / 64, NT = BN / 64, LOADS = (BM + BN) / 32;
-    uint32_t as[MT], ws[NT];
     f32x16m_t acc[NT][MT];
     uint32_t from[LOADS];                   // byte offsets of a wave's pieces from the tile's rows
     uint32_t afrom[MT], wfrom[NT];          // of its scales
     const uint8_t *a, *w, *sa, *sw;         // the tile's first rows
+
+    struct Scales {
+        u32x4_t a[MT], w[NT];               // a dword a stage
+    };
 
     __device__ __forceinline__ void init(const Mx &p, int m0, int n0) {
         const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -182,17 +189,16 @@ struct Tile {
         sw = p.ws + (int64_t)n0 * blocks;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = 32 * i + tid / 8, slot = tid & 7;
+            const int row = 32 * i + tid / 8;
             const bool is_a = 32 * i < BM;
-            const int r = is_a ? min(row, p.M - 1 - m0) : min(row - BM, p.N - 1 - n0);
-            from[i] = (uint32_t)r * pitch + 16 * (slot ^ (row & 7));
+            from[i] = (uint32_t)(is_a ? min(row, p.M - 1 - m0) : min(row - BM, p.N - 1 - n0)) * pitch;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-            afrom[i] = (uint32_t)min((wave & 1) * (BM / 2) + 32 * i + (lane & 31), p.M - 1 - m0) * blocks + 4 * (lane >> 5);
+            afrom[i] = (uint32_t)min((wave & 1) * (BM / 2) + 32 * i + (lane & 31), p.M - 1 - m0) * blocks;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
-            wfrom[i] = (uint32_t)min((wave >> 1) * (BN / 2) + 32 * i + (lane & 31), p.N - 1 - n0) * blocks + 4 * (lane >> 5);
+            wfrom[i] = (uint32_t)min((wave >> 1) * (BN / 2) + 32 * i + (lane & 31), p.N - 1 - n0) * blocks;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -200,68 +206,105 @@ struct Tile {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     }
+    // The block of a stage that a thread brings.
+    __device__ __forceinline__ static int mine() { return (threadIdx.x & 7) ^ (threadIdx.x >> 4 & 7); }
 
-    // Stage t, of which all blocks are there, on its way into LDS.
-    __device__ __forceinline__ void request(StageLds<BM, BN> &lds, int t) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        const uint8_t *ga = a + 128 * (int64_t)t, *gw = w + 128 * (int64_t)t;
+    // Stage s of the four at 1024 t, on its way into LDS.
+    __device__ __forceinline__ void request(StageLds<BM, BN> &lds, int t, int s) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), j = mine();
+        const uint32_t in = 256 * (j >> 2) + 16 * (j & 3);
+        const uint8_t *ga = a + 512 * (int64_t)t + 64 * s, *gw = w + 512 * (int64_t)t + 64 * s;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((32 * i < BM ? ga : gw) + from[i]),
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((32 * i < BM ? ga : gw) + from[i] + in),
                                              (__attribute__((address_space(3))) void *)&lds.x[4096 * i + 1024 * wave], 16, 0, 0);
     }
-    __device__ __forceinline__ void scales(int t, uint32_t (&na)[MT], uint32_t (&nw)[NT]) const {
+    __device__ __forceinline__ void scales(int t, Scales &sc) const {
+        const int h = (threadIdx.x & 63) >> 5;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) na[i] = load4(sa + 8 * (int64_t)t + afrom[i]);
+        for (int i = 0; i < MT; ++i) __builtin_memcpy(&sc.a[i], sa + 32 * (int64_t)t + 16 * h + afrom[i], 16);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) nw[i] = load4(sw + 8 * (int64_t)t + wfrom[i]);
+        for (int i = 0; i < NT; ++i) __builtin_memcpy(&sc.w[i], sw + 32 * (int64_t)t + 16 * h + wfrom[i], 16);
     }
-    // The last stage where K ends inside it: through registers, zeros past the end.
-    __device__ __forceinline__ void request_part(StageLds<BM, BN> &lds, int t, int blocks) const {
-        const int tid = threadIdx.x;
+    // Eight blocks from b0 on, of which those past the last are zeros with scale 1: through
+    // registers.
+    __device__ __forceinline__ void request_part(StageLds<BM, BN> &lds, int b0, int blocks) const {
+        const int tid = threadIdx.x, b = b0 + mine();
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = 32 * i + tid / 8, b = 8 * t + ((tid & 7) ^ (row & 7));
             u32x4_t v{0, 0, 0, 0};
-            if (b < blocks) v = *reinterpret_cast<const u32x4_t *>((32 * i < BM ? a : w) + 128 * (int64_t)t + from[i]);
+            if (b < blocks) v = *reinterpret_cast<const u32x4_t *>((32 * i < BM ? a : w) + from[i] + 16 * (int64_t)b);
             *reinterpret_cast<u32x4_t *>(&lds.x[4096 * i + 16 * tid]) = v;
         }
     }
     __device__ __forceinline__ static uint32_t scales_of(const uint8_t *p, int b0, int blocks) {
         uint32_t v = 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v |= (b0 + s < blocks ? (uint32_t)p[s] : 127u) << (8 * s);
+        for (int s = 0; s < 4; ++s) v |= (b0 + s < blocks ? (uint32_t)p[b0 + s] : 127u) << (8 * s);
         return v;
     }
-    __device__ __forceinline__ void scales_part(int t, int blocks, uint32_t (&na)[MT], uint32_t (&nw)[NT]) const {
-        const int b0 = 8 * t + 4 * ((threadIdx.x & 63) >> 5);
+    __device__ __forceinline__ void scales_part(int b0, int blocks, Scales &sc) const {
+        const int b = b0 + 4 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) na[i] = scales_of(sa + 8 * (int64_t)t + afrom[i], b0, blocks);
+        for (int i = 0; i < MT; ++i) sc.a[i].x = scales_of(sa + afrom[i], b, blocks);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) nw[i] = scales_of(sw + 8 * (int64_t)t + wfrom[i], b0, blocks);
+        for (int i = 0; i < NT; ++i) sc.w[i].x = scales_of(sw + wfrom[i], b, blocks);
     }
 
+    // Operands of step S of a stage.
+    struct Frags {
+        u32x4_t a[MT], w[NT];
+    };
     template <int S>
-    __device__ __forceinline__ void step(const StageLds<BM, BN> &lds) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = 4 * (lane >> 5) + S;
+    __device__ __forceinline__ void read(const StageLds<BM, BN> &lds, Frags &f) const {
+        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), j = 4 * (lane >> 5) + S;
         const int ra = (wave & 1) * (BM / 2) + (lane & 31), rw = BM + (wave >> 1) * (BN / 2) + (lane & 31);
-        u32x4_t fa[MT], fw[NT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) fa[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(ra + 32 * i) * 128 + 16 * (j ^ (ra & 7))]);
+        for (int i = 0; i < MT; ++i) f.a[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(ra + 32 * i) * 128 + 16 * (j ^ (ra >> 1 & 7))]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) fw[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(rw + 32 * i) * 128 + 16 * (j ^ (rw & 7))]);
+        for (int i = 0; i < NT; ++i) f.w[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(rw + 32 * i) * 128 + 16 * (j ^ (rw >> 1 & 7))]);
+    }
+    // Step S of stage Q; R of the next step's operands are read meanwhile.
+    template <int S, int Q, int R>
+    __device__ __forceinline__ void products(const Frags &f, const Scales &sc) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(fw[i], fa[k], acc[i][k], ws[i], as[k]);
+            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(f.a[k], f.w[i], acc[i][k], sc.a[k][Q], sc.w[i][Q]);
+        // reads between the first products, and nothing moves over the step's end: left
+        // alone, the compiler reads all operands first or multiplies behind the wait for
+        // the next stage
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // an LDS read
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a matrix instruction
+        }
+        __builtin_amdgcn_sched_barrier(0);
     }
-    __device__ __forceinline__ void multiply(const StageLds<BM, BN> &lds) {
-        step<0>(lds);
-        step<1>(lds);
-        step<2>(lds);
-        step<3>(lds);
+    template <int Q>
+    __device__ __forceinline__ void multiply(const StageLds<BM, BN> &lds, const Scales &sc) {
+        Frags f, g;
+        read<0>(lds, f);
+        __builtin_amdgcn_sched_barrier(0);
+        read<1>(lds, g);
+        products<0, Q, MT + NT>(f, sc);
+        read<2>(lds, f);
+        products<1, Q, MT + NT>(g, sc);
+        read<3>(lds, g);
+        products<2, Q, MT + NT>(f, sc);
+        products<3, Q, 0>(g, sc);
     }
 };
+
+// Tile `at` of mt x nt: each of the 8 XCDs (workgroups go round them) takes a run of
+// tiles, in blocks of 8 rows of A's tiles, so that its L2 holds what its tiles share.
+__device__ __forceinline__ void tile_of(int at, int mt, int nt, int &m, int &n) {
+    const int all = mt * nt, each = all / 8, rest = all % 8, x = at % 8;
+    const int t = x * each + min(x, rest) + at / 8;
+    const int group = t / (8 * nt), first = group * 8, rows = min(8, mt - first), in = t - group * 8 * nt;
+    m = first + in % rows;
+    n = in / rows;
+}
 
 template <int BM, int BN, class T>
 __global__ void __launch_bounds__(256)
@@ -269,59 +312,66 @@ mxfp4_tiles_kernel(const Mx p, int mtiles) {
     __shared__ StageLds<BM, BN> lds0, lds1;
     using X = Tile<BM, BN>;
     const int piece = (int)(blockIdx.x % p.pieces), at = (int)(blockIdx.x / p.pieces);
-    const int m0 = at % mtiles * BM, n0 = at / mtiles * BN;
-    const int blocks = p.K / 32, whole = blocks / 8, all = (blocks + 7) / 8;      // stages
-    const int each = (all + p.pieces - 1) / p.pieces;
-    const int t0 = piece * each, t1 = min(t0 + each, all);
+    int m0, n0;
+    tile_of(at, mtiles, (p.N + BN - 1) / BN, m0, n0);
+    m0 *= BM;
+    n0 *= BN;
+    const int blocks = p.K / 32, fours = blocks / 32;      // blocks, and stages by four
+    const int each = (fours + p.pieces - 1) / p.pieces;
+    const int t0 = min(piece * each, fours), t1 = min(t0 + each, fours);
     X x;
     x.init(p, m0, n0);
-    uint32_t na[X::MT], nw[X::NT];
-    const auto fetch = [&](StageLds<BM, BN> &lds, int t) {
-        x.request(lds, t);
-        x.scales(t, na, nw);
-    };
-    // the requested stage is in place, and the other buffer has been read
-    const auto arrive = [&] {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < X::MT; ++i) x.as[i] = na[i];
-#pragma unroll
-        for (int i = 0; i < X::NT; ++i) x.ws[i] = nw[i];
-    };
-    // whole stages two by two, then what is left one by one
-    const int pairs = max(min(t1, whole) - t0, 0) / 2;
-    if (pairs > 0) fetch(lds0, t0);
-    for (int i = 0; i < pairs; ++i) {
-        const int t = t0 + 2 * i;
-        arrive();
-        fetch(lds1, t + 1);
-        x.multiply(lds0);
-        arrive();
-        if (i + 1 < pairs) fetch(lds0, t + 2);
-        x.multiply(lds1);
+    typename X::Scales sc, next;
+    if (t0 < t1) {
+        x.request(lds0, t0, 0);
+        x.scales(t0, next);
     }
-    for (int t = t0 + 2 * pairs; t < t1; ++t) {
+    for (int t = t0; t < t1; ++t) {
+        // the last turn asks for its own stage again: a branch here would let the
+        // compiler move the products behind the loads' end
+        const int u = min(t + 1, t1 - 1);
+        __syncthreads();      // the requested stage is in place, the other buffer has been read
+        sc = next;
+        x.request(lds1, t, 1);
+        x.template multiply<0>(lds0, sc);
         __syncthreads();
-        x.request_part(lds0, t, blocks);
-        x.scales_part(t, blocks, na, nw);
-        arrive();
-        x.multiply(lds0);
+        x.request(lds0, t, 2);
+        x.template multiply<1>(lds1, sc);
+        __syncthreads();
+        x.request(lds1, t, 3);
+        x.template multiply<2>(lds0, sc);
+        __syncthreads();
+        x.request(lds0, u, 0);
+        x.scales(u, next);
+        x.template multiply<3>(lds1, sc);
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (piece == p.pieces - 1)      // what is left of K, stage by stage
+        for (int b = 32 * fours; b < blocks; b += 8) {
+            __syncthreads();
+            x.request_part(lds0, b, blocks);
+            x.scales_part(b, blocks, sc);
+            __syncthreads();
+            x.template multiply<0>(lds0, sc);
+        }
+    // a lane holds one n of 16 m
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int m1 = m0 + (wave & 1) * (BM / 2) + 4 * (lane >> 5), n1 = n0 + (wave >> 1) * (BN / 2) + (lane & 31);
 #pragma unroll
-    for (int k = 0; k < X::MT; ++k) {
-        const int m = m0 + (wave & 1) * (BM / 2) + 32 * k + (lane & 31);
-        if (m >= p.M) continue;
+    for (int k = 0; k < X::MT; ++k)
 #pragma unroll
-        for (int i = 0; i < X::NT; ++i)
+        for (int e = 0; e < 16; ++e) {
+            const int m = m1 + 32 * k + 8 * (e >> 2) + (e & 3);
+            if (m >= p.M) continue;
+            float *part = p.part + ((int64_t)piece * p.M + m) * p.N;
+            T *y = static_cast<T *>(p.y) + m * p.ys;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int n = n0 + (wave >> 1) * (BN / 2) + 32 * i + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            for (int i = 0; i < X::NT; ++i) {
+                const int n = n1 + 32 * i;
                 if (n >= p.N) continue;
-                if (p.part) p.part[((int64_t)piece * p.M + m) * p.N + n] = x.acc[i][k][e];
-                else static_cast<T *>(p.y)[m * p.ys + n] = rounded<T>(x.acc[i][k][e]);
+                if (p.part) part[n] = x.acc[i][k][e];
+                else y[n] = rounded<T>(x.acc[i][k][e]);
             }
-    }
+        }
 }
 
 template <class T>
@@ -349,9 +399,9 @@ MxPlan plan_of(int M, int N, int K) {
     if (p.rows) return p;
     const auto tiles = [&](int b) { return (int64_t)((M + b - 1) / b) * ((N + b - 1) / b); };
     p.bm = p.bn = tiles(256) >= 256 ? 256 : 128;
-    const int64_t n = tiles(p.bm), stages = (K / 32 + 7) / 8;
+    const int64_t n = tiles(p.bm);
     int64_t pieces = n >= kWant ? 1 : (2 * kWant) / n;
-    const int64_t most = stages / 4;      // at least four stages a piece
+    const int64_t most = K / 1024;      // at least four stages a piece
     if (pieces > most) pieces = most;
     p.pieces = pieces < 1 ? 1 : (int)pieces;
     if (p.pieces > 1) p.part_bytes = (size_t)p.pieces * M * N * 4;
