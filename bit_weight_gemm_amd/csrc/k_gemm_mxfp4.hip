@@ -5,6 +5,8 @@
 //
 // Sums are fp32 (the instruction adds a block's exact sum).  A scale byte of 255 makes
 // its row NaN.
+#include <type_traits>
+
 #include "mx_device.h"
 
 namespace biloco {
@@ -154,51 +156,74 @@ mxfp4_rows_kernel(const Mx p) {
 }
 
 // ---------------------------------------------------------------- many rows
-// A workgroup of four waves takes BM rows of A and BN of W, a wave a quarter; stages of
-// 256 k go straight from memory to LDS, the next one while this one is multiplied.
-// Rows of a stage are 128 bytes in LDS, half of the banks; block j of row r lies in slot
-// j ^ (r >> 1 & 7), so that sixteen successive rows' reads of one block meet all banks.
-// Lanes of half h multiply blocks 4 h .. 4 h + 3 of a stage, one a step, whose four scale
-// bytes are one dword.  Four stages are taken together, 1024 k: stage s has blocks 4 s ..
-// of the first 16 for h = 0 and of the others for h = 1, so that a lane's scales of four
-// stages are 16 bytes.  (A load of a dword a row costs as many requests to L2 as a stage's
-// codes: with one a stage 249 us for 4096 rows of 8192 to 8192.)
+// A workgroup of WM x WN waves takes BM rows of A and BN of W.  Stages of 128 k go
+// straight from memory to LDS, four of them under way: all workgroups of an XCD walk along
+// K together, so every stage waits for lines that none of them has touched yet.
+// Rows of a stage are 64 bytes in LDS, a quarter of the banks; block j of row r lies in slot
+// j ^ (r >> 2 & 3), so that sixteen successive rows' reads of one block meet all banks.
+// Lanes of half h multiply blocks 2 h and 2 h + 1 of a stage, one a step; their scale
+// bytes are half a dword.  Scales come by 32 a row, for eight stages (a load of a dword a
+// row costs as many requests to L2 as two stages' codes).
+constexpr int kStages = 4, kGroup = 8;      // stages in LDS; stages whose scales come together
+
 template <int BM, int BN>
 struct StageLds {
-    alignas(16) uint8_t x[(BM + BN) * 128];
+    alignas(16) uint8_t x[(BM + BN) * 64];
+};
+// Scales of a group of stages, a row's 32 bytes in the order of its blocks.
+template <int BM, int BN>
+struct ScaleLds {
+    alignas(16) uint8_t x[(BM + BN) * 32];
 };
 
-template <int BM, int BN>
+// Waits until at most N of the wave's loads are under way, and for its LDS reads and writes.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "the counter's range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);
+}
+__device__ __forceinline__ void meet() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int BM, int BN, int WM, int WN>
 struct Tile {
-    static constexpr int MT = BM / 64, NT = BN / 64, LOADS = (BM + BN) / 32;
+    static constexpr int THREADS = 64 * WM * WN, MT = BM / (32 * WM), NT = BN / (32 * WN);
+    static constexpr int STEP = THREADS / 4, LOADS = (BM + BN) / STEP;      // rows that the threads bring at a time
+    static constexpr int SROWS = THREADS / 8, SCALES = (BM + BN) / SROWS;       // likewise of scales
+    using Stage = StageLds<BM, BN>;
     f32x16m_t acc[NT][MT];
-    uint32_t from[LOADS];                   // byte offsets of a wave's pieces from the tile's rows
-    uint32_t afrom[MT], wfrom[NT];          // of its scales
-    const uint8_t *a, *w, *sa, *sw;         // the tile's first rows
+    uint32_t from[LOADS];               // byte offsets of a thread's codes from the tile's rows
+    const uint8_t *a, *w, *sa, *sw;     // the tile's first rows
+    int mlast, nlast, blocks;           // the last rows that are there, blocks a row
+
+    // The wave's first row of A and of W.
+    __device__ __forceinline__ static int m_of() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) % WM * (32 * MT); }
+    __device__ __forceinline__ static int n_of() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) / WM * (32 * NT); }
+    // The block of a stage that a thread brings.
+    __device__ __forceinline__ static int mine() { return (threadIdx.x & 3) ^ (threadIdx.x >> 4 & 3); }
 
     struct Scales {
-        u32x4_t a[MT], w[NT];               // a dword a stage
+        uint32_t a[MT], w[NT];      // of a stage, the lane's two in the low half
     };
 
     __device__ __forceinline__ void init(const Mx &p, int m0, int n0) {
-        const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-        const uint32_t pitch = p.K / 2, blocks = p.K / 32;
+        const int tid = threadIdx.x;
+        const uint32_t pitch = p.K / 2;
+        blocks = p.K / 32;
+        mlast = min(BM, p.M - m0) - 1;
+        nlast = min(BN, p.N - n0) - 1;
         a = p.ac + (int64_t)m0 * pitch;
         sa = p.as + (int64_t)m0 * blocks;
         w = p.wc + (int64_t)n0 * pitch;
         sw = p.ws + (int64_t)n0 * blocks;
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-            const int row = 32 * i + tid / 8;
-            const bool is_a = 32 * i < BM;
-            from[i] = (uint32_t)(is_a ? min(row, p.M - 1 - m0) : min(row - BM, p.N - 1 - n0)) * pitch;
+            const int row = STEP * i + tid / 4;
+            from[i] = (uint32_t)(STEP * i < BM ? min(row, mlast) : min(row - BM, nlast)) * pitch + 16 * mine();
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-            afrom[i] = (uint32_t)min((wave & 1) * (BM / 2) + 32 * i + (lane & 31), p.M - 1 - m0) * blocks;
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            wfrom[i] = (uint32_t)min((wave >> 1) * (BN / 2) + 32 * i + (lane & 31), p.N - 1 - n0) * blocks;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -206,93 +231,123 @@ struct Tile {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     }
-    // The block of a stage that a thread brings.
-    __device__ __forceinline__ static int mine() { return (threadIdx.x & 7) ^ (threadIdx.x >> 4 & 7); }
 
-    // Stage s of the four at 1024 t, on its way into LDS.
-    __device__ __forceinline__ void request(StageLds<BM, BN> &lds, int t, int s) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), j = mine();
-        const uint32_t in = 256 * (j >> 2) + 16 * (j & 3);
-        const uint8_t *ga = a + 512 * (int64_t)t + 64 * s, *gw = w + 512 * (int64_t)t + 64 * s;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((32 * i < BM ? ga : gw) + from[i] + in),
-                                             (__attribute__((address_space(3))) void *)&lds.x[4096 * i + 1024 * wave], 16, 0, 0);
+    // A stage on its way into LDS in LOADS parts; t: the stage.
+    struct Request {
+        const uint8_t *a, *w;
+        uint8_t *to;
+    };
+    __device__ __forceinline__ Request request(Stage &lds, int t) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        const int64_t at = 64 * (int64_t)t;
+        return Request{a + at, w + at, &lds.x[1024 * wave]};
     }
-    __device__ __forceinline__ void scales(int t, Scales &sc) const {
-        const int h = (threadIdx.x & 63) >> 5;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) __builtin_memcpy(&sc.a[i], sa + 32 * (int64_t)t + 16 * h + afrom[i], 16);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) __builtin_memcpy(&sc.w[i], sw + 32 * (int64_t)t + 16 * h + wfrom[i], 16);
+    __device__ __forceinline__ void load(const Request &r, int i) const {
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((STEP * i < BM ? r.a : r.w) + from[i]),
+                                         (__attribute__((address_space(3))) void *)(r.to + 16 * THREADS * i), 16, 0, 0);
     }
-    // Eight blocks from b0 on, of which those past the last are zeros with scale 1: through
+    // Part i of SCALES of the scales of group t: a dword a lane, since they begin at
+    // multiples of four bytes.
+    __device__ __forceinline__ void load_scales(ScaleLds<BM, BN> &lds, int t, int i) const {
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), row = SROWS * i + (int)threadIdx.x / 8;
+        const bool is_a = SROWS * i < BM;
+        const uint32_t at = (uint32_t)(is_a ? min(row, mlast) : min(row - BM, nlast)) * (uint32_t)blocks + 4 * (threadIdx.x & 7);
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((is_a ? sa : sw) + 32 * (int64_t)t + at),
+                                         (__attribute__((address_space(3))) void *)&lds.x[4 * THREADS * i + 256 * wave],
+                                         4, 0, 0);
+    }
+    // Dwords of its stage q.
+    __device__ __forceinline__ static uint32_t scale_at(const ScaleLds<BM, BN> &lds, int r, int q) {
+        const int lane = threadIdx.x & 63;
+        return *reinterpret_cast<const uint32_t *>(&lds.x[32 * (r + (lane & 31)) + 4 * q]);
+    }
+    __device__ __forceinline__ void get_scales(const ScaleLds<BM, BN> &lds, int q, Scales &sc) const {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sc.a[i] = scale_at(lds, m_of() + 32 * i, q);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sc.w[i] = scale_at(lds, BM + n_of() + 32 * i, q);
+    }
+    // Dwords as read, to the lane's two bytes.
+    __device__ __forceinline__ static void halve(Scales &sc) {
+        const int shift = (threadIdx.x & 63) >> 5 << 4;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sc.a[i] >>= shift;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) sc.w[i] >>= shift;
+    }
+    // Four blocks from b0 on, of which those past the last are zeros with scale 1: through
     // registers.
-    __device__ __forceinline__ void request_part(StageLds<BM, BN> &lds, int b0, int blocks) const {
+    __device__ __forceinline__ void request_part(Stage &lds, int b0) const {
         const int tid = threadIdx.x, b = b0 + mine();
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             u32x4_t v{0, 0, 0, 0};
-            if (b < blocks) v = *reinterpret_cast<const u32x4_t *>((32 * i < BM ? a : w) + from[i] + 16 * (int64_t)b);
-            *reinterpret_cast<u32x4_t *>(&lds.x[4096 * i + 16 * tid]) = v;
+            if (b < blocks) v = *reinterpret_cast<const u32x4_t *>((STEP * i < BM ? a : w) + from[i] + 16 * (int64_t)b0);
+            *reinterpret_cast<u32x4_t *>(&lds.x[16 * (THREADS * i + tid)]) = v;
         }
     }
-    __device__ __forceinline__ static uint32_t scales_of(const uint8_t *p, int b0, int blocks) {
+    __device__ __forceinline__ uint32_t scales_of(const uint8_t *p, int b0) const {
         uint32_t v = 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v |= (b0 + s < blocks ? (uint32_t)p[b0 + s] : 127u) << (8 * s);
+        for (int s = 0; s < 2; ++s) v |= (b0 + s < blocks ? (uint32_t)p[b0 + s] : 127u) << (8 * s);
         return v;
     }
-    __device__ __forceinline__ void scales_part(int b0, int blocks, Scales &sc) const {
-        const int b = b0 + 4 * ((threadIdx.x & 63) >> 5);
+    __device__ __forceinline__ void scales_part(int b0, Scales &sc) const {
+        const int lane = threadIdx.x & 63, b = b0 + 2 * (lane >> 5);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sc.a[i].x = scales_of(sa + afrom[i], b, blocks);
+        for (int i = 0; i < MT; ++i) sc.a[i] = scales_of(sa + (int64_t)min(m_of() + 32 * i + (lane & 31), mlast) * blocks, b);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) sc.w[i].x = scales_of(sw + wfrom[i], b, blocks);
+        for (int i = 0; i < NT; ++i) sc.w[i] = scales_of(sw + (int64_t)min(n_of() + 32 * i + (lane & 31), nlast) * blocks, b);
     }
 
-    // Operands of step S of a stage.
+    // Operands of a step of a stage.
     struct Frags {
         u32x4_t a[MT], w[NT];
     };
     template <int S>
-    __device__ __forceinline__ void read(const StageLds<BM, BN> &lds, Frags &f) const {
-        const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), j = 4 * (lane >> 5) + S;
-        const int ra = (wave & 1) * (BM / 2) + (lane & 31), rw = BM + (wave >> 1) * (BN / 2) + (lane & 31);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) f.a[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(ra + 32 * i) * 128 + 16 * (j ^ (ra >> 1 & 7))]);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) f.w[i] = *reinterpret_cast<const u32x4_t *>(&lds.x[(rw + 32 * i) * 128 + 16 * (j ^ (rw >> 1 & 7))]);
+    __device__ __forceinline__ static u32x4_t at(const Stage &lds, int r) {
+        const int lane = threadIdx.x & 63, j = 2 * (lane >> 5) + S, row = r + (lane & 31);
+        return *reinterpret_cast<const u32x4_t *>(&lds.x[row * 64 + 16 * (j ^ (row >> 2 & 3))]);
     }
-    // Step S of stage Q; R of the next step's operands are read meanwhile.
-    template <int S, int Q, int R>
-    __device__ __forceinline__ void products(const Frags &f, const Scales &sc) {
+    template <int S>
+    __device__ __forceinline__ void read(const Stage &lds, Frags &f, int i) const {
+        if (i < MT) f.a[i] = at<S>(lds, m_of() + 32 * i);
+        if (i < NT) f.w[i] = at<S>(lds, BM + n_of() + 32 * i);
+    }
+    // Step S by groups of MT products, and between them reads of the operands of the step
+    // after it (step 1 - S of `lds`) and, in the second step, the parts of a request (all
+    // at once they hold up the wave).  Nothing moves over a group's end: left alone, the
+    // compiler reads all operands first or multiplies behind the next wait.
+    template <int S, class More>
+    __device__ __forceinline__ void step(const Frags &f, const Scales &sc, const Stage &lds, Frags &next, const Request *r, More more) {
+        constexpr int EACH = LOADS / NT;
+        static_assert(MT <= NT && LOADS % NT == 0, "a group a fragment, as many parts of the request in each");
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (2 * i < NT) {      // early: the next step begins with them
+                read<1 - S>(lds, next, 2 * i);
+                read<1 - S>(lds, next, 2 * i + 1);
+            }
+            if (r)
+#pragma unroll
+                for (int k = 0; k < EACH; ++k) load(*r, EACH * i + k);
+            more(i);
+#pragma unroll
+            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(f.a[k], f.w[i], acc[i][k], sc.a[k], sc.w[i]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    // One stage with nothing to follow.
+    template <int S>
+    __device__ __forceinline__ void step_alone(const Stage &lds, const Scales &sc) {
+        Frags f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) read<S>(lds, f, i);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(f.a[k], f.w[i], acc[i][k], sc.a[k][Q], sc.w[i][Q]);
-        // reads between the first products, and nothing moves over the step's end: left
-        // alone, the compiler reads all operands first or multiplies behind the wait for
-        // the next stage
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // an LDS read
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);      // a matrix instruction
-        }
+            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(f.a[k], f.w[i], acc[i][k], sc.a[k], sc.w[i]);
         __builtin_amdgcn_sched_barrier(0);
-    }
-    template <int Q>
-    __device__ __forceinline__ void multiply(const StageLds<BM, BN> &lds, const Scales &sc) {
-        Frags f, g;
-        read<0>(lds, f);
-        __builtin_amdgcn_sched_barrier(0);
-        read<1>(lds, g);
-        products<0, Q, MT + NT>(f, sc);
-        read<2>(lds, f);
-        products<1, Q, MT + NT>(g, sc);
-        read<3>(lds, g);
-        products<2, Q, MT + NT>(f, sc);
-        products<3, Q, 0>(g, sc);
     }
 };
 
@@ -306,56 +361,102 @@ __device__ __forceinline__ void tile_of(int at, int mt, int nt, int &m, int &n) 
     n = in / rows;
 }
 
-template <int BM, int BN, class T>
-__global__ void __launch_bounds__(256)
+template <int BM, int BN, int WM, int WN, class T>
+__global__ void __launch_bounds__(64 * WM * WN)
 mxfp4_tiles_kernel(const Mx p, int mtiles) {
-    __shared__ StageLds<BM, BN> lds0, lds1;
-    using X = Tile<BM, BN>;
+    __shared__ StageLds<BM, BN> lds0, lds1, lds2, lds3;      // apart: the compiler knows which the loads go to
+    __shared__ ScaleLds<BM, BN> scales0, scales1;
+    using X = Tile<BM, BN, WM, WN>;
     const int piece = (int)(blockIdx.x % p.pieces), at = (int)(blockIdx.x / p.pieces);
     int m0, n0;
     tile_of(at, mtiles, (p.N + BN - 1) / BN, m0, n0);
     m0 *= BM;
     n0 *= BN;
-    const int blocks = p.K / 32, fours = blocks / 32;      // blocks, and stages by four
-    const int each = (fours + p.pieces - 1) / p.pieces;
-    const int t0 = min(piece * each, fours), t1 = min(t0 + each, fours);
+    // whole groups of stages where rows of scales begin at multiples of four bytes
+    const int blocks = p.K / 32, groups = blocks % 4 == 0 ? blocks / (4 * kGroup) : 0;
+    const int each = (groups + p.pieces - 1) / p.pieces;
+    const int g0 = min(piece * each, groups), g1 = min(g0 + each, groups);
     X x;
     x.init(p, m0, n0);
-    typename X::Scales sc, next;
-    if (t0 < t1) {
-        x.request(lds0, t0, 0);
-        x.scales(t0, next);
-    }
-    for (int t = t0; t < t1; ++t) {
-        // the last turn asks for its own stage again: a branch here would let the
-        // compiler move the products behind the loads' end
-        const int u = min(t + 1, t1 - 1);
-        __syncthreads();      // the requested stage is in place, the other buffer has been read
-        sc = next;
-        x.request(lds1, t, 1);
-        x.template multiply<0>(lds0, sc);
-        __syncthreads();
-        x.request(lds0, t, 2);
-        x.template multiply<1>(lds1, sc);
-        __syncthreads();
-        x.request(lds1, t, 3);
-        x.template multiply<2>(lds0, sc);
-        __syncthreads();
-        x.request(lds0, u, 0);
-        x.scales(u, next);
-        x.template multiply<3>(lds1, sc);
+    if (g0 < g1) {
+        constexpr int L = X::LOADS, SC = X::SCALES / 4;      // the next group's scales come in four of the stages
+        static_assert(SC % X::NT == 0 || X::NT % SC == 0, "spread over a step's groups");
+        const int last = kGroup * g1 - 1;
+        typename X::Scales now, then;
+        typename X::Frags f, g;
+        const auto bring = [&](StageLds<BM, BN> &lds, int t) {
+            const auto r = x.request(lds, t);
+#pragma unroll
+            for (int i = 0; i < L; ++i) x.load(r, i);
+        };
+#pragma unroll
+        for (int i = 0; i < X::SCALES; ++i) x.load_scales(scales0, g0, i);
+        bring(lds0, kGroup * g0);
+        bring(lds1, kGroup * g0 + 1);
+        bring(lds2, kGroup * g0 + 2);
+        bring(lds3, kGroup * g0 + 3);
+        wait_loads<3 * L>();
+        meet();
+        x.get_scales(scales0, 0, now);
+        X::halve(now);
+#pragma unroll
+        for (int i = 0; i < X::NT; ++i) x.template read<0>(lds0, f, i);
+        const auto nothing = [](int) __attribute__((always_inline)) {};
+        // Stage q of group u in `here`, the next one in `next`.  Between its two steps the
+        // wave's loads of the next stage are done (of later ones: two stages' codes, and the
+        // scales that the two stages before asked for), and all waves have read the last of
+        // `here`, which takes the fourth stage from now.  Past the last one it is asked for
+        // again: a branch would let the compiler move the products.
+        const auto stage = [&](auto q, StageLds<BM, BN> &here, const StageLds<BM, BN> &next, int u,
+                               const ScaleLds<BM, BN> &mine, ScaleLds<BM, BN> &coming) __attribute__((always_inline)) {
+            constexpr int Q = decltype(q)::value;
+            constexpr int LATER = 2 * L + SC * ((Q >= 1 && Q <= 4) + (Q >= 2 && Q <= 5));
+            x.template step<0>(f, now, here, g, nullptr, nothing);
+            wait_loads<LATER>();
+            meet();
+            const auto r = x.request(here, min(kGroup * u + Q + kStages, last));
+            if constexpr (Q + 1 < kGroup) x.get_scales(mine, Q + 1, then);
+            else x.get_scales(coming, 0, then);
+            x.template step<1>(g, now, next, f, &r, [&](int i) __attribute__((always_inline)) {
+                if constexpr (Q < 4) {
+#pragma unroll
+                    for (int k = 0; k < SC; ++k)
+                        if (k % X::NT == i) x.load_scales(coming, min(u + 1, g1 - 1), SC * Q + k);
+                }
+            });
+            now = then;
+            X::halve(now);
+        };
+        const auto group = [&](int u, const ScaleLds<BM, BN> &mine, ScaleLds<BM, BN> &coming) __attribute__((always_inline)) {
+            stage(std::integral_constant<int, 0>(), lds0, lds1, u, mine, coming);
+            stage(std::integral_constant<int, 1>(), lds1, lds2, u, mine, coming);
+            stage(std::integral_constant<int, 2>(), lds2, lds3, u, mine, coming);
+            stage(std::integral_constant<int, 3>(), lds3, lds0, u, mine, coming);
+            stage(std::integral_constant<int, 4>(), lds0, lds1, u, mine, coming);
+            stage(std::integral_constant<int, 5>(), lds1, lds2, u, mine, coming);
+            stage(std::integral_constant<int, 6>(), lds2, lds3, u, mine, coming);
+            stage(std::integral_constant<int, 7>(), lds3, lds0, u, mine, coming);
+        };
+        int u = g0;
+        for (; u + 1 < g1; u += 2) {
+            group(u, scales0, scales1);
+            group(u + 1, scales1, scales0);
+        }
+        if (u < g1) group(u, scales0, scales1);
+        wait_loads<0>();
     }
     if (piece == p.pieces - 1)      // what is left of K, stage by stage
-        for (int b = 32 * fours; b < blocks; b += 8) {
+        for (int b = 4 * kGroup * groups; b < blocks; b += 4) {
+            typename X::Scales sc;
             __syncthreads();
-            x.request_part(lds0, b, blocks);
-            x.scales_part(b, blocks, sc);
+            x.request_part(lds0, b);
+            x.scales_part(b, sc);
             __syncthreads();
-            x.template multiply<0>(lds0, sc);
+            x.template step_alone<0>(lds0, sc);
+            x.template step_alone<1>(lds0, sc);
         }
     // a lane holds one n of 16 m
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int m1 = m0 + (wave & 1) * (BM / 2) + 4 * (lane >> 5), n1 = n0 + (wave >> 1) * (BN / 2) + (lane & 31);
+    const int lane = threadIdx.x & 63, m1 = m0 + X::m_of() + 4 * (lane >> 5), n1 = n0 + X::n_of() + (lane & 31);
 #pragma unroll
     for (int k = 0; k < X::MT; ++k)
 #pragma unroll
@@ -401,7 +502,7 @@ MxPlan plan_of(int M, int N, int K) {
     p.bm = p.bn = tiles(256) >= 256 ? 256 : 128;
     const int64_t n = tiles(p.bm);
     int64_t pieces = n >= kWant ? 1 : (2 * kWant) / n;
-    const int64_t most = K / 1024;      // at least four stages a piece
+    const int64_t most = K / (128 * kGroup);      // whole groups of stages a piece
     if (pieces > most) pieces = most;
     p.pieces = pieces < 1 ? 1 : (int)pieces;
     if (p.pieces > 1) p.part_bytes = (size_t)p.pieces * M * N * 4;
@@ -416,13 +517,14 @@ void rows_launch(const Mx &p, bool fp32, hipStream_t stream) {
     if (fp32) hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, float>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
     else hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, uint16_t>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
 }
-template <int BM, int BN>
+template <int BM, int BN, int WM, int WN>
 hipError_t tiles_launch(const Mx &p, bool fp32, hipStream_t stream) {
     const int mt = (p.M + BM - 1) / BM;
     const int64_t grid = (int64_t)mt * ((p.N + BN - 1) / BN) * p.pieces;
     if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (fp32) hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, float>), dim3((unsigned)grid), dim3(256), 0, stream, p, mt);
-    else hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, uint16_t>), dim3((unsigned)grid), dim3(256), 0, stream, p, mt);
+    const dim3 threads(64 * WM * WN);
+    if (fp32) hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, WM, WN, float>), dim3((unsigned)grid), threads, 0, stream, p, mt);
+    else hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, WM, WN, uint16_t>), dim3((unsigned)grid), threads, 0, stream, p, mt);
     return hipGetLastError();
 }
 
@@ -463,7 +565,8 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream) {
         else rows_launch<2, 2, 8>(p, a.y_fp32, stream);
         return hipGetLastError();
     }
-    const hipError_t e = plan.bm == 256 ? tiles_launch<256, 256>(p, a.y_fp32, stream) : tiles_launch<128, 128>(p, a.y_fp32, stream);
+    const hipError_t e = plan.bm == 256 ? tiles_launch<256, 256, 2, 2>(p, a.y_fp32, stream)
+                                          : tiles_launch<128, 128, 2, 2>(p, a.y_fp32, stream);
     if (e != hipSuccess || plan.pieces == 1) return e;
     const int64_t n = ((int64_t)a.M * a.N + 255) / 256;
     const unsigned grid = (unsigned)(n < 4096 ? n : 4096);
