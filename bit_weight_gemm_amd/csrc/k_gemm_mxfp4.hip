@@ -18,6 +18,8 @@ using namespace mx;
 // Operands, outputs and sizes of a call.
 struct Mx {
     const uint8_t *ac, *as, *wc, *ws;
+    const uint16_t *x;      // or rows to be quantised in place of ac and as
+    int64_t xs;
     int M, N, K;
     void *y;
     int64_t ys;
@@ -28,9 +30,9 @@ struct Mx {
 __device__ __forceinline__ i32x8m_t frag(const u32x4_t &v) {
     return i32x8m_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
-template <int S>
+template <int SA, int SB = SA>
 __device__ __forceinline__ f32x4m_t mfma16(const u32x4_t &a, const u32x4_t &b, f32x4m_t c, uint32_t sa, uint32_t sb) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, S, (int)sa, S, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag(a), frag(b), c, 4, 4, SA, (int)sa, SB, (int)sb);
 }
 template <int S>
 __device__ __forceinline__ f32x16m_t mfma32(const u32x4_t &a, const u32x4_t &b, f32x16m_t c, uint32_t sa, uint32_t sb) {
@@ -43,7 +45,7 @@ __device__ __forceinline__ uint32_t load4(const uint8_t *p) {      // at any add
 }
 template <class T>
 __device__ __forceinline__ T rounded(float v) {
-    if constexpr (sizeof(T) == 2) return f32_to_bf16_rne(v);
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(uint16_t, (__bf16)v);      // to nearest, ties to even
     else return v;
 }
 
@@ -153,6 +155,181 @@ mxfp4_rows_kernel(const Mx p) {
         for (int w = 0; w < WAVES; ++w) v += flat[w * NT * MT * 256 + at];
         static_cast<T *>(p.y)[m * p.ys + n0 + n] = rounded<T>(v);
     }
+}
+
+// Rows of A that fit into LDS: a workgroup a CU holds them there, quantised by itself where
+// they come as bf16, and its waves walk along W by themselves, 16 rows of it in chunks of
+// 512 k, with kAhead chunks under way.  A workgroup's chunks, tile after tile, are one list,
+// of which each wave takes an equal run; a tile belongs to the wave that begins it, and those
+// that go on with it leave their sums in LDS.
+// Step s of a chunk multiplies blocks 4 s + g in lanes l >> 4 == g, so that a load brings 64
+// bytes in a row of each of 16 rows (16 bytes out of 64, four times: 122 us below, since what
+// the first load brings is gone from L1 before the last).
+// Blocks of a row of A lie an odd number of 16-byte slots apart from row to row, so that
+// sixteen rows' reads of one block meet all banks.
+// Bound by reading W, of which as many bytes are under way as the registers hold: 32 rows to
+// 100001 columns of 5120 take 75 us, 3.7 TB/s (a plain read of W 51, 5.5 TB/s; the kernel
+// below for other sizes 110), one row to 13824 of 5120 10.0 us (11.0).  12 waves with four
+// chunks under way 75.6 and 10.6, eight with six 83 and 10.3; rows quantised by a launch of
+// their own 78.5 and 11.9.
+constexpr int kAhead = 2, kHeldWaves = 16, kHeldThreads = 64 * kHeldWaves;
+constexpr size_t kHeldLds = 160 * 1024;
+struct Held {
+    int chunks, pitch, spitch;      // chunks a row; from row to row: slots of codes, bytes of scales
+    size_t sums, bytes;             // where the sums lie (behind A), and all of it
+};
+__host__ __device__ __forceinline__ Held held_of(int M, int K) {
+    Held h;
+    h.chunks = K / 512;
+    h.pitch = 16 * h.chunks + 1;
+    h.spitch = 16 * h.chunks + 4;
+    h.sums = ((size_t)M * (16 * (size_t)h.pitch + h.spitch) + 15) / 16 * 16;
+    h.bytes = h.sums + (size_t)kHeldWaves * (M > 16 ? 2 : 1) * 64 * 16;
+    return h;
+}
+
+template <int MT, class T>
+__global__ void __launch_bounds__(kHeldThreads)
+mxfp4_held_kernel(const Mx p, int tiles) {
+    extern __shared__ u32x4_t held_lds[];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), g = lane >> 4;
+    const Held h = held_of(p.M, p.K);
+    const int blocks = p.K / 32;
+    uint8_t *scales = reinterpret_cast<uint8_t *>(held_lds + p.M * h.pitch);
+    f32x4m_t *sums = reinterpret_cast<f32x4m_t *>(reinterpret_cast<uint8_t *>(held_lds) + h.sums);
+    // this workgroup's tiles of 16 columns, and this wave's run of their chunks
+    const int wgs = (int)gridDim.x, each = tiles / wgs, rest = tiles % wgs, b = (int)blockIdx.x;
+    const int t0 = b * each + min(b, rest), list = (each + (b < rest)) * h.chunks;
+    const auto begins = [&](int w) { return w * (list / kHeldWaves) + min(w, list % kHeldWaves); };
+    const int c0 = begins(wave), c1 = begins(wave + 1);
+
+    u32x4_t w[kAhead][4], ws[kAhead];
+    int at = t0 + c0 / h.chunks, ac = c0 % h.chunks;      // the tile and chunk to ask for next
+    // By buffer loads: rows past the last and, without a request, chunks past the run (`left`
+    // counts down to it) read as zeros, codes and scales, which add nothing.
+    int left = c1 - c0;
+    const int row = (lane & 15) * blocks;
+    const auto ask = [&](int i) __attribute__((always_inline)) {
+        const int64_t base = 16 * (int64_t)at * blocks + 16 * ac;
+        const int here = left > 0 ? min(16, p.N - 16 * at) * blocks - 16 * ac : 0;      // blocks from there on
+        const auto wr = buffer_of(p.wc + 16 * base, 16 * (int64_t)here);
+        ws[i] = load16(buffer_of(p.ws + base, here), row);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w[i][s] = load16(wr, 16 * (row + g) + 64 * s);
+        --left;
+        if (++ac == h.chunks) {
+            ac = 0;
+            ++at;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ask(i);
+
+    // A into LDS, each row by as many waves as there are for it,
+    // four chunks of a row at a time.  Of a chunk's scale bytes those of blocks g, 4 + g, ..
+    // make up dword g.
+    const int share = max(kHeldWaves / (p.M > 8 ? 16 : p.M > 4 ? 8 : p.M > 2 ? 4 : p.M), 1);
+    for (int m = wave / share; m < p.M; m += kHeldWaves / share)
+        for (int k = wave % share; k < h.chunks; k += 4 * share) {
+            uint8_t *sc = scales + m * h.spitch;
+            if (p.x) {
+                u32x4_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)      // eight elements a lane
+                    v[i] = *reinterpret_cast<const u32x4_t *>(p.x + m * p.xs + 8 * (64 * min(k + i * share, h.chunks - 1) + lane));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = k + i * share;
+                    if (kk >= h.chunks) break;
+                    uint32_t most = amax8(v[i]);
+                    most = max(most, (uint32_t)__shfl_xor((int)most, 1, 64));
+                    most = max(most, (uint32_t)__shfl_xor((int)most, 2, 64));
+                    const uint32_t byte = scale_byte(most), c = codes8(v[i], scale_value(min(byte, 254u)));
+                    reinterpret_cast<uint32_t *>(held_lds)[4 * m * h.pitch + 64 * kk + lane] = byte == 255u ? 0u : c;
+                    if ((lane & 3) == 0) sc[16 * kk + (lane >> 2 & 3) * 4 + (lane >> 4)] = (uint8_t)byte;
+                }
+            } else if (lane < 16) {
+                u32x4_t v[4];
+                uint8_t e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {      // a block a lane
+                    const int64_t j = (int64_t)m * blocks + 16 * min(k + i * share, h.chunks - 1) + lane;
+                    v[i] = *reinterpret_cast<const u32x4_t *>(p.ac + 16 * j);
+                    e[i] = p.as[j];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = k + i * share;
+                    if (kk >= h.chunks) break;
+                    held_lds[m * h.pitch + 16 * kk + lane] = v[i];
+                    sc[16 * kk + (lane & 3) * 4 + (lane >> 2)] = e[i];
+                }
+            }
+        }
+    __syncthreads();
+    int arow[MT], srow[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {
+        const int m = min(16 * j + (lane & 15), p.M - 1);
+        arow[j] = m * h.pitch + g;
+        srow[j] = m * h.spitch + 4 * g;
+    }
+    f32x4m_t acc[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[j] = f32x4m_t{0, 0, 0, 0};
+    int tile = t0 + c0 / h.chunks, c = c0 % h.chunks;
+    bool leads = c != 0;      // the tile was begun by another wave
+    const auto leave = [&] {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sums[(wave * MT + j) * 64 + lane] = acc[j];
+    };
+    const auto store = [&] {
+        const int n = 16 * tile + 4 * g;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+            const int m = 16 * j + (lane & 15);
+            if (m >= p.M) continue;
+            T *y = static_cast<T *>(p.y) + m * p.ys + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.N) y[e] = rounded<T>(acc[j][e]);
+        }
+    };
+    for (int u = c0; u < c1; u += kAhead)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const u32x4_t e = ws[i] >> (uint32_t)(8 * g);
+            const bool in = u + i < c1;
+            const int k = in ? c : 0;      // past the run: zeros times any of A
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const u32x4_t *a = held_lds + arow[j] + 16 * k;
+                const uint32_t as = *reinterpret_cast<const uint32_t *>(scales + srow[j] + 16 * k);
+                acc[j] = mfma16<0, 0>(w[i][0], a[0], acc[j], e.x, as);
+                acc[j] = mfma16<0, 1>(w[i][1], a[4], acc[j], e.y, as);
+                acc[j] = mfma16<0, 2>(w[i][2], a[8], acc[j], e.z, as);
+                acc[j] = mfma16<0, 3>(w[i][3], a[12], acc[j], e.w, as);
+            }
+            ask(i);
+            __builtin_amdgcn_sched_barrier(0);      // the next chunk's reads of A would only take registers here
+            c += in;
+            if (c == h.chunks) {
+                if (leads) leave();
+                else store();
+                leads = false;
+                c = 0;
+                ++tile;
+#pragma unroll
+                for (int j = 0; j < MT; ++j) acc[j] = f32x4m_t{0, 0, 0, 0};
+            }
+        }
+    if (leads) leave();      // the tile does not end here either
+    __syncthreads();
+    if (leads || c == 0) return;
+    for (int v = wave + 1; v < kHeldWaves && begins(v) < (tile + 1 - t0) * h.chunks; ++v)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[j] += sums[(v * MT + j) * 64 + lane];
+    store();
 }
 
 // ---------------------------------------------------------------- many rows
@@ -490,6 +667,9 @@ mxfp4_join_kernel(const Mx p) {
 constexpr int kRows = 32;              // rows of A up to which W is streamed
 constexpr int kWant = 256;             // workgroups that the pieces of K are to make
 
+constexpr int kCUs = 256;
+
+bool held(int M, int K) { return M <= kRows && K % 512 == 0 && held_of(M, K).bytes <= kHeldLds; }
 struct MxPlan {
     bool rows;
     int bm, bn, pieces;
@@ -517,6 +697,16 @@ void rows_launch(const Mx &p, bool fp32, hipStream_t stream) {
     if (fp32) hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, float>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
     else hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, uint16_t>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
 }
+template <int MT, class T>
+hipError_t held_launch(const Mx &p, hipStream_t stream) {
+    const int lds = (int)held_of(p.M, p.K).bytes, tiles = (p.N + 15) / 16;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(mxfp4_held_kernel<MT, T>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kHeldLds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((mxfp4_held_kernel<MT, T>), dim3(tiles < kCUs ? tiles : kCUs), dim3(kHeldThreads), lds, stream, p, tiles);
+    return hipGetLastError();
+}
+
 template <int BM, int BN, int WM, int WN>
 hipError_t tiles_launch(const Mx &p, bool fp32, hipStream_t stream) {
     const int mt = (p.M + BM - 1) / BM;
@@ -550,7 +740,8 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream) {
     const MxPlan plan = plan_of(a.M, a.N, a.K);
     const uint8_t *ac = a.a_codes, *as = a.a_scales;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
-    if (a.x) {
+    const bool holds = held(a.M, a.K), own = a.x && holds;
+    if (a.x && !own) {
         uint8_t *c = ws, *s = ws + codes_bytes(a.M, a.K);
         ws = s + scales_bytes(a.M, a.K);
         const hipError_t e = launch_quant_mxfp4(a.x, a.x_stride, false, a.M, a.K, c, s, stream);
@@ -558,8 +749,12 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream) {
         ac = c;
         as = s;
     }
-    const Mx p{ac, as, a.w_codes, a.w_scales, a.M, a.N, a.K, a.y, a.y_stride,
+    const Mx p{ac, as, a.w_codes, a.w_scales, own ? a.x : nullptr, a.x_stride, a.M, a.N, a.K, a.y, a.y_stride,
                plan.pieces > 1 ? reinterpret_cast<float *>(ws) : nullptr, plan.pieces};
+    if (holds) {
+        if (a.M <= 16) return a.y_fp32 ? held_launch<1, float>(p, stream) : held_launch<1, uint16_t>(p, stream);
+        return a.y_fp32 ? held_launch<2, float>(p, stream) : held_launch<2, uint16_t>(p, stream);
+    }
     if (plan.rows) {
         if (a.M <= 16) rows_launch<1, 1, 8>(p, a.y_fp32, stream);
         else rows_launch<2, 2, 8>(p, a.y_fp32, stream);

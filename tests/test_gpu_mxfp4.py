@@ -214,3 +214,29 @@ def test_captured(M):
         want = B.biloco_gemm_mxfp4_quant(x, *w)
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("K", [512, 1536, 5120])
+@pytest.mark.parametrize("M", [1, 3, 6, 17, 32])
+def test_few_rows_many_columns(M, K):
+    """Several tiles a CU, some of them cut between waves; a NaN in the last block of one
+    row of W and of A's last row stays in that column and row."""
+    N = 16 * 256 * 2 + 16 * 77 + 5
+    x, a, w = _operands(K + M, M, N, K)
+    for dtype in (torch.float32, torch.bfloat16):
+        _compare(B.biloco_gemm_mxfp4(*a, *w, out_dtype=dtype), a, w)
+    assert torch.equal(B.biloco_gemm_mxfp4(*a, *w), B.biloco_gemm_mxfp4_quant(x, *w))
+    x[M - 1, K - 1] = float("inf")
+    w[1][N - 3, K // 32 - 1] = 255
+    y = B.biloco_gemm_mxfp4_quant(x, *w)
+    assert bool(y[M - 1].isnan().all()) and bool(y[:, N - 3].isnan().all())
+    y[M - 1], y[:, N - 3] = 0, 0
+    assert not bool(y.isnan().any())
+
+
+@pytest.mark.parametrize("M,K", [(16, 16384), (17, 8192), (32, 7168), (32, 8192)])
+def test_few_long_rows(M, K):
+    """On both sides of what a CU's LDS holds."""
+    x, a, w = _operands(K, M, 200, K)
+    _compare(B.biloco_gemm_mxfp4(*a, *w, out_dtype=torch.float32), a, w)
+    assert torch.equal(B.biloco_gemm_mxfp4(*a, *w), B.biloco_gemm_mxfp4_quant(x, *w))
