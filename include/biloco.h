@@ -509,7 +509,7 @@ biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
 
 /* The same for rows that are quantised first, as biloco_quant_mxfp4 does:
  * x [M][K] bf16, x_stride in elements, a multiple of 8, at least K.  The codes
- * stay in the workspace.  One to three launches. */
+ * stay in the workspace or on the chip.  One to three launches. */
 biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const uint8_t *w_codes,
                                       const uint8_t *w_scales, int32_t M, int32_t N, int32_t K,
                                       void *y, int64_t y_stride, int32_t y_fp32, void *workspace,
@@ -539,7 +539,7 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
  * workspace: >= biloco_attn_shared_workspace_bytes(...) bytes, no fill needed; not
  *   shared by calls that can run at the same time.
  * 1 <= n_groups <= 65535.  Contents that break these rules give unspecified values,
- * but no access outside the arrays.  T = 0 or B = 0 does nothing.  Two to six
+ * but no access outside the arrays.  T = 0 or B = 0 does nothing.  One to six
  * launches. */
 biloco_status biloco_attn_shared(const uint8_t *k_codes, const uint8_t *v_codes,
                                  const uint8_t *k_scales, const uint8_t *v_scales,
@@ -586,7 +586,7 @@ biloco_status biloco_attn_shared_workspace_bytes(int32_t B, int32_t T, int32_t q
  *   u fp32 [rows]; token int32 [rows]; logprob fp32 [rows] or NULL
  *   workspace: >= biloco_sample_workspace_bytes(...) bytes, no fill needed; not
  *     shared by calls that can run at the same time.
- * 1 <= V < 2^20.  rows = 0 does nothing.  One to three launches. */
+ * 1 <= V < 2^20.  rows = 0 does nothing.  One to five launches. */
 biloco_status biloco_sample(const void *logits, int64_t stride, int32_t fp32, int32_t rows,
                             int32_t V, const float *temperature, const int32_t *top_k,
                             const float *top_p, const float *min_p, const float *u,
