@@ -349,9 +349,7 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int dim, int rows, 
 // are left over end at once.  K::of(b): the call's arguments for sequence b.  An item
 // that is one piece is written as it is to be, unless it is part of a longer one.
 template <int D, class K>
-__global__ void __launch_bounds__(64 * kSplitWaves, 2)
-attn_split_kernel(const K k, int which, int most_rows) {
-    __shared__ JoinLds<D, kSplitWaves> lds;
+__device__ __forceinline__ void split_rows(const K &k, int which, int most_rows, int wg, JoinLds<D, kSplitWaves> &lds) {
     const AttnArgs &a = k.a;
     const int wave = uniform((int)(threadIdx.x >> 6));
     const auto shift_of = [&](const Seq &s) { return row_shift_of(rows_of(a, s, most_rows)); };
@@ -380,12 +378,12 @@ attn_split_kernel(const K k, int which, int most_rows) {
         if (wave_sum_dpp(count[z]) * (float)a.kv_heads <= (float)kPieces) more = z;
     const int size = even + (uniform(more) <= even ? uniform(more) : 0);
     const auto pieces = [&](const Seq &s) { return (int)(((uint32_t)units(s) + size - 1) / (uint32_t)size); };
-    const int b = uniform(find_seq(a.B, blockIdx.x, before,
+    const int b = uniform(find_seq(a.B, wg, before,
                                    [&](int i) { return (int64_t)pieces(seq_of(k.of(i), i, which)) * a.kv_heads; }));
     if (b < 0) return;
     const auto &part = k.of(b);
     const Seq s = seq_uniform(part, b, which);
-    const int n = uniform(pieces(s)), at = (int)(blockIdx.x - uniform(before));
+    const int n = uniform(pieces(s)), at = (int)(wg - uniform(before));
     const int h = uniform(at / n), u0 = uniform((at - h * n) * size);
     const int rows = rows_of(a, s, most_rows), row_shift = shift_of(s), lanes = kSplitWaves >> row_shift;
     const int mine = 16 * (wave & ((1 << row_shift) - 1));
@@ -394,9 +392,16 @@ attn_split_kernel(const K k, int which, int most_rows) {
     Stage<D> st;
     if (mine < rows)
         x.run(part, w, s, st, false, u0 * lanes + (wave >> row_shift), min((u0 + size) * lanes, s.c.nc), lanes);
-    if (u0 == 0 && threadIdx.x == 0) static_cast<Begun *>(a.ws)[b * a.kv_heads + h] = Begun{(int)blockIdx.x, n};
+    if (u0 == 0 && threadIdx.x == 0) static_cast<Begun *>(a.ws)[b * a.kv_heads + h] = Begun{wg, n};
     finish<D, kSplitWaves>(a, s, x, lds, h, rows, 1 << row_shift,
-                           n == 1 && !K::kPart ? nullptr : part_of(a, D, most_rows, blockIdx.x), most_rows);
+                           n == 1 && !K::kPart ? nullptr : part_of(a, D, most_rows, wg), most_rows);
+}
+
+template <int D, class K>
+__global__ void __launch_bounds__(64 * kSplitWaves, 2)
+attn_split_kernel(const K k, int which, int most_rows) {
+    __shared__ JoinLds<D, kSplitWaves> lds;
+    split_rows<D>(k, which, most_rows, (int)blockIdx.x, lds);
 }
 
 }  // namespace attn

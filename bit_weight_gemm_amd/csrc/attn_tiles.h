@@ -295,10 +295,7 @@ struct TileWork {
 // walk over chunks as a function of its own costs the compiler 32 registers' moves a
 // turn (chunks of 64 channels 356 -> 380 us).
 template <int D, class K>
-__global__ void __launch_bounds__(256, 2)
-attn_tiles_kernel(const K k, int splits) {
-    __shared__ TileLds<D> lds;
-    __shared__ typename K::Lds more;
+__device__ __forceinline__ void tile_rows(const K &k, int splits, TileLds<D> &lds, typename K::Lds &more) {
     Rows32<D> w;
     TileWork<typename K::Args> t{k.args()};
     if (!k.begin(w, t, more, splits)) return;
@@ -367,6 +364,14 @@ attn_tiles_kernel(const K k, int splits) {
         }
     }
     k.end(w, t, w.l + __shfl_xor(w.l, 32, 64), splits);
+}
+
+template <int D, class K>
+__global__ void __launch_bounds__(256, 2)
+attn_tiles_kernel(const K k, int splits) {
+    __shared__ TileLds<D> lds;
+    __shared__ typename K::Lds more;
+    tile_rows<D>(k, splits, lds, more);
 }
 
 // A row's sums as a piece of them: [kTileRows][D], then maxima and sums of the weights.

@@ -202,6 +202,24 @@ struct OwnRows {
     __device__ __forceinline__ PartArgs of(int b) const { return PartArgs(a, tables_of(s, a.B).from[b], 0x7FFFFFFF); }
 };
 
+// Both in one launch, the tiles' workgroups first; neither waits for the other.  Four answers
+// behind 16 shared pages, groups with drafts and many answers: 18.1, 39.2 and 77 us, as two
+// launches 25.5, 48.5 and 82.
+template <int D>
+__global__ void __launch_bounds__(256, 2)
+attn_shared_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int most_rows, int tiles, int splits) {
+    union Lds {
+        struct {
+            TileLds<D> chunks;
+            SharedTiles::Lds rows;
+        } tiles;
+        JoinLds<D, kSplitWaves> join;
+    };
+    __shared__ Lds lds;
+    if ((int)blockIdx.x < tiles) tile_rows<D>(SharedTiles{a, s, which}, splits, lds.tiles.chunks, lds.tiles.rows);
+    else split_rows<D>(OwnRows{a, s}, which, most_rows, (int)blockIdx.x - tiles, lds.join);
+}
+
 // Joins a row's parts: a wave a row.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -300,13 +318,11 @@ hipError_t launch(const AttnArgs &a, SharedAttnArgs s, const SharedPlan &p, hipS
     s.parts = ws + p.table_bytes + p.own_bytes;
     const int64_t tiles = (int64_t)p.shared_tiles * p.splits * a.kv_heads, pieces = p.items + kPieces;
     const int64_t join = p.items * ((p.most_rows + 3) / 4);
-    if (tiles > 0x7FFFFFFF || pieces > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (tiles + pieces > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL(attn_shared_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, own, s, which, p.shared_tiles);
-    if (tiles > 0)
-        hipLaunchKernelGGL((attn_tiles_kernel<D, SharedTiles>), dim3((unsigned)tiles), dim3(256), 0, stream,
-                           SharedTiles{own, s, which}, p.splits);
-    hipLaunchKernelGGL((attn_split_kernel<D, OwnRows>), dim3((unsigned)pieces), dim3(64 * kSplitWaves), 0, stream,
-                       OwnRows{own, s}, which, p.most_rows);
+    static_assert(kSplitWaves == 4, "both kinds of workgroups in one grid");
+    hipLaunchKernelGGL((attn_shared_kernel<D>), dim3((unsigned)(tiles + pieces)), dim3(256), 0, stream, own, s, which,
+                       p.most_rows, (int)tiles, p.splits);
     hipLaunchKernelGGL((attn_shared_join_kernel<D>), dim3((unsigned)join), dim3(256), 0, stream, own, s, which, p.most_rows,
                        (int)p.items, p.splits);
     return hipGetLastError();
