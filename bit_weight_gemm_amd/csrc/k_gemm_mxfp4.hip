@@ -665,7 +665,9 @@ mxfp4_join_kernel(const Mx p) {
 }
 
 constexpr int kRows = 32;              // rows of A up to which W is streamed
-constexpr int kWant = 256;             // workgroups that the pieces of K are to make
+// Workgroups that the pieces of K are to make, one a CU: 200 rows of 13824 to 5120 in 3
+// pieces (240 workgroups) 31.4 us, in 2 36.7, in 6 34.0, in 9 44.
+constexpr int kWant = 256;
 
 constexpr int kCUs = 256;
 
@@ -681,7 +683,7 @@ MxPlan plan_of(int M, int N, int K) {
     const auto tiles = [&](int b) { return (int64_t)((M + b - 1) / b) * ((N + b - 1) / b); };
     p.bm = p.bn = tiles(256) >= 256 ? 256 : 128;
     const int64_t n = tiles(p.bm);
-    int64_t pieces = n >= kWant ? 1 : (2 * kWant) / n;
+    int64_t pieces = n >= kWant ? 1 : (kWant + n / 2) / n;
     const int64_t most = K / (128 * kGroup);      // whole groups of stages a piece
     if (pieces > most) pieces = most;
     p.pieces = pieces < 1 ? 1 : (int)pieces;
@@ -724,7 +726,7 @@ size_t mxfp4_plan_bytes(int M, int N, int K, bool quant) {
     return plan_of(M, N, K).part_bytes + (quant ? codes_bytes(M, K) + scales_bytes(M, K) : 0);
 }
 // For every call of up to M rows: only where there are fewer than kWant tiles of 128
-// is K cut, into at most 2 kWant pieces of tiles in all.
+// is K cut, into at most 3/2 kWant pieces of tiles in all.
 size_t mxfp4_ws_bytes(int M, int N, int K) {
     size_t most = 0;
     for (int64_t m = 128;; m += 128) {
