@@ -21,6 +21,7 @@ struct Mx {
     const uint16_t *x;      // or rows to be quantised in place of ac and as
     int64_t xs;
     int M, N, K;
+    int spitch;      // bytes from one row of scales to the next (many rows)
     void *y;
     int64_t ys;
     float *part;      // sums of the pieces of K, [piece][M][N], or NULL
@@ -340,7 +341,12 @@ mxfp4_held_kernel(const Mx p, int tiles) {
 // j ^ (r >> 2 & 3), so that sixteen successive rows' reads of one block meet all banks.
 // Lanes of half h multiply blocks 2 h and 2 h + 1 of a stage, one a step; their scale
 // bytes are half a dword.  Scales come by 32 a row, for eight stages (a load of a dword a
-// row costs as many requests to L2 as two stages' codes).
+// row costs as many requests to L2 as two stages' codes: one a stage 249 us for the last size
+// below where four at a time took 205).
+// Bound by the matrix instructions and what holds them up: 4096 x 8192 x 8192 takes 177 us of
+// its own, 3.1 PFLOP/s, and 195 with the quantisation; the instruction alone on random
+// operands 90 us (6.1 PFLOP/s, from registers) or 103 (from LDS).  Two buffers of 256 k
+// instead 200 us with it; eight waves 194, but their registers spill.
 constexpr int kStages = 4, kGroup = 8;      // stages in LDS; stages whose scales come together
 
 template <int BM, int BN>
@@ -359,6 +365,13 @@ __device__ __forceinline__ void wait_loads() {
     static_assert(N < 64, "the counter's range");
     __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x70);
 }
+// 16 or 4 bytes a lane straight into LDS.
+__device__ __forceinline__ void bring16(const uint8_t *from, int bytes, uint32_t off, uint8_t *to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(from, bytes), (__attribute__((address_space(3))) void *)to, 16, (int)off, 0, 0, 0);
+}
+__device__ __forceinline__ void bring4(const uint8_t *from, int bytes, uint32_t off, uint8_t *to) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(from, bytes), (__attribute__((address_space(3))) void *)to, 4, (int)off, 0, 0, 0);
+}
 __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
@@ -372,9 +385,8 @@ struct Tile {
     static constexpr int SROWS = THREADS / 8, SCALES = (BM + BN) / SROWS;       // likewise of scales
     using Stage = StageLds<BM, BN>;
     f32x16m_t acc[NT][MT];
-    uint32_t from[LOADS];               // byte offsets of a thread's codes from the tile's rows
     const uint8_t *a, *w, *sa, *sw;     // the tile's first rows
-    int mlast, nlast, blocks;           // the last rows that are there, blocks a row
+    int m, n, blocks, spitch;           // rows that are there, blocks a row, bytes from one row of scales to the next
 
     // The wave's first row of A and of W.
     __device__ __forceinline__ static int m_of() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) % WM * (32 * MT); }
@@ -387,20 +399,15 @@ struct Tile {
     };
 
     __device__ __forceinline__ void init(const Mx &p, int m0, int n0) {
-        const int tid = threadIdx.x;
         const uint32_t pitch = p.K / 2;
         blocks = p.K / 32;
-        mlast = min(BM, p.M - m0) - 1;
-        nlast = min(BN, p.N - n0) - 1;
+        spitch = p.spitch;
+        m = min(BM, p.M - m0);
+        n = min(BN, p.N - n0);
         a = p.ac + (int64_t)m0 * pitch;
-        sa = p.as + (int64_t)m0 * blocks;
+        sa = p.as + (int64_t)m0 * spitch;
         w = p.wc + (int64_t)n0 * pitch;
-        sw = p.ws + (int64_t)n0 * blocks;
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const int row = STEP * i + tid / 4;
-            from[i] = (uint32_t)(STEP * i < BM ? min(row, mlast) : min(row - BM, nlast)) * pitch + 16 * mine();
-        }
+        sw = p.ws + (int64_t)n0 * spitch;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -409,29 +416,37 @@ struct Tile {
                 for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     }
 
-    // A stage on its way into LDS in LOADS parts; t: the stage.
+    // Stage t on its way into LDS in LOADS parts.  Buffer loads: rows past the last come as
+    // zeros.  So do blocks past a row's last, in A by an offset that is past everything; in W
+    // they are whatever follows, which A's zeros make nothing of.
     struct Request {
         const uint8_t *a, *w;
+        int bytes_a, bytes_w;      // up to the tile's end
         uint8_t *to;
+        uint32_t from_a, from_w;
     };
     __device__ __forceinline__ Request request(Stage &lds, int t) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-        const int64_t at = 64 * (int64_t)t;
-        return Request{a + at, w + at, &lds.x[1024 * wave]};
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), tid = opaque(threadIdx.x);
+        const int64_t at = 64 * (int64_t)t, pitch = 16 * (int64_t)blocks;
+        const uint32_t from = tid / 4 * 16 * blocks + 16 * mine();
+        return Request{a + at, w + at, (int)max(m * pitch - at, (int64_t)0), (int)max(n * pitch - at, (int64_t)0), &lds.x[1024 * wave],
+                       4 * t + mine() < blocks ? from : (uint32_t)kOob, from};
     }
     __device__ __forceinline__ void load(const Request &r, int i) const {
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((STEP * i < BM ? r.a : r.w) + from[i]),
-                                         (__attribute__((address_space(3))) void *)(r.to + 16 * THREADS * i), 16, 0, 0);
+        const bool is_a = STEP * i < BM;
+        const uint32_t pitch = 16 * blocks, off = is_a ? r.from_a + STEP * i * pitch : r.from_w + (STEP * i - BM) * pitch;
+        bring16(is_a ? r.a : r.w, is_a ? r.bytes_a : r.bytes_w, off, r.to + 16 * THREADS * i);
     }
-    // Part i of SCALES of the scales of group t: a dword a lane, since they begin at
-    // multiples of four bytes.
+    // Part i of SCALES of the scales of group t: a dword a lane, since rows of them begin at
+    // multiples of four bytes.  Past a row's end they are zeros (2^-127), in both, lest the
+    // next row's NaN come in.
     __device__ __forceinline__ void load_scales(ScaleLds<BM, BN> &lds, int t, int i) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), row = SROWS * i + (int)threadIdx.x / 8;
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), tid = opaque(threadIdx.x);
         const bool is_a = SROWS * i < BM;
-        const uint32_t at = (uint32_t)(is_a ? min(row, mlast) : min(row - BM, nlast)) * (uint32_t)blocks + 4 * (threadIdx.x & 7);
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)((is_a ? sa : sw) + 32 * (int64_t)t + at),
-                                         (__attribute__((address_space(3))) void *)&lds.x[4 * THREADS * i + 256 * wave],
-                                         4, 0, 0);
+        const int row = SROWS * i - (is_a ? 0 : BM) + tid / 8, col = 4 * (tid & 7);
+        const int64_t at = 32 * (int64_t)t, pitch = spitch;
+        bring4((is_a ? sa : sw) + at, (int)((is_a ? m : n) * pitch - at), 32 * t + col < blocks ? row * spitch + col : kOob,
+               &lds.x[4 * THREADS * i + 256 * wave]);
     }
     // Dwords of its stage q.
     __device__ __forceinline__ static uint32_t scale_at(const ScaleLds<BM, BN> &lds, int r, int q) {
@@ -452,31 +467,6 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < NT; ++i) sc.w[i] >>= shift;
     }
-    // Four blocks from b0 on, of which those past the last are zeros with scale 1: through
-    // registers.
-    __device__ __forceinline__ void request_part(Stage &lds, int b0) const {
-        const int tid = threadIdx.x, b = b0 + mine();
-#pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            u32x4_t v{0, 0, 0, 0};
-            if (b < blocks) v = *reinterpret_cast<const u32x4_t *>((STEP * i < BM ? a : w) + from[i] + 16 * (int64_t)b0);
-            *reinterpret_cast<u32x4_t *>(&lds.x[16 * (THREADS * i + tid)]) = v;
-        }
-    }
-    __device__ __forceinline__ uint32_t scales_of(const uint8_t *p, int b0) const {
-        uint32_t v = 0;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) v |= (b0 + s < blocks ? (uint32_t)p[b0 + s] : 127u) << (8 * s);
-        return v;
-    }
-    __device__ __forceinline__ void scales_part(int b0, Scales &sc) const {
-        const int lane = threadIdx.x & 63, b = b0 + 2 * (lane >> 5);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) sc.a[i] = scales_of(sa + (int64_t)min(m_of() + 32 * i + (lane & 31), mlast) * blocks, b);
-#pragma unroll
-        for (int i = 0; i < NT; ++i) sc.w[i] = scales_of(sw + (int64_t)min(n_of() + 32 * i + (lane & 31), nlast) * blocks, b);
-    }
-
     // Operands of a step of a stage.
     struct Frags {
         u32x4_t a[MT], w[NT];
@@ -514,18 +504,6 @@ struct Tile {
             __builtin_amdgcn_sched_barrier(0);
         }
     }
-    // One stage with nothing to follow.
-    template <int S>
-    __device__ __forceinline__ void step_alone(const Stage &lds, const Scales &sc) {
-        Frags f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) read<S>(lds, f, i);
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int k = 0; k < MT; ++k) acc[i][k] = mfma32<S>(f.a[k], f.w[i], acc[i][k], sc.a[k], sc.w[i]);
-        __builtin_amdgcn_sched_barrier(0);
-    }
 };
 
 // Tile `at` of mt x nt: each of the 8 XCDs (workgroups go round them) takes a run of
@@ -549,8 +527,7 @@ mxfp4_tiles_kernel(const Mx p, int mtiles) {
     tile_of(at, mtiles, (p.N + BN - 1) / BN, m0, n0);
     m0 *= BM;
     n0 *= BN;
-    // whole groups of stages where rows of scales begin at multiples of four bytes
-    const int blocks = p.K / 32, groups = blocks % 4 == 0 ? blocks / (4 * kGroup) : 0;
+    const int groups = (p.K / 32 + 4 * kGroup - 1) / (4 * kGroup);      // of stages
     const int each = (groups + p.pieces - 1) / p.pieces;
     const int g0 = min(piece * each, groups), g1 = min(g0 + each, groups);
     X x;
@@ -619,19 +596,9 @@ mxfp4_tiles_kernel(const Mx p, int mtiles) {
             group(u, scales0, scales1);
             group(u + 1, scales1, scales0);
         }
-        if (u < g1) group(u, scales0, scales1);
+        for (; u < g1; ++u) group(u, scales0, scales1);      // once at most; as a plain branch it costs the compiler registers
         wait_loads<0>();
     }
-    if (piece == p.pieces - 1)      // what is left of K, stage by stage
-        for (int b = 4 * kGroup * groups; b < blocks; b += 4) {
-            typename X::Scales sc;
-            __syncthreads();
-            x.request_part(lds0, b);
-            x.scales_part(b, sc);
-            __syncthreads();
-            x.template step_alone<0>(lds0, sc);
-            x.template step_alone<1>(lds0, sc);
-        }
     // a lane holds one n of 16 m
     const int lane = threadIdx.x & 63, m1 = m0 + X::m_of() + 4 * (lane >> 5), n1 = n0 + X::n_of() + (lane & 31);
 #pragma unroll
@@ -664,14 +631,39 @@ mxfp4_join_kernel(const Mx p) {
     }
 }
 
-constexpr int kRows = 32;              // rows of A up to which W is streamed
+// Rows of scales to rows that begin at multiples of four bytes, zeros at their ends.
+__global__ void __launch_bounds__(256)
+mxfp4_scales_kernel(const uint8_t *__restrict__ a, int M, const uint8_t *__restrict__ w, int N, int blocks, uint32_t *__restrict__ out) {
+    const int dwords = (blocks + 3) / 4;
+    const int64_t n = ((int64_t)M + N) * dwords;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+        const int64_t row = e / dwords;
+        const int j = (int)(e - row * dwords);
+        const uint8_t *from = row < M ? a + row * blocks : w + (row - M) * blocks;
+        uint32_t v = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 * j + i < blocks) v |= (uint32_t)from[4 * j + i] << (8 * i);
+        out[e] = v;
+    }
+}
+
+// Rows of A up to which W is streamed.  32 rows of 5120 to 13824 20.0 us, in tiles 22.2; 8192
+// to 8192 16.8 and 19.6; 17 rows of 5120 to 5120 9.5 and 14.2; 48 are past the kernels' operands.
+constexpr int kRows = 32;
 // Workgroups that the pieces of K are to make, one a CU: 200 rows of 13824 to 5120 in 3
 // pieces (240 workgroups) 31.4 us, in 2 36.7, in 6 34.0, in 9 44.
 constexpr int kWant = 256;
 
 constexpr int kCUs = 256;
 
-bool held(int M, int K) { return M <= kRows && K % 512 == 0 && held_of(M, K).bytes <= kHeldLds; }
+// Every workgroup quantises all of A, which pays where it has much of W to read or A is
+// short.  M rows of K to N, held against streamed: 1 x 5120 to 5120 8.0 and 8.0 us, 8 rows 9.4
+// and 9.0, 32 rows 15.0 and 10.9; to 13824 1 row 12.0 and 12.9, 8 rows 13.5 and 14.9, 32 rows
+// 20.0 and 20.5; 8192 to 8192 1 row 11.5 and 13.2, 16 rows 16.8 and 15.9.
+bool held(int M, int N, int K) {
+    return M <= kRows && (M <= 4 || N >= 48 * kCUs) && K % 512 == 0 && held_of(M, K).bytes <= kHeldLds;
+}
 struct MxPlan {
     bool rows;
     int bm, bn, pieces;
@@ -681,14 +673,23 @@ MxPlan plan_of(int M, int N, int K) {
     MxPlan p{M <= kRows, 0, 0, 1, 0};
     if (p.rows) return p;
     const auto tiles = [&](int b) { return (int64_t)((M + b - 1) / b) * ((N + b - 1) / b); };
-    p.bm = p.bn = tiles(256) >= 256 ? 256 : 128;
+    // Large tiles where they fill at least four fifths of their rounds over the CUs: 2048 x
+    // 8192 x 8192 (256 of them) 87 us, in small ones 109; 4096 x 4096 x 4096 54 and 60; but
+    // 4096 x 5120 x 5120 (320) 110 and 84, 1500 x 13824 x 5120 (324) 114 and 95.
+    const int64_t large = tiles(256), rounds = (large + kCUs - 1) / kCUs;
+    p.bm = p.bn = 5 * large >= 4 * kCUs * rounds ? 256 : 128;
     const int64_t n = tiles(p.bm);
     int64_t pieces = n >= kWant ? 1 : (kWant + n / 2) / n;
-    const int64_t most = K / (128 * kGroup);      // whole groups of stages a piece
+    const int64_t most = ((int64_t)K + 128 * kGroup - 1) / (128 * kGroup);      // groups of stages
     if (pieces > most) pieces = most;
     p.pieces = pieces < 1 ? 1 : (int)pieces;
     if (p.pieces > 1) p.part_bytes = (size_t)p.pieces * M * N * 4;
     return p;
+}
+// Of A's and W's rows of scales in multiples of four bytes, where they are not so already.
+size_t padded_bytes(int64_t M, int64_t N, int K) {
+    const int64_t blocks = K / 32;
+    return M <= kRows || blocks % 4 == 0 ? 0 : (size_t)((M + N) * ((blocks + 3) / 4 * 4) + 255) / 256 * 256;
 }
 size_t codes_bytes(int64_t M, int64_t K) { return ((size_t)(M * (K / 2)) + 255) / 256 * 256; }
 size_t scales_bytes(int64_t M, int64_t K) { return ((size_t)(M * (K / 32)) + 255) / 256 * 256; }
@@ -723,7 +724,7 @@ hipError_t tiles_launch(const Mx &p, bool fp32, hipStream_t stream) {
 }  // namespace
 
 size_t mxfp4_plan_bytes(int M, int N, int K, bool quant) {
-    return plan_of(M, N, K).part_bytes + (quant ? codes_bytes(M, K) + scales_bytes(M, K) : 0);
+    return plan_of(M, N, K).part_bytes + padded_bytes(M, N, K) + (quant ? codes_bytes(M, K) + scales_bytes(M, K) : 0);
 }
 // For every call of up to M rows: only where there are fewer than kWant tiles of 128
 // is K cut, into at most 3/2 kWant pieces of tiles in all.
@@ -735,14 +736,14 @@ size_t mxfp4_ws_bytes(int M, int N, int K) {
         if (p.part_bytes > most) most = p.part_bytes;
         if (m >= M || (!p.rows && ((at + 127) / 128) * ((N + 127) / 128) >= kWant)) break;
     }
-    return most + codes_bytes(M, K) + scales_bytes(M, K);
+    return most + padded_bytes(M, N, K) + codes_bytes(M, K) + scales_bytes(M, K);
 }
 
 hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream) {
     const MxPlan plan = plan_of(a.M, a.N, a.K);
     const uint8_t *ac = a.a_codes, *as = a.a_scales;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
-    const bool holds = held(a.M, a.K), own = a.x && holds;
+    const bool holds = held(a.M, a.N, a.K), own = a.x && holds;
     if (a.x && !own) {
         uint8_t *c = ws, *s = ws + codes_bytes(a.M, a.K);
         ws = s + scales_bytes(a.M, a.K);
@@ -751,7 +752,18 @@ hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream) {
         ac = c;
         as = s;
     }
-    const Mx p{ac, as, a.w_codes, a.w_scales, own ? a.x : nullptr, a.x_stride, a.M, a.N, a.K, a.y, a.y_stride,
+    const uint8_t *wsc = a.w_scales;
+    int pitch = a.K / 32;
+    if (const size_t n = padded_bytes(a.M, a.N, a.K)) {
+        const int64_t dwords = (int64_t)(n / 4), grid = (dwords + 255) / 256;
+        hipLaunchKernelGGL(mxfp4_scales_kernel, dim3((unsigned)(grid < 4096 ? grid : 4096)), dim3(256), 0, stream, as, a.M, wsc, a.N,
+                           pitch, reinterpret_cast<uint32_t *>(ws));
+        pitch = (pitch + 3) / 4 * 4;
+        as = ws;
+        wsc = ws + (int64_t)a.M * pitch;
+        ws += n;
+    }
+    const Mx p{ac, as, a.w_codes, wsc, own ? a.x : nullptr, a.x_stride, a.M, a.N, a.K, pitch, a.y, a.y_stride,
                plan.pieces > 1 ? reinterpret_cast<float *>(ws) : nullptr, plan.pieces};
     if (holds) {
         if (a.M <= 16) return a.y_fp32 ? held_launch<1, float>(p, stream) : held_launch<1, uint16_t>(p, stream);

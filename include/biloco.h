@@ -501,7 +501,7 @@ biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, 
  *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
  *     not shared by calls that can run at the same time.
  * M >= 0 (0 does nothing), N >= 1.  The result does not depend on what else
- * runs: sums are taken in a fixed order.  One or two launches. */
+ * runs: sums are taken in a fixed order.  One to three launches. */
 biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const uint8_t *w_codes, const uint8_t *w_scales, int32_t M,
                                 int32_t N, int32_t K, void *y, int64_t y_stride, int32_t y_fp32,
@@ -509,7 +509,7 @@ biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
 
 /* The same for rows that are quantised first, as biloco_quant_mxfp4 does:
  * x [M][K] bf16, x_stride in elements, a multiple of 8, at least K.  The codes
- * stay in the workspace or on the chip.  One to three launches. */
+ * stay in the workspace or on the chip.  One to four launches. */
 biloco_status biloco_gemm_mxfp4_quant(const uint16_t *x, int64_t x_stride, const uint8_t *w_codes,
                                       const uint8_t *w_scales, int32_t M, int32_t N, int32_t K,
                                       void *y, int64_t y_stride, int32_t y_fp32, void *workspace,

@@ -240,3 +240,17 @@ def test_few_long_rows(M, K):
     x, a, w = _operands(K, M, 200, K)
     _compare(B.biloco_gemm_mxfp4(*a, *w, out_dtype=torch.float32), a, w)
     assert torch.equal(B.biloco_gemm_mxfp4(*a, *w), B.biloco_gemm_mxfp4_quant(x, *w))
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 40, 992), (64, 300, 5152), (130, 129, 1056), (200, 320, 13856), (300, 600, 3040),
+                                   (4100, 4100, 1120), (257, 100, 16352)])
+def test_rows_of_scales_at_any_address(M, N, K):
+    """K / 32 no multiple of 4 or of 32: the last of a row's blocks next to the following
+    row's, whose scales are NaN."""
+    x, a, w = _operands(K, M, N, K)
+    a[1][M // 2, 0] = 255
+    w[1][N // 2, 0] = 255
+    y = B.biloco_gemm_mxfp4(*a, *w, out_dtype=torch.float32)
+    _compare(y, a, w)
+    whole = torch.arange(M, device="cuda") != M // 2
+    assert not bool(y[whole][:, torch.arange(N, device="cuda") != N // 2].isnan().any())
