@@ -387,6 +387,7 @@ struct Tile {
     f32x16m_t acc[NT][MT];
     const uint8_t *a, *w, *sa, *sw;     // the tile's first rows
     int m, n, blocks, spitch;           // rows that are there, blocks a row, bytes from one row of scales to the next
+    uint32_t from, sfrom;               // byte offsets of a thread's first codes and scales
 
     // The wave's first row of A and of W.
     __device__ __forceinline__ static int m_of() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) % WM * (32 * MT); }
@@ -402,6 +403,8 @@ struct Tile {
         const uint32_t pitch = p.K / 2;
         blocks = p.K / 32;
         spitch = p.spitch;
+        from = threadIdx.x / 4 * 16 * blocks + 16 * mine();
+        sfrom = threadIdx.x / 8 * spitch + 4 * (threadIdx.x & 7);
         m = min(BM, p.M - m0);
         n = min(BN, p.N - n0);
         a = p.ac + (int64_t)m0 * pitch;
@@ -426,9 +429,8 @@ struct Tile {
         uint32_t from_a, from_w;
     };
     __device__ __forceinline__ Request request(Stage &lds, int t) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), tid = opaque(threadIdx.x);
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
         const int64_t at = 64 * (int64_t)t, pitch = 16 * (int64_t)blocks;
-        const uint32_t from = tid / 4 * 16 * blocks + 16 * mine();
         return Request{a + at, w + at, (int)max(m * pitch - at, (int64_t)0), (int)max(n * pitch - at, (int64_t)0), &lds.x[1024 * wave],
                        4 * t + mine() < blocks ? from : (uint32_t)kOob, from};
     }
@@ -441,11 +443,10 @@ struct Tile {
     // multiples of four bytes.  Past a row's end they are zeros (2^-127), in both, lest the
     // next row's NaN come in.
     __device__ __forceinline__ void load_scales(ScaleLds<BM, BN> &lds, int t, int i) const {
-        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)), tid = opaque(threadIdx.x);
+        const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
         const bool is_a = SROWS * i < BM;
-        const int row = SROWS * i - (is_a ? 0 : BM) + tid / 8, col = 4 * (tid & 7);
         const int64_t at = 32 * (int64_t)t, pitch = spitch;
-        bring4((is_a ? sa : sw) + at, (int)((is_a ? m : n) * pitch - at), 32 * t + col < blocks ? row * spitch + col : kOob,
+        bring4((is_a ? sa : sw) + at, (int)((is_a ? m : n) * pitch - at), 32 * t + 4 * (int)(threadIdx.x & 7) < blocks ? sfrom + (SROWS * i - (is_a ? 0 : BM)) * spitch : (uint32_t)kOob,
                &lds.x[4 * THREADS * i + 256 * wave]);
     }
     // Dwords of its stage q.
