@@ -12,6 +12,7 @@ using namespace biloco;
 namespace {
 
 constexpr int32_t kMostK = 1 << 20;
+constexpr int32_t kMostRows = 1 << 30;        // of a product's operands: their tiles' ends stay 32-bit numbers
 constexpr int32_t kMostLogits = 1 << 20;      // of weights up to 2^44, whose sums are to fit 64 bits
 
 biloco_status check_k(int32_t K) {
@@ -37,6 +38,7 @@ biloco_status gemm(const uint16_t *x, int64_t x_stride, const uint8_t *a_codes, 
     if (M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
     biloco_status st = check_k(K);
     if (st != BILOCO_OK) return st;
+    if (M > kMostRows || N > kMostRows) return BILOCO_ERR_UNSUPPORTED;
     if ((quant ? !x : !a_codes || !a_scales) || !w_codes || !w_scales || !y) return BILOCO_ERR_INVALID_VALUE;
     const void *ptrs[] = {x, a_codes, a_scales, w_codes, w_scales, y, workspace};
     for (const void *p : ptrs)
@@ -91,6 +93,7 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
     if (!bytes || M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
     const biloco_status st = check_k(K);
     if (st != BILOCO_OK) return st;
+    if (M > kMostRows || N > kMostRows) return BILOCO_ERR_UNSUPPORTED;
     *bytes = M == 0 ? 0 : mxfp4_ws_bytes(M, N, K);
     return BILOCO_OK;
 }

@@ -500,8 +500,8 @@ biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, 
  *   y [M][N] bf16, or fp32 if y_fp32 != 0; y_stride in elements, at least N
  *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
  *     not shared by calls that can run at the same time.
- * M >= 0 (0 does nothing), N >= 1.  The result does not depend on what else
- * runs: sums are taken in a fixed order.  One to three launches. */
+ * 0 <= M <= 2^30 (0 does nothing), 1 <= N <= 2^30.  The result does not depend
+ * on what else runs: sums are taken in a fixed order.  One to three launches. */
 biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const uint8_t *w_codes, const uint8_t *w_scales, int32_t M,
                                 int32_t N, int32_t K, void *y, int64_t y_stride, int32_t y_fp32,

@@ -69,7 +69,7 @@ def test_codes_over_scales():
     assert quant(M=3, s=2 * A + 512) == BAD
 
 
-GEMM = [(dict(M=-1), BAD), (dict(N=0), BAD), (dict(N=-4), BAD), (dict(K=0), BAD), (dict(K=40), BAD), (dict(K=1 << 21), UNS),
+GEMM = [(dict(M=-1), BAD), (dict(M=(1 << 30) + 1), UNS), (dict(N=(1 << 30) + 1, sy=(1 << 30) + 8), UNS), (dict(N=0), BAD), (dict(N=-4), BAD), (dict(K=0), BAD), (dict(K=40), BAD), (dict(K=1 << 21), UNS),
         (dict(wc=None), BAD), (dict(ws=None), BAD), (dict(y=None), BAD), (dict(wc=3 * A + 4), BAD), (dict(ws=4 * A + 2), BAD),
         (dict(y=5 * A + 2), BAD), (dict(w=6 * A + 8), BAD), (dict(sy=299), BAD), (dict(sy=1 << 31), UNS),
         (dict(M=40, K=8192, sx=8192, w=None), BAD), (dict(M=40, K=8192, sx=8192, wb=0), SMALL), (dict(M=2, y=3 * A + 64), BAD),
