@@ -343,10 +343,10 @@ mxfp4_held_kernel(const Mx p, int tiles) {
 // bytes are half a dword.  Scales come by 32 a row, for eight stages (a load of a dword a
 // row costs as many requests to L2 as two stages' codes: one a stage 249 us for the last size
 // below where four at a time took 205).
-// Bound by the matrix instructions and what holds them up: 4096 x 8192 x 8192 takes 177 us of
-// its own, 3.1 PFLOP/s, and 195 with the quantisation; the instruction alone on random
+// Bound by the matrix instructions and what holds them up: 4096 x 8192 x 8192 takes 171 to
+// 175 us of its own, 3.2 PFLOP/s, and 190 to 203 with the quantisation; the instruction alone on random
 // operands 90 us (6.1 PFLOP/s, from registers) or 103 (from LDS).  Two buffers of 256 k
-// instead 200 us with it; eight waves 194, but their registers spill.
+// instead 200 us with it where this one took 205; eight waves then 194, but their registers spill.
 constexpr int kStages = 4, kGroup = 8;      // stages in LDS; stages whose scales come together
 
 template <int BM, int BN>

@@ -960,13 +960,17 @@ sample_pick_kernel(const SampleArgs a, int S) {
 }
 
 // Slices a row where the rows alone leave CUs idle: at most kMostSlices, of at least
-// kLeastSlice logits each.
-constexpr int kCUs = 256, kLeastSlice = 4096;
+// kLeastSlice logits each, and only if a workgroup is spared kLeastSpared logits, which is
+// what the launches cost.  In slices against a workgroup a row (fp32, p 0.9): one row of 16000
+// 41.6 and 31.0 us, of 32000 44.6 and 45.9, of 50000 48.5 and 63.5, of 262144 89 and 247; 32
+// rows of 32000 47.9 and 46.7, of 100000 66.5 and 112; 64 of 50000 58.9 and 66.6; 128 of 64000
+// (two slices) 83.5 and 77.3, of 150000 147 and 157.
+constexpr int kCUs = 256, kLeastSlice = 4096, kLeastSpared = 32768;
 int slices_of(int rows, int V) {
     int s = kCUs / rows;
     if (s > kMostSlices) s = kMostSlices;
     if (s > V / kLeastSlice) s = V / kLeastSlice;
-    return s < 2 ? 1 : s;
+    return s < 2 || V - V / s < kLeastSpared ? 1 : s;
 }
 
 template <class T>

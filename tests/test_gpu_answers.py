@@ -144,10 +144,14 @@ def test_shared_steps_are_those_of_whole_tables():
     s.block.step(x, None, None, x.clone(), _ints([[PROMPT] * ANSWERS]), _ints(range(ANSWERS + 1)),
                  _ints([PROMPT + 1] * ANSWERS), whole, 1)
     assert all(torch.equal(a, b) for a, b in zip(cache, s.cache))
-    # both within their bound of the same value, |o| and sum w |v| at most the largest |v|
-    pages = torch.cat([whole[0], whole[1:, PROMPT // PAGE:].flatten()]).long()
-    k, v = (c[pages].view(torch.float8_e4m3fn).double().abs().amax((2, 3) if c.dim() == 4 else (2, 3, 4))
-            * torch.exp2(e[pages].double() - 127) for c, e in ((s.cache[0], s.cache[2]), (s.cache[1], s.cache[3])))
+    # both within their bound of the same value, |o| and sum w |v| at most the largest |v| of
+    # the tokens that are there: the prompt's pages, and the first token of each answer's own
+    kc, vc, ks, vs = s.cache
+    k = kc.view(torch.float8_e4m3fn).double().abs() * torch.exp2(ks.double() - 127)[..., None, None]
+    v = vc.view(torch.float8_e4m3fn).double().abs() * torch.exp2(vs.double() - 127)[..., None, None, None]
+    prompt, own = whole[0, :PROMPT // PAGE].long(), whole[:, PROMPT // PAGE].long()
+    k = torch.maximum(k[prompt].max(), k[own, :, 0].max())
+    v = torch.maximum(v[prompt].max(), v[own, :, 0, :, 0].max())
     terms = k.max() * s.block._q[:ANSWERS].double().abs().sum(2).max() * DIM ** -0.5
     e = 2 * (DIM + 8) * 2.0 ** -24 * terms + 2.0 ** -20
     assert bool(((s.block._o[:ANSWERS].double() - o.double()).abs() <= 2 * (2 * 2.0 ** -8 + e) * v.max()).all())
