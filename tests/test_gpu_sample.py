@@ -195,3 +195,26 @@ def test_captured(R, V):
         want = B.biloco_sample(x, u, top_p=p, logprob=other)
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(got_lp, other)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_slices_of_odd_rows(dtype):
+    """Rows cut over several workgroups: ties, rows and slices without weight, one logit in
+    the last slice, infinities, NaN."""
+    rng = np.random.default_rng(7)
+    R, V = 12, 60003
+    x = torch.from_numpy(rng.integers(0, 3, (R, V)).astype(np.float32))
+    x[1] = -float("inf")
+    x[2] = float("nan")
+    x[3] = -float("inf")
+    x[3, V - 1] = 1.0
+    x[4, [100, V - 2]] = float("inf")
+    x[5, ::2] = float("nan")
+    x[6, : V // 2] = -float("inf")
+    x[7, 10:] = -200.0
+    u = rng.random(R, np.float32)
+    x = x.to(dtype)
+    check(x, u)
+    check(x, u, k=[1, 5, 5, 5, 1, 1025, 4000, 3, 20000, 20500, 59999, 60003])
+    check(x, u, p=np.linspace(0.05, 0.97, R))
+    check(x, u, t=[0.0, 1.0, 0.5, 0.0, 0.7, 2.0, 0.0, 1.0, 0.3, 1.5, 3.0, 0.0], p=[0.8] * R, m=[0.2] * R)
