@@ -290,7 +290,7 @@ struct TileWork {
     Seq s;              // the sequence, where it is one
 };
 
-// The kernel of both calls: K::begin gives a workgroup its rows and its work (false:
+// What the kernels of both calls do: K::begin gives a workgroup its rows and its work (false:
 // there is none), K::end takes what the rows have gathered.  In one function, since the
 // walk over chunks as a function of its own costs the compiler 32 registers' moves a
 // turn (chunks of 64 channels 356 -> 380 us).

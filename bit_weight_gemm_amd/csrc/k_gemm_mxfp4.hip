@@ -164,13 +164,13 @@ mxfp4_rows_kernel(const Mx p) {
 // of which each wave takes an equal run; a tile belongs to the wave that begins it, and those
 // that go on with it leave their sums in LDS.
 // Step s of a chunk multiplies blocks 4 s + g in lanes l >> 4 == g, so that a load brings 64
-// bytes in a row of each of 16 rows (16 bytes out of 64, four times: 122 us below, since what
-// the first load brings is gone from L1 before the last).
+// bytes in a row of each of 16 rows (16 bytes out of 64, four times and non-temporal: 122 us
+// for the logits below, with plain loads 95, since L1 does not hold the lines that long).
 // Blocks of a row of A lie an odd number of 16-byte slots apart from row to row, so that
 // sixteen rows' reads of one block meet all banks.
 // Bound by reading W, of which as many bytes are under way as the registers hold: 32 rows to
 // 100001 columns of 5120 take 75 us, 3.7 TB/s (a plain read of W 51, 5.5 TB/s; the kernel
-// below for other sizes 110), one row to 13824 of 5120 10.0 us (11.0).  12 waves with four
+// above 110), one row to 13824 of 5120 10.0 us (11.0).  12 waves with four
 // chunks under way 75.6 and 10.6, eight with six 83 and 10.3; rows quantised by a launch of
 // their own 78.5 and 11.9.
 constexpr int kAhead = 2, kHeldWaves = 16, kHeldThreads = 64 * kHeldWaves;
