@@ -105,7 +105,15 @@ struct Loader {
     }
 };
 
-template <int D>
+// Weights go into the product with v rounded to bf16 (2^-8 of each at most), or as two
+// bf16 terms, the second one what that rounding left (together within 2^-16), as in the
+// kernel for few rows; their sum is taken before that.  The second term brings o's error
+// to that of its own rounding (from 1.3 to 1.4 times that, root mean square) and takes half
+// as many matrix instructions again: on sequences of many rows 259 us for 210 on a prompt of
+// 4096 tokens, 441 for 348 on chunks of 64 channels, so these have one term.  Shared tokens
+// have two, so that a row's result is as exact as without sharing: four answers behind 608
+// tokens 19.2 us for 18.1, 64 behind 16384 84 for 77.
+template <int D, int TERMS>
 struct Rows32 {
     u32x4_t q[D / 16];
     f32x16a_t o[D / 32];
@@ -171,13 +179,15 @@ struct Rows32 {
             for (int n = 0; n < D / 32; ++n) o[n] *= alpha;
         }
     }
-    // Scores to weights, rounded to bf16 for the product (2^-8 of each at
-    // most); their sum is taken before that.  What the rounding leaves as a second
-    // term, as in the kernel for few rows, brings o's error to that of its own rounding
-    // (from 1.3 to 1.4 times that, root mean square) and takes half as many matrix
-    // instructions again, which that kernel has time for and this one has not: 259 us
-    // for 210 on a prompt of 4096 tokens, 441 for 348 on chunks of 64 channels.
-    __device__ __forceinline__ void weigh(f32x16a_t &sc, float c2, u32x4_t (&pt)[2]) {
+    // Two weights as pair i of terms.
+    __device__ __forceinline__ static void pack(u32x4_t (&pt)[TERMS][2], int i, float w0, float w1) {
+        const uint32_t w = narrow2a(w0, w1);
+        pt[0][i >> 2][i & 3] = w;
+        if constexpr (TERMS == 2)
+            pt[1][i >> 2][i & 3] = narrow2a(w0 - __uint_as_float(w << 16), w1 - __uint_as_float(w & 0xFFFF0000u));
+    }
+    // Scores to weights.
+    __device__ __forceinline__ void weigh(f32x16a_t &sc, float c2, u32x4_t (&pt)[TERMS][2]) {
         const float base = m == -__builtin_inff() ? 0.0f : m;      // a row that sees nothing yet
         float sum = 0.0f;
 #pragma unroll
@@ -187,19 +197,20 @@ struct Rows32 {
         }
         l += sum;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-            pt[c] = u32x4_t{narrow2a(sc[8 * c], sc[8 * c + 1]), narrow2a(sc[8 * c + 2], sc[8 * c + 3]),
-                            narrow2a(sc[8 * c + 4], sc[8 * c + 5]), narrow2a(sc[8 * c + 6], sc[8 * c + 7])};
+        for (int i = 0; i < 8; ++i) pack(pt, i, sc[2 * i], sc[2 * i + 1]);
     }
 
-    __device__ __forceinline__ void gather(const TileLds<D> &lds, int buf, int t, const u32x4_t (&pt)[2]) {
+    __device__ __forceinline__ void gather(const TileLds<D> &lds, int buf, int t, const u32x4_t (&pt)[TERMS][2]) {
         const int lane = threadIdx.x & 63;
         const uint16_t *v = &lds.v[buf][8 * ((4 * t + (lane >> 5)) * D + (lane & 31))];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int n = 0; n < D / 32; ++n)
-                o[n] = mfma32(*reinterpret_cast<const u32x4_t *>(v + 16 * c * D + 256 * n), pt[c], o[n]);
+            for (int n = 0; n < D / 32; ++n) {
+                const u32x4_t w = *reinterpret_cast<const u32x4_t *>(v + 16 * c * D + 256 * n);
+#pragma unroll
+                for (int e = 0; e < TERMS; ++e) o[n] = mfma32(w, pt[e][c], o[n]);
+            }
     }
 
     // One tile on, in the order in which it is to be issued: between two matrix
@@ -222,7 +233,7 @@ struct Rows32 {
         };
         const float base = m == -__builtin_inff() ? 0.0f : m;
         float sum = 0.0f;
-        u32x4_t pt[2], f[M];
+        u32x4_t pt[TERMS][2], f[M];
         f[0] = key(0);
         f[1] = key(1);
         next = zero16();
@@ -234,7 +245,7 @@ struct Rows32 {
             for (int j = E * i; j < E * i + E; ++j) {
                 s[j] = exp2a(__builtin_fmaf(s[j], c2, -base));
                 sum += s[j];
-                if (j & 1) pt[j >> 3][(j >> 1) & 3] = narrow2a(s[j - 1], s[j]);
+                if (j & 1) pack(pt, j >> 1, s[j - 1], s[j]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -245,7 +256,8 @@ struct Rows32 {
 #pragma unroll
         for (int i = 0; i < M; ++i) {
             if (i + 2 < M) f[i + 2] = value(i + 2);
-            o[i % (D / 32)] = mfma32(f[i], pt[i / (D / 32)], o[i % (D / 32)]);
+#pragma unroll
+            for (int e = 0; e < TERMS; ++e) o[i % (D / 32)] = mfma32(f[i], pt[e][i / (D / 32)], o[i % (D / 32)]);
             if constexpr (ADVANCE) ld.store_part(lds, buf ^ 1, i);
 #pragma unroll
             for (int j = E * i; j < E * i + E; ++j) mx = fmaxf(mx, next[j]);
@@ -296,7 +308,7 @@ struct TileWork {
 // turn (chunks of 64 channels 356 -> 380 us).
 template <int D, class K>
 __device__ __forceinline__ void tile_rows(const K &k, int splits, TileLds<D> &lds, typename K::Lds &more) {
-    Rows32<D> w;
+    Rows32<D, K::kTerms> w;
     TileWork<typename K::Args> t{k.args()};
     if (!k.begin(w, t, more, splits)) return;
     const auto &a = t.a;
@@ -340,7 +352,7 @@ __device__ __forceinline__ void tile_rows(const K &k, int splits, TileLds<D> &ld
                 ++c;
             }
             const int buf = (c - c0) & 1, j0 = span.start(c);
-            u32x4_t pt[2];
+            u32x4_t pt[K::kTerms][2];
             __syncthreads();
             if (c + 1 < c1) {
                 ld.store(a, lds, buf ^ 1, span.start(c + 1), p_min, p_max);
@@ -375,8 +387,8 @@ attn_tiles_kernel(const K k, int splits) {
 }
 
 // A row's sums as a piece of them: [kTileRows][D], then maxima and sums of the weights.
-template <int D>
-__device__ __forceinline__ void leave(const Rows32<D> &w, float l, float *part, int row) {
+template <int D, int TERMS>
+__device__ __forceinline__ void leave(const Rows32<D, TERMS> &w, float l, float *part, int row) {
     const int half = (threadIdx.x & 63) >> 5;
     float *dst = part + row * D + 4 * half;
 #pragma unroll

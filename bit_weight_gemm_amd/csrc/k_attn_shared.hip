@@ -128,6 +128,7 @@ __device__ __forceinline__ float *shared_part(const SharedAttnArgs &s, int64_t i
 // A workgroup takes 128 rows of a group, whose tokens and positions it first lists.
 struct SharedTiles {
     using Args = PartArgs;
+    static constexpr int kTerms = 2;
     struct Lds {
         int token[kTileRows], pos[kTileRows];
     };
@@ -142,7 +143,7 @@ struct SharedTiles {
         return uniform(v);
     }
     template <int D>
-    __device__ __forceinline__ bool begin(Rows32<D> &w, TileWork<PartArgs> &t, Lds &lds, int splits) const {
+    __device__ __forceinline__ bool begin(Rows32<D, kTerms> &w, TileWork<PartArgs> &t, Lds &lds, int splits) const {
         const Tables tab = tables_of(s, a.B);
         t.h = (int)(blockIdx.x % a.kv_heads);
         const int rest = (int)(blockIdx.x / a.kv_heads);
@@ -188,7 +189,7 @@ struct SharedTiles {
         return true;
     }
     template <int D>
-    __device__ __forceinline__ void end(const Rows32<D> &w, const TileWork<PartArgs> &t, float l, int splits) const {
+    __device__ __forceinline__ void end(const Rows32<D, kTerms> &w, const TileWork<PartArgs> &t, float l, int splits) const {
         const int row = 32 * (int)(threadIdx.x >> 6) + (int)(threadIdx.x & 31);
         if (row < t.rows) leave(w, l, shared_part<D>(s, (int64_t)t.at * a.kv_heads + t.h, splits, t.split), row);
     }

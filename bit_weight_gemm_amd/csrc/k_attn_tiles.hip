@@ -45,13 +45,14 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs &a, const Seq &s) {
 // one XCD's L2 where the number of heads is a multiple of 8.
 struct PagedTiles {
     using Args = AttnArgs;
+    static constexpr int kTerms = 1;
     struct Lds {};
     AttnArgs a;
     int which, tiles;
 
     __device__ __forceinline__ const AttnArgs &args() const { return a; }
     template <int D>
-    __device__ __forceinline__ bool begin(Rows32<D> &w, TileWork<AttnArgs> &t, Lds &, int splits) const {
+    __device__ __forceinline__ bool begin(Rows32<D, kTerms> &w, TileWork<AttnArgs> &t, Lds &, int splits) const {
         t.h = (int)(blockIdx.x % a.kv_heads);
         const int rest = (int)(blockIdx.x / a.kv_heads);
         t.split = rest % splits;
@@ -75,7 +76,7 @@ struct PagedTiles {
         return true;
     }
     template <int D>
-    __device__ __forceinline__ void end(const Rows32<D> &w, const TileWork<AttnArgs> &t, float l, int splits) const {
+    __device__ __forceinline__ void end(const Rows32<D, kTerms> &w, const TileWork<AttnArgs> &t, float l, int splits) const {
         const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), G = a.q_heads / a.kv_heads;
         const int row = t.r0 + 32 * wave + (lane & 31), half = lane >> 5;
         if (row >= t.rows) return;

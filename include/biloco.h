@@ -531,8 +531,8 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
  * biloco_attn_paged on sequences whose tables name the same pages first.
  * shared_len may end inside a page, and may pass a sequence's kv_len (its rows then
  * see the shared tokens up to their position).
- * For the product with v a weight of a shared token is rounded to bf16 (2^-8);
- * others as there.  A sequence of more than 64 rows (new tokens times q_heads /
+ * For the product with v a weight of a shared token is the sum of two bf16, as are
+ * those of own tokens.  A sequence of more than 64 rows (new tokens times q_heads /
  * kv_heads) fills the matrix cores by itself: its tokens are read through its own
  * table, which has to name the shared pages too.
  * max_shared_len bounds shared_len on the host; it shapes the launch.

@@ -1,0 +1,71 @@
+"""biloco_attn_shared where test_gpu_attn_shared.py does not look: how exact the weights
+of shared tokens are.
+
+Tolerance.  With e, t and the output's rounding as there, a weight is within 2^-16 of
+itself (two bf16 terms, each rounded to 8 significant bits: 2^-8 of 2^-8).  Over n tokens
+the products take n / 16 steps of two terms (each at most one truncation to 24 bits, 2^-23:
+n / 4 times 2^-24), a lane's sum of weights n / 2 roundings of 2^-24, the joins under 64:
+  |o - o64| <= E sum w |v| + 2^-8 (|o64| + E sum w |v|),  E = 2^-16 + e + (3 n / 4 + 64) 2^-24.
+Values are chosen so that o64 nearly cancels: there the output's rounding is small
+against sum w |v| and E is what is seen.  One term alone, put into the plain form,
+has to exceed the bound.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer
+from test_gpu_attn_shared import Case
+
+pytestmark = pytest.mark.gpu
+
+
+def _cancel(c, seed):
+    """Gives each channel of a group and key/value head two shared tokens whose weighted
+    values nearly cancel in one of the group's rows; the others, own ones too, are zero."""
+    rng = np.random.default_rng(seed)
+    kval, _ = layer.cache_values(c.cache)
+    q, G = c.q.double().numpy(), c.hq // c.hk
+    c.cache[1][:] = 0
+    c.cache[3][:] = 120
+    for g0, g1, n in zip(c.group_start[:-1], c.group_start[1:], c.shared):
+        for h in range(c.hk):
+            for d in range(c.dim):
+                b, g = rng.integers(g0, g1), rng.integers(G)
+                i = rng.integers(c.new[b])
+                at = c.seen[b, :min(n, c.kv_len[b] - c.new[b] + i + 1)]
+                s = kval[at // c.page, h, at % c.page] @ q[c.q_start[b] + i, h * G + g] * c.scale
+                first = rng.choice(np.argsort(-s)[:max(2, len(s) // 2)])
+                other = np.argsort(np.abs(s - s[first]))[1]
+                v = rng.uniform(60, 120)
+                for j, x in ((first, v), (other, -v * np.exp(s[first] - s[other]))):
+                    c.cache[1][at[j] // c.page, h, at[j] % c.page // 8, d, at[j] % 8] = layer.e4m3_encode(np.clip(x, -448, 448))
+
+
+def _one_term(c):
+    """The plain form with weights of a single bf16 term."""
+    exp = np.exp
+    try:
+        np.exp = lambda x: torch.from_numpy(exp(x)).to(torch.bfloat16).double().numpy()
+        return c.want(0, 0)[0]
+    finally:
+        np.exp = exp
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("groups,hq,hk", [
+    ([(200, [(1, 201), (1, 230), (2, 300)])], 2, 2),
+    ([(513, [(1, 514 + i) for i in range(40)])], 8, 1),      # more rows than a tile's
+    ([(640, [(1, 700), (3, 650)]), (64, [(1, 65)] * 3), (130, [(5, 140), (1, 131)])], 16, 2),
+    ([(1500, [(1, 1501), (4, 1600)])], 4, 2)])      # in pieces
+def test_weights_of_shared_tokens(dim, groups, hq, hk):
+    c = Case(groups, hq, hk, dim, 32, seed=dim + hq)
+    _cancel(c, seed=3)
+    want, _, size, terms = c.want(0, 0)
+    e = 2 * (dim + 8) * 2.0 ** -24 * terms[..., None] + 2.0 ** -20 + 2.0 ** -16
+    e = e + (3 * int(c.kv_len.max()) / 4 + 64) * 2.0 ** -24
+    bound = e * size + 2.0 ** -8 * (np.abs(want) + e * size)
+    assert (np.abs(_one_term(c) - want) > 2 * bound).any()
+    o, _ = c.run()
+    over = np.abs(o.double().cpu().numpy() - want) - bound
+    assert over.max() <= 0, over.max()
