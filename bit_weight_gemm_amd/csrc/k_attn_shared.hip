@@ -23,7 +23,7 @@ constexpr int kWantItems = 512;      // workgroups that fill the chip (two a CU)
 
 // Where the sequences' rows lie in the groups' tiles; made by one workgroup first.
 struct Tables {
-    int *before;      // [B + 1] new tokens of the sequences before (of few rows)
+    int *before;      // [B + 1] new tokens of the sequences before (of few rows), T at most
     int *tile;        // [groups + 1] tiles of the groups before
     int *from;        // [B] the first own token
     int *row;         // [B] the first row among the tiles' rows, or -1: nothing is shared
@@ -52,19 +52,20 @@ __device__ __forceinline__ Group group_at(const AttnArgs &a, const SharedAttnArg
 }
 
 constexpr int kTableThreads = 1024;
-// Exclusive sums over the workgroup; all: the sum.
-__device__ __forceinline__ int sums_before(int v, int (&tmp)[kTableThreads / 64], int &all) {
+// Exclusive sums over the workgroup; all: the sum.  In 64 bits: lists that are not in order
+// can claim every row for each second sequence.
+__device__ __forceinline__ int64_t sums_before(int v, int64_t (&tmp)[kTableThreads / 64], int64_t &all) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int in = v;
+    int64_t in = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int t = __shfl_up(in, o, 64);
+        const int64_t t = __shfl_up((long long)in, o, 64);
         if (lane >= o) in += t;
     }
     __syncthreads();
     if (lane == 63) tmp[wave] = in;
     __syncthreads();
-    int b = in - v;
+    int64_t b = in - v;
     all = 0;
     for (int i = 0; i < kTableThreads / 64; ++i) {
         if (i < wave) b += tmp[i];
@@ -75,17 +76,17 @@ __device__ __forceinline__ int sums_before(int v, int (&tmp)[kTableThreads / 64]
 
 __global__ void __launch_bounds__(kTableThreads)
 attn_shared_tables_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int tiles) {
-    __shared__ int tmp[kTableThreads / 64];
+    __shared__ int64_t tmp[kTableThreads / 64];
     const Tables t = tables_of(s, a.B);
     const int G = a.q_heads / a.kv_heads;
-    int carry = 0, all;
+    int64_t carry = 0, all;
     for (int at = 0; at < a.B; at += kTableThreads) {
         const int b = at + threadIdx.x, n = b < a.B ? seq_of(a, b, which).n : 0;
-        const int mine = carry + sums_before(n, tmp, all);
-        if (b < a.B) t.before[b] = mine;
+        const int64_t mine = carry + sums_before(n, tmp, all);
+        if (b < a.B) t.before[b] = (int)min(mine, (int64_t)a.T);
         carry += all;
     }
-    if (threadIdx.x == 0) t.before[a.B] = carry;
+    if (threadIdx.x == 0) t.before[a.B] = (int)min(carry, (int64_t)a.T);
     __threadfence_block();
     __syncthreads();
     carry = 0;
@@ -97,11 +98,11 @@ attn_shared_tables_kernel(const AttnArgs a, const SharedAttnArgs s, int which, i
             const int64_t rows = (int64_t)(t.before[x.b1] - t.before[x.b0]) * G;
             n = x.upto > 0 ? (int)min((rows + kTileRows - 1) / kTileRows, (int64_t)tiles) : 0;
         }
-        const int mine = min(carry + sums_before(n, tmp, all), tiles);
-        if (g < s.groups) t.tile[g] = mine;
-        carry = min(carry + all, tiles);
+        const int64_t mine = carry + sums_before(n, tmp, all);
+        if (g < s.groups) t.tile[g] = (int)min(mine, (int64_t)tiles);
+        carry += all;
     }
-    if (threadIdx.x == 0) t.tile[s.groups] = carry;
+    if (threadIdx.x == 0) t.tile[s.groups] = (int)min(carry, (int64_t)tiles);
     __threadfence_block();
     __syncthreads();
     for (int b = threadIdx.x; b < a.B; b += kTableThreads) {
@@ -162,8 +163,9 @@ struct SharedTiles {
         t.rows = min((scalar_load(tab.before + x.b1) - first) * G - r0, kTileRows);
         for (int b = x.b0 + threadIdx.x; b < x.b1; b += 256) {
             const Seq q = seq_of(a, b, which);
-            const int at0 = (tab.before[b] - first) * G - r0;      // row of its first row in the tile
-            for (int r = max(at0, 0); r < min(at0 + q.n * G, kTileRows); ++r) {
+            // rows of its first row and behind its last one in the tile
+            const int at0 = (tab.before[b] - first) * G - r0, at1 = (tab.before[b + 1] - first) * G - r0;
+            for (int r = max(at0, 0); r < min(at1, kTileRows); ++r) {
                 const int i = (r - at0) / G;
                 lds.token[r] = q.first + i;
                 lds.pos[r] = q.past + i;

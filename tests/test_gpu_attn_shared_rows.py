@@ -1,7 +1,7 @@
 """biloco_attn_shared where test_gpu_attn_shared.py does not look: how exact the weights
-of shared tokens are.
+of shared tokens are, and batches of many sequences, lists out of order among them.
 
-Tolerance.  With e, t and the output's rounding as there, a weight is within 2^-16 of
+Tolerance of the weights.  With e, t and the output's rounding as there, a weight is within 2^-16 of
 itself (two bf16 terms, each rounded to 8 significant bits: 2^-8 of 2^-8).  Over n tokens
 the products take n / 16 steps of two terms (each at most one truncation to 24 bits, 2^-23:
 n / 4 times 2^-24), a lane's sum of weights n / 2 roundings of 2^-24, the joins under 64:
@@ -14,6 +14,7 @@ import numpy as np
 import pytest
 import torch
 
+from bit_weight_gemm_amd import binding as B
 from oracle import layer
 from test_gpu_attn_shared import Case
 
@@ -69,3 +70,31 @@ def test_weights_of_shared_tokens(dim, groups, hq, hk):
     o, _ = c.run()
     over = np.abs(o.double().cpu().numpy() - want) - bound
     assert over.max() <= 0, over.max()
+
+
+def test_lists_out_of_order_that_claim_more_rows_than_32_bits_count():
+    """Every second sequence claims all T rows: unspecified values, no access outside the
+    arrays, in 2^31 rows of heads and more; a batch that is in order is right again after it."""
+    n, T, G, dim = 4096, 17000, 64, 64
+    assert np.int64(n // 2 * T * G).astype(np.int32) < 0
+    cache = B.biloco_kv_cache(40, 1, 32, dim)
+    for t in cache:
+        t.fill_(0x38)
+    q = torch.randn((T, G, dim), device="cuda").to(torch.bfloat16)
+    table = (torch.arange(n * 8, device="cuda", dtype=torch.int32) % 40).reshape(n, 8)
+
+    def ints(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+    kv_len, out = torch.full((n,), 200, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    for start in ([0, T] * (n // 2) + [0], [T, 0] * (n // 2) + [T]):
+        for groups, lens in ((ints(0, n), ints(128)), (ints(0, n // 3, n), ints(64, 150))):
+            B.biloco_attn_shared(cache, q, ints(*start), kv_len, table, groups, lens, 1, 200, 150, 0.125, out=out)
+            torch.cuda.synchronize()
+    Case([(100, [(1, 140), (1, 101)]), (64, [(1, 70)])], 8, 2, dim, 32, seed=1).check()
+
+
+def test_more_sequences_and_groups_than_the_table_takes_at_a_time():
+    rng = np.random.default_rng(0)
+    Case([(int(rng.integers(0, 40)), [(1, int(rng.integers(1, 60)))] * int(rng.integers(0, 4))) for _ in range(1300)], 2, 1, 64, 16,
+         seed=5).check()
+    Case([(70, [(int(rng.integers(0, 3)), 80) for _ in range(2100)]), (20, [(1, 30)] * 50)], 2, 1, 64, 16, seed=6).check()
