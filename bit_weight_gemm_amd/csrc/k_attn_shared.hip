@@ -275,8 +275,10 @@ struct SharedPlan {
     size_t bytes, most_bytes;      // for this call; for it and every smaller one
 };
 
+// A multiple of 16: the shared parts behind them are written 16 bytes at a time.
 size_t own_bytes(int64_t items, int dim, int rows) {
-    return begun_slots(items) * sizeof(Begun) + (size_t)((items + kPieces) * part_floats(dim, rows)) * sizeof(float);
+    const size_t n = begun_slots(items) * sizeof(Begun) + (size_t)((items + kPieces) * part_floats(dim, rows)) * sizeof(float);
+    return (n + 15) / 16 * 16;
 }
 
 // Sequences of many rows, if the host cannot exclude them, are taken first, in the same

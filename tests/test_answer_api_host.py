@@ -277,3 +277,11 @@ def test_calls_of_no_rows():
     assert B.biloco_gemm_mxfp4(u8(0, K // 2), u8(0, K // 32), u8(N, K // 2), u8(N, K // 32)).shape == (0, N)
     assert B.biloco_gemm_mxfp4_quant(bf16(0, K), u8(N, K // 2), u8(N, K // 32)).shape == (0, N)
     assert B.biloco_sample(f32(0, V), f32(0)).shape == (0,)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_shared_workspace_is_made_of_aligned_arrays(dim):
+    """Odd numbers of items and rows: every array in it begins at a multiple of 16 bytes,
+    and all are multiples of 16 long."""
+    for b, hq, hk, q in ((1, 1, 1, 1), (3, 5, 1, 1), (3, 5, 1, 3), (5, 9, 3, 1), (7, 21, 7, 5), (1, 63, 1, 1), (2, 5, 1, 1)):
+        assert B.biloco_attn_shared_workspace_bytes(b, b * q, hq, hk, dim, q, 500, 1, 300) % 16 == 0, (b, hq, hk, q)

@@ -1,5 +1,6 @@
 """biloco_attn_shared where test_gpu_attn_shared.py does not look: how exact the weights
-of shared tokens are, and batches of many sequences, lists out of order among them.
+of shared tokens are, batches of many sequences, lists out of order among them, and odd numbers of heads
+and rows.
 
 Tolerance of the weights.  With e, t and the output's rounding as there, a weight is within 2^-16 of
 itself (two bf16 terms, each rounded to 8 significant bits: 2^-8 of 2^-8).  Over n tokens
@@ -98,3 +99,10 @@ def test_more_sequences_and_groups_than_the_table_takes_at_a_time():
     Case([(int(rng.integers(0, 40)), [(1, int(rng.integers(1, 60)))] * int(rng.integers(0, 4))) for _ in range(1300)], 2, 1, 64, 16,
          seed=5).check()
     Case([(70, [(int(rng.integers(0, 3)), 80) for _ in range(2100)]), (20, [(1, 30)] * 50)], 2, 1, 64, 16, seed=6).check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,hk,groups", [(1, 1, [(200, [(1, 201)])]), (5, 1, [(130, [(1, 140), (1, 131), (1, 300)])]),
+                                          (9, 3, [(700, [(1, 701)] * 4 + [(3, 720)])]), (63, 1, [(90, [(1, 91)])])])
+def test_odd_numbers_of_heads_and_rows(dim, hq, hk, groups):
+    Case(groups, hq, hk, dim, 32, seed=hq).check()
