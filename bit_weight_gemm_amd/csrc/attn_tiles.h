@@ -33,6 +33,12 @@ struct TileLds {
     int odd[2][kWaves];
 };
 
+// Bit j: some row of the tile sees token t0 + j.  Rows of one sequence follow one another,
+// so what they see has no gaps.
+__device__ __forceinline__ uint32_t tile_sees8(const AttnArgs &a, int p_min, int p_max, int t0) {
+    return any_sees8(a, p_min, p_max, t0);
+}
+
 // A chunk's way into LDS.  A thread moves 16 bytes N times: of K's token
 // tid / (D / 16) + 32 i, and of V's token group tid / (D / 2) + 4 i.  The
 // tokens of a wave lie within 16 aligned ones, so its pages are uniform.
@@ -86,7 +92,7 @@ struct Loader {
             uint32_t any = 0;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const uint32_t bits = any_sees8(a, p_min, p_max, j0 + 8 * (tid / (D / 2) + 4 * i));
+                const uint32_t bits = tile_sees8(a, p_min, p_max, j0 + 8 * (tid / (D / 2) + 4 * i));
                 const uint32_t m0 = spread4(bits), m1 = spread4(bits >> 4);
                 v[i] &= u32x4_t{m0, m1, m0, m1};
                 if (bits == 0) vscale[i] = 127;
@@ -387,8 +393,9 @@ attn_tiles_kernel(const K k, int splits) {
 }
 
 // A row's sums as a piece of them: [kTileRows][D], then maxima and sums of the weights.
+// blind: nothing in their place.
 template <int D, int TERMS>
-__device__ __forceinline__ void leave(const Rows32<D, TERMS> &w, float l, float *part, int row) {
+__device__ __forceinline__ void leave(const Rows32<D, TERMS> &w, float l, float *part, int row, bool blind = false) {
     const int half = (threadIdx.x & 63) >> 5;
     float *dst = part + row * D + 4 * half;
 #pragma unroll
@@ -396,10 +403,10 @@ __device__ __forceinline__ void leave(const Rows32<D, TERMS> &w, float l, float 
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<f32x4a_t *>(dst + 32 * n + 8 * j) =
-                f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
+                blind ? f32x4a_t{0, 0, 0, 0} : f32x4a_t{w.o[n][4 * j], w.o[n][4 * j + 1], w.o[n][4 * j + 2], w.o[n][4 * j + 3]};
     if (half == 0) {
-        part[kTileRows * D + 2 * row] = w.m;
-        part[kTileRows * D + 2 * row + 1] = l;
+        part[kTileRows * D + 2 * row] = blind ? -__builtin_inff() : w.m;
+        part[kTileRows * D + 2 * row + 1] = blind ? 0.0f : l;
     }
 }
 

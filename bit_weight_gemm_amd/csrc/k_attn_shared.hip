@@ -126,9 +126,27 @@ __device__ __forceinline__ float *shared_part(const SharedAttnArgs &s, int64_t i
     return static_cast<float *>(s.parts) + (item * splits + split) * kTileRows * (D + 2);
 }
 
-// A workgroup takes 128 rows of a group, whose tokens and positions it first lists.
+// A tile's rows are of several sequences: where their positions lie further apart than a
+// window, there are tokens between them that none of them sees (`gaps`).
+struct SharedArgs : PartArgs {
+    const int *pos;      // of the tile's rows
+    int rows;
+    bool gaps, blind;    // blind: the lane's row sees none of the shared tokens
+    __device__ __forceinline__ explicit SharedArgs(const AttnArgs &a) : PartArgs(a, 0, 0), pos(nullptr), rows(0), gaps(false), blind(false) {}
+};
+__device__ __forceinline__ uint32_t tile_sees8(const SharedArgs &a, int p_min, int p_max, int t0) {
+    const uint32_t bits = any_sees8(a, p_min, p_max, t0);
+    if (!a.gaps || bits == 0) return bits;
+    uint32_t some = 0;
+    for (int r = 0; r < a.rows; ++r) some |= sees8(a, a.pos[r], t0);
+    return some;
+}
+
+// A workgroup takes 128 rows of a group, whose tokens and positions it first lists.  Rows
+// that see none of the shared tokens (idle slots, windows that begin behind them) go along
+// at another row's position, so that they do not mask the others' chunks, and leave nothing.
 struct SharedTiles {
-    using Args = PartArgs;
+    using Args = SharedArgs;
     static constexpr int kTerms = 2;
     struct Lds {
         int token[kTileRows], pos[kTileRows];
@@ -137,14 +155,17 @@ struct SharedTiles {
     SharedAttnArgs s;
     int which;
 
-    __device__ __forceinline__ PartArgs args() const { return PartArgs(a, 0, 0); }
+    __device__ __forceinline__ SharedArgs args() const { return SharedArgs(a); }
+    __device__ __forceinline__ bool sees_any(int pos, int upto) const {
+        return pos >= 0 && (low_of(a, pos) < upto || a.sinks > 0);
+    }
     __device__ __forceinline__ static int lowest(int v) {
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) v = min(v, __shfl_xor(v, o, 64));
         return uniform(v);
     }
     template <int D>
-    __device__ __forceinline__ bool begin(Rows32<D, kTerms> &w, TileWork<PartArgs> &t, Lds &lds, int splits) const {
+    __device__ __forceinline__ bool begin(Rows32<D, kTerms> &w, TileWork<SharedArgs> &t, Lds &lds, int splits) const {
         const Tables tab = tables_of(s, a.B);
         t.h = (int)(blockIdx.x % a.kv_heads);
         const int rest = (int)(blockIdx.x / a.kv_heads);
@@ -174,26 +195,31 @@ struct SharedTiles {
         __syncthreads();
         const int wave = uniform((int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
         const int p0 = lds.pos[min(lane, t.rows - 1)], p1 = lds.pos[min(lane + 64, t.rows - 1)];
-        t.p_min = lowest(min(p0, p1));
-        t.p_max = -lowest(min(-p0, -p1));
+        const bool s0 = sees_any(p0, x.upto), s1 = sees_any(p1, x.upto);
+        t.p_min = lowest(min(s0 ? p0 : 0x7FFFFFFF, s1 ? p1 : 0x7FFFFFFF));
+        t.p_max = -lowest(min(s0 ? -p0 : 1, s1 ? -p1 : 1));      // -1: none sees any
         const int row = min(32 * wave + (lane & 31), t.rows - 1), gi = (r0 + row) % G;
-        w.p = lds.pos[row];
+        t.a.blind = !sees_any(lds.pos[row], x.upto);
+        w.p = t.a.blind ? t.p_max : lds.pos[row];
         w.p_min = lowest(w.p);
         w.p_max = -lowest(-w.p);
         w.start(a.q + (int64_t)lds.token[row] * a.q_stride + (int64_t)(t.h * G + gi) * D + 8 * (lane >> 5));
         t.a.upto = x.upto;
+        t.a.pos = lds.pos;
+        t.a.rows = t.rows;
+        t.a.gaps = a.window > 0 && t.p_min < x.upto - 1 && t.p_max - a.window > t.p_min;
         t.last = x.upto - 1;
         t.table = a.table + (int64_t)x.b0 * a.max_pages;
-        t.span = span_of(t.a, t.p_min, t.p_max);
+        t.span = t.p_max < 0 ? Span64{0, 0, 0} : span_of(t.a, t.p_min, t.p_max);
         const int each = (t.span.nc + splits - 1) / splits;
         t.c0 = min(t.split * each, t.span.nc);
         t.c1 = min(t.c0 + each, t.span.nc);
         return true;
     }
     template <int D>
-    __device__ __forceinline__ void end(const Rows32<D, kTerms> &w, const TileWork<PartArgs> &t, float l, int splits) const {
+    __device__ __forceinline__ void end(const Rows32<D, kTerms> &w, const TileWork<SharedArgs> &t, float l, int splits) const {
         const int row = 32 * (int)(threadIdx.x >> 6) + (int)(threadIdx.x & 31);
-        if (row < t.rows) leave(w, l, shared_part<D>(s, (int64_t)t.at * a.kv_heads + t.h, splits, t.split), row);
+        if (row < t.rows) leave(w, l, shared_part<D>(s, (int64_t)t.at * a.kv_heads + t.h, splits, t.split), row, t.a.blind);
     }
 };
 

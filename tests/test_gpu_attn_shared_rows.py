@@ -1,6 +1,6 @@
 """biloco_attn_shared where test_gpu_attn_shared.py does not look: how exact the weights
 of shared tokens are, batches of many sequences, lists out of order among them, and odd numbers of heads
-and rows.
+and rows, and rows of one tile that see far-apart tokens or none.
 
 Tolerance of the weights.  With e, t and the output's rounding as there, a weight is within 2^-16 of
 itself (two bf16 terms, each rounded to 8 significant bits: 2^-8 of 2^-8).  Over n tokens
@@ -106,3 +106,47 @@ def test_more_sequences_and_groups_than_the_table_takes_at_a_time():
                                           (9, 3, [(700, [(1, 701)] * 4 + [(3, 720)])]), (63, 1, [(90, [(1, 91)])])])
 def test_odd_numbers_of_heads_and_rows(dim, hq, hk, groups):
     Case(groups, hq, hk, dim, 32, seed=hq).check()
+
+
+def _forget(c, window, sinks):
+    """Shared pages of which no row sees a token hold NaN codes and scales without a value,
+    and every other one of them is named no more."""
+    seen = [set() for _ in c.shared]
+    group = np.repeat(np.arange(len(c.shared)), np.diff(c.group_start))
+    for b, n in enumerate(c.new):
+        for p in range(c.kv_len[b] - n, c.kv_len[b]):
+            lo = max(0, p - window + 1)
+            if p >= 0:
+                seen[group[b]].update(j // c.page for j in list(range(min(sinks, lo))) + list(range(lo, p + 1)))
+    k, v, ks, vs = c.cache
+    forgotten = 0
+    for g, n in enumerate(c.shared):
+        for i in set(range(n // c.page)) - seen[g]:
+            at = c.table[c.group_start[g], i]
+            k[at], v[at], ks[at], vs[at] = 0x7F, 0xFF, 255, 255
+            if i % 2:
+                c.table[c.group_start[g], i] = -1
+            forgotten += 1
+    return forgotten
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(64, 0), (64, 4), (100, 70), (30, 0), (1, 0)])
+@pytest.mark.parametrize("groups", [
+    [(640, [(1, 700), (1, 0), (2, 100), (1, 660)])],      # an idle slot, one that ends among the shared tokens
+    [(640, [(1, 0), (1, 641)]), (256, [(3, 2), (1, 300), (1, 120)])],
+    [(1280, [(1, 1281 + 3 * i if i % 5 else 40 * i) for i in range(30)])],      # several tiles
+    [(512, [(1, 2000), (1, 0)]), (512, [(1, 520), (1, 2000), (1, 300)])]])      # windows past the shared tokens
+def test_what_no_row_sees_of_the_shared_tokens_may_hold_anything(dim, window, sinks, groups):
+    c = Case(groups, 8, 1, dim, 32, seed=window + sinks)
+    assert _forget(c, window, sinks) > 0
+    c.check(window, sinks)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_idle_slots_among_answers(dim):
+    """Rows that see nothing, in every tile and wave, without a window and with one."""
+    c = Case([(700, [(1, 0 if i % 3 == 1 else 705 + i) for i in range(40)]), (300, [(2, 0)] * 9), (64, [(1, 65)])], 8, 1, dim, 16, seed=2)
+    for window, sinks in ((0, 0), (128, 0), (128, 9)):
+        o, lse = c.check(window, sinks)
+        assert not o[1::3][:13].any() and np.isneginf(lse[1::3][:13]).all()
