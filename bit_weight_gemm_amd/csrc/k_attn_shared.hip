@@ -52,41 +52,43 @@ __device__ __forceinline__ Group group_at(const AttnArgs &a, const SharedAttnArg
 }
 
 constexpr int kTableThreads = 1024;
-// Exclusive sums over the workgroup; all: the sum.  In 64 bits: lists that are not in order
+// Sums that stop at a cap below 2^31, as those of lists that are not in order have to: these
 // can claim every row for each second sequence.
-__device__ __forceinline__ int64_t sums_before(int v, int64_t (&tmp)[kTableThreads / 64], int64_t &all) {
+__device__ __forceinline__ int capped(int a, int b, int cap) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)cap); }
+// Exclusive sums over the workgroup of numbers from 0 to `cap`, behind `carry`, which
+// becomes the whole sum.
+__device__ __forceinline__ int sums_before(int v, int cap, int (&tmp)[kTableThreads / 64], int &carry) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int64_t in = v;
+    int in = v;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const int64_t t = __shfl_up((long long)in, o, 64);
-        if (lane >= o) in += t;
+        const int t = __shfl_up(in, o, 64);
+        if (lane >= o) in = capped(in, t, cap);
     }
     __syncthreads();
     if (lane == 63) tmp[wave] = in;
     __syncthreads();
-    int64_t b = in - v;
-    all = 0;
+    const int up = __shfl_up(in, 1, 64);
+    int before = carry;
     for (int i = 0; i < kTableThreads / 64; ++i) {
-        if (i < wave) b += tmp[i];
-        all += tmp[i];
+        if (i == wave) before = capped(carry, lane > 0 ? up : 0, cap);
+        carry = capped(carry, tmp[i], cap);
     }
-    return b;
+    return before;
 }
 
 __global__ void __launch_bounds__(kTableThreads)
 attn_shared_tables_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int tiles) {
-    __shared__ int64_t tmp[kTableThreads / 64];
+    __shared__ int tmp[kTableThreads / 64];
     const Tables t = tables_of(s, a.B);
     const int G = a.q_heads / a.kv_heads;
-    int64_t carry = 0, all;
+    int carry = 0;
     for (int at = 0; at < a.B; at += kTableThreads) {
         const int b = at + threadIdx.x, n = b < a.B ? seq_of(a, b, which).n : 0;
-        const int64_t mine = carry + sums_before(n, tmp, all);
-        if (b < a.B) t.before[b] = (int)min(mine, (int64_t)a.T);
-        carry += all;
+        const int mine = sums_before(n, a.T, tmp, carry);
+        if (b < a.B) t.before[b] = mine;
     }
-    if (threadIdx.x == 0) t.before[a.B] = (int)min(carry, (int64_t)a.T);
+    if (threadIdx.x == 0) t.before[a.B] = carry;
     __threadfence_block();
     __syncthreads();
     carry = 0;
@@ -98,11 +100,10 @@ attn_shared_tables_kernel(const AttnArgs a, const SharedAttnArgs s, int which, i
             const int64_t rows = (int64_t)(t.before[x.b1] - t.before[x.b0]) * G;
             n = x.upto > 0 ? (int)min((rows + kTileRows - 1) / kTileRows, (int64_t)tiles) : 0;
         }
-        const int64_t mine = carry + sums_before(n, tmp, all);
-        if (g < s.groups) t.tile[g] = (int)min(mine, (int64_t)tiles);
-        carry += all;
+        const int mine = sums_before(n, tiles, tmp, carry);
+        if (g < s.groups) t.tile[g] = mine;
     }
-    if (threadIdx.x == 0) t.tile[s.groups] = (int)min(carry, (int64_t)tiles);
+    if (threadIdx.x == 0) t.tile[s.groups] = carry;
     __threadfence_block();
     __syncthreads();
     for (int b = threadIdx.x; b < a.B; b += kTableThreads) {
