@@ -137,8 +137,9 @@ struct SharedArgs : PartArgs {
 };
 __device__ __forceinline__ uint32_t tile_sees8(const SharedArgs &a, int p_min, int p_max, int t0) {
     const uint32_t bits = any_sees8(a, p_min, p_max, t0);
-    if (!a.gaps || bits == 0) return bits;
+    if (__builtin_expect(!a.gaps || bits == 0, 1)) return bits;
     uint32_t some = 0;
+#pragma unroll 1      // out of the walk's way: unrolled, groups with drafts take 43.5 us for 43.1
     for (int r = 0; r < a.rows; ++r) some |= sees8(a, a.pos[r], t0);
     return some;
 }
