@@ -191,6 +191,9 @@ struct NormArgs {
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
 
+// A launch counts its threads along x in 32 bits; more wrap to fewer, without an error.
+inline bool fits_grid(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
+
 // ---------------------------------------------------------------- several answers to one prompt
 hipError_t launch_quant_mxfp4(const void *x, int64_t stride, bool fp32, int64_t M, int64_t K, uint8_t *codes,
                               uint8_t *scales, hipStream_t stream);

@@ -973,13 +973,32 @@ int slices_of(int rows, int V) {
     return s < 2 || V - V / s < kLeastSpared ? 1 : s;
 }
 
+// Rows of a launch: more than 2^22 would take 2^32 threads, which it cannot count.
+constexpr int kMostGrid = 1 << 21;
+SampleArgs rows_from(const SampleArgs &a, int64_t first, size_t size) {
+    SampleArgs b = a;
+    b.rows = (int)(a.rows - first < kMostGrid ? a.rows - first : kMostGrid);
+    b.logits = static_cast<const char *>(a.logits) + first * a.stride * (int64_t)size;
+    const auto on = [&](auto *&p) { if (p) p += first; };
+    on(b.temperature);
+    on(b.top_k);
+    on(b.top_p);
+    on(b.min_p);
+    on(b.u);
+    on(b.token);
+    on(b.logprob);
+    return b;
+}
 template <class T>
 void launch_rows(const SampleArgs &a, int S, hipStream_t stream) {
-    const dim3 rows((unsigned)a.rows), slices((unsigned)(a.rows * S)), threads(kThreads);
     if (S == 1) {
-        hipLaunchKernelGGL(sample_row_kernel<T>, rows, threads, 0, stream, a);
+        for (int64_t r = 0; r < a.rows; r += kMostGrid) {
+            const SampleArgs b = rows_from(a, r, sizeof(T));
+            hipLaunchKernelGGL(sample_row_kernel<T>, dim3((unsigned)b.rows), dim3(kThreads), 0, stream, b);
+        }
         return;
     }
+    const dim3 rows((unsigned)a.rows), slices((unsigned)(a.rows * S)), threads(kThreads);
     hipLaunchKernelGGL(sample_best_kernel<T>, slices, threads, 0, stream, a, S);
     hipLaunchKernelGGL(sample_sums_kernel<T>, slices, threads, 0, stream, a, S);
     hipLaunchKernelGGL(sample_cut_kernel<T>, rows, threads, 0, stream, a, S);

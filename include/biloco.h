@@ -586,7 +586,8 @@ biloco_status biloco_attn_shared_workspace_bytes(int32_t B, int32_t T, int32_t q
  *   u fp32 [rows]; token int32 [rows]; logprob fp32 [rows] or NULL
  *   workspace: >= biloco_sample_workspace_bytes(...) bytes, no fill needed; not
  *     shared by calls that can run at the same time.
- * 1 <= V < 2^20.  rows = 0 does nothing.  One to five launches. */
+ * 1 <= V < 2^20.  rows = 0 does nothing.  One to five launches, from 2^21 rows on
+ * one for every 2^21. */
 biloco_status biloco_sample(const void *logits, int64_t stride, int32_t fp32, int32_t rows,
                             int32_t V, const float *temperature, const int32_t *top_k,
                             const float *top_p, const float *min_p, const float *u,
