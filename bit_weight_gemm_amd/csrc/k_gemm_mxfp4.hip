@@ -695,11 +695,20 @@ size_t padded_bytes(int64_t M, int64_t N, int K) {
 size_t codes_bytes(int64_t M, int64_t K) { return ((size_t)(M * (K / 2)) + 255) / 256 * 256; }
 size_t scales_bytes(int64_t M, int64_t K) { return ((size_t)(M * (K / 32)) + 255) / 256 * 256; }
 
+// Columns of a launch: 2^27 take more threads (512 for 16 of them) than it can count.
+constexpr int64_t kMostColumns = 1 << 26;
 template <int NT, int MT, int WAVES>
-void rows_launch(const Mx &p, bool fp32, hipStream_t stream) {
-    const unsigned grid = (unsigned)((p.N + 16 * NT - 1) / (16 * NT));
-    if (fp32) hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, float>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
-    else hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, uint16_t>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
+void rows_launch(const Mx &all, bool fp32, hipStream_t stream) {
+    for (int64_t n0 = 0; n0 < all.N; n0 += kMostColumns) {
+        Mx p = all;
+        p.N = (int)(all.N - n0 < kMostColumns ? all.N - n0 : kMostColumns);
+        p.wc += n0 * (p.K / 2);
+        p.ws += n0 * (p.K / 32);
+        p.y = static_cast<char *>(p.y) + n0 * (fp32 ? 4 : 2);
+        const unsigned grid = (unsigned)((p.N + 16 * NT - 1) / (16 * NT));
+        if (fp32) hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, float>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
+        else hipLaunchKernelGGL((mxfp4_rows_kernel<NT, MT, WAVES, uint16_t>), dim3(grid), dim3(64 * WAVES), 0, stream, p);
+    }
 }
 template <int MT, class T>
 hipError_t held_launch(const Mx &p, hipStream_t stream) {

@@ -501,7 +501,8 @@ biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, 
  *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
  *     not shared by calls that can run at the same time.
  * 0 <= M <= 2^30 (0 does nothing), 1 <= N <= 2^30.  The result does not depend
- * on what else runs: sums are taken in a fixed order.  One to three launches. */
+ * on what else runs: sums are taken in a fixed order.  One to three launches, and for
+ * up to 32 rows one for every 2^26 columns. */
 biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const uint8_t *w_codes, const uint8_t *w_scales, int32_t M,
                                 int32_t N, int32_t K, void *y, int64_t y_stride, int32_t y_fp32,

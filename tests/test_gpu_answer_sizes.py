@@ -13,6 +13,11 @@ def _gen(seed=1):
     return torch.Generator(device="cuda").manual_seed(seed)
 
 
+def _weight(gen, rows, K):
+    return (torch.randint(0, 256, (rows, K // 2), generator=gen, device="cuda", dtype=torch.uint8),
+            torch.randint(120, 131, (rows, K // 32), generator=gen, device="cuda", dtype=torch.uint8))
+
+
 def _repeats(y, want, dim=0):
     """y along dim is `want` over and over."""
     n, at = want.shape[dim], 0
@@ -38,3 +43,15 @@ def test_sample_of_millions_of_rows(dtype):
     want, got = call(4096), call(n)
     for a, b in zip(got, want):
         _repeats(a, b)
+
+
+@pytest.mark.parametrize("M,N,dtype", [(1, (1 << 27) + 5, torch.bfloat16), (20, (1 << 28) + 37, torch.bfloat16)])
+def test_few_rows_to_millions_of_columns(M, N, dtype):
+    g, K = _gen(), 32
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    w = _weight(g, 1 << 16, K)
+    want = B.biloco_gemm_mxfp4_quant(x, *w, out_dtype=dtype)
+    times = -(-N // (1 << 16))
+    got = B.biloco_gemm_mxfp4_quant(x, *(t.repeat(times, 1)[:N] for t in w), out_dtype=dtype)
+    assert bool(want.isfinite().all()) and int(want.count_nonzero()) > 0
+    _repeats(got, want, 1)
