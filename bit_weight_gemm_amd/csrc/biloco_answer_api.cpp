@@ -23,6 +23,7 @@ biloco_status check_mx(int32_t M, int32_t K, const void *x, int64_t x_stride, co
     if (M < 0) return BILOCO_ERR_INVALID_VALUE;
     const biloco_status st = check_k(K);
     if (st != BILOCO_OK) return st;
+    if (!mxfp4_rows_fit(M, K)) return BILOCO_ERR_UNSUPPORTED;
     if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
         return BILOCO_ERR_INVALID_VALUE;
     return check_stride(x_stride, K);
@@ -38,7 +39,7 @@ biloco_status gemm(const uint16_t *x, int64_t x_stride, const uint8_t *a_codes, 
     if (M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
     biloco_status st = check_k(K);
     if (st != BILOCO_OK) return st;
-    if (M > kMostRows || N > kMostRows) return BILOCO_ERR_UNSUPPORTED;
+    if (M > kMostRows || N > kMostRows || !mxfp4_fits(M, N, K)) return BILOCO_ERR_UNSUPPORTED;
     if ((quant ? !x : !a_codes || !a_scales) || !w_codes || !w_scales || !y) return BILOCO_ERR_INVALID_VALUE;
     const void *ptrs[] = {x, a_codes, a_scales, w_codes, w_scales, y, workspace};
     for (const void *p : ptrs)
@@ -93,7 +94,7 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
     if (!bytes || M < 0 || N < 1) return BILOCO_ERR_INVALID_VALUE;
     const biloco_status st = check_k(K);
     if (st != BILOCO_OK) return st;
-    if (M > kMostRows || N > kMostRows) return BILOCO_ERR_UNSUPPORTED;
+    if (M > kMostRows || N > kMostRows || !mxfp4_fits(M, N, K)) return BILOCO_ERR_UNSUPPORTED;
     *bytes = M == 0 ? 0 : mxfp4_ws_bytes(M, N, K);
     return BILOCO_OK;
 }
@@ -120,6 +121,8 @@ biloco_status biloco_attn_shared_workspace_bytes(int32_t B, int32_t T, int32_t q
     if (n_groups > 65535 || max_shared_len > kMostTokens) return BILOCO_ERR_UNSUPPORTED;
     const biloco_status st = check_attn_sizes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len);
     if (st != BILOCO_OK) return st;
+    if (!attn_shared_fits(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, n_groups, max_shared_len))
+        return BILOCO_ERR_UNSUPPORTED;
     *bytes = attn_shared_ws_bytes(B, T, q_heads, kv_heads, head_dim, max_q_len, max_kv_len, n_groups, max_shared_len);
     return BILOCO_OK;
 }

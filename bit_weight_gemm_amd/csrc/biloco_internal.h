@@ -195,6 +195,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
 inline bool fits_grid(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
 
 // ---------------------------------------------------------------- several answers to one prompt
+bool mxfp4_rows_fit(int64_t M, int64_t K);      // a launch of the two below
 hipError_t launch_quant_mxfp4(const void *x, int64_t stride, bool fp32, int64_t M, int64_t K, uint8_t *codes,
                               uint8_t *scales, hipStream_t stream);
 hipError_t launch_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K, void *out,
@@ -210,6 +211,7 @@ struct MxGemmArgs {
     bool y_fp32;
     void *ws;
 };
+bool mxfp4_fits(int M, int N, int K);                         // its launches
 size_t mxfp4_plan_bytes(int M, int N, int K, bool quant);      // what this call uses
 size_t mxfp4_ws_bytes(int M, int N, int K);                    // what every call of up to M rows uses
 hipError_t launch_gemm_mxfp4(const MxGemmArgs &a, hipStream_t stream);
@@ -235,6 +237,8 @@ struct SharedAttnArgs {
     int groups, max_shared;
     void *tables, *parts;      // in the workspace
 };
+bool attn_shared_fits(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups,
+                      int max_shared);      // its launches
 size_t attn_shared_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups,
                             int max_shared);
 hipError_t launch_attn_shared(const AttnArgs &a, const SharedAttnArgs &s, size_t ws_bytes, hipStream_t stream);

@@ -298,7 +298,7 @@ attn_shared_join_kernel(const AttnArgs a, const SharedAttnArgs sh, int which, in
 struct SharedPlan {
     bool rows, tiles;      // sequences of few rows; of many
     int most_rows, shared_tiles, splits;
-    int64_t items;
+    int64_t items, tile_grid, join_grid;      // workgroups for the shared tokens, and for the join
     size_t table_bytes, own_bytes;
     size_t bytes, most_bytes;      // for this call; for it and every smaller one
 };
@@ -326,6 +326,8 @@ SharedPlan plan_of(int B, int T, int q_heads, int kv_heads, int dim, int max_q, 
     int64_t splits = wgs > 0 ? (kWantItems + wgs - 1) / wgs : 1;
     if (splits > most) splits = most;
     p.splits = splits < 1 ? 1 : (int)splits;
+    p.tile_grid = wgs * p.splits;
+    p.join_grid = p.items * ((p.most_rows + 3) / 4);
     p.table_bytes = table_ints(B, groups) * sizeof(int);
     p.own_bytes = own_bytes(p.items, dim, p.most_rows);
     const size_t part = (size_t)kTileRows * (dim + 2) * sizeof(float);
@@ -349,9 +351,7 @@ hipError_t launch(const AttnArgs &a, SharedAttnArgs s, const SharedPlan &p, hipS
     s.tables = ws;
     own.ws = ws + p.table_bytes;
     s.parts = ws + p.table_bytes + p.own_bytes;
-    const int64_t tiles = (int64_t)p.shared_tiles * p.splits * a.kv_heads, pieces = p.items + kPieces;
-    const int64_t join = p.items * ((p.most_rows + 3) / 4);
-    if (tiles + pieces > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int64_t tiles = p.tile_grid, pieces = p.items + kPieces, join = p.join_grid;
     hipLaunchKernelGGL(attn_shared_tables_kernel, dim3(1), dim3(kTableThreads), 0, stream, own, s, which, p.shared_tiles);
     static_assert(kSplitWaves == 4, "both kinds of workgroups in one grid");
     hipLaunchKernelGGL((attn_shared_kernel<D>), dim3((unsigned)(tiles + pieces)), dim3(256), 0, stream, own, s, which,
@@ -362,6 +362,12 @@ hipError_t launch(const AttnArgs &a, SharedAttnArgs s, const SharedPlan &p, hipS
 }
 
 }  // namespace
+
+bool attn_shared_fits(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups, int max_shared) {
+    if (B == 0 || T == 0) return true;
+    const SharedPlan p = plan_of(B, T, q_heads, kv_heads, dim, max_q, max_kv, groups, max_shared, 0, 0);
+    return fits_grid(p.tile_grid + p.items + kPieces, 256) && fits_grid(p.join_grid, 256);
+}
 
 size_t attn_shared_ws_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_q, int max_kv, int groups,
                             int max_shared) {

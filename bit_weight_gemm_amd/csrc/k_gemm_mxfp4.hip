@@ -724,7 +724,7 @@ template <int BM, int BN, int WM, int WN>
 hipError_t tiles_launch(const Mx &p, bool fp32, hipStream_t stream) {
     const int mt = (p.M + BM - 1) / BM;
     const int64_t grid = (int64_t)mt * ((p.N + BN - 1) / BN) * p.pieces;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 64 * WM * WN)) return hipErrorInvalidValue;
     const dim3 threads(64 * WM * WN);
     if (fp32) hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, WM, WN, float>), dim3((unsigned)grid), threads, 0, stream, p, mt);
     else hipLaunchKernelGGL((mxfp4_tiles_kernel<BM, BN, WM, WN, uint16_t>), dim3((unsigned)grid), threads, 0, stream, p, mt);
@@ -733,6 +733,12 @@ hipError_t tiles_launch(const Mx &p, bool fp32, hipStream_t stream) {
 
 }  // namespace
 
+bool mxfp4_fits(int M, int N, int K) {
+    if (M == 0) return true;
+    const MxPlan p = plan_of(M, N, K);
+    const int64_t b = p.rows ? 1 : p.bm, tiles = p.rows ? 1 : ((M + b - 1) / b) * ((N + b - 1) / b);
+    return mxfp4_rows_fit(M, K) && fits_grid(tiles * p.pieces, 256);
+}
 size_t mxfp4_plan_bytes(int M, int N, int K, bool quant) {
     return plan_of(M, N, K).part_bytes + padded_bytes(M, N, K) + (quant ? codes_bytes(M, K) + scales_bytes(M, K) : 0);
 }

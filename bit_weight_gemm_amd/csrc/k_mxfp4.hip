@@ -112,12 +112,17 @@ int64_t grid_of(int64_t n, int each) { return (n + 256 * each - 1) / (256 * each
 
 }  // namespace
 
+bool mxfp4_rows_fit(int64_t M, int64_t K) {
+    const int64_t n = M * (K / 8);
+    return fits_grid(grid_of(n, n <= kFew ? 1 : 4), 256);
+}
+
 hipError_t launch_quant_mxfp4(const void *x, int64_t stride, bool fp32, int64_t M, int64_t K, uint8_t *codes,
                               uint8_t *scales, hipStream_t stream) {
     const Groups g = groups_of(M, K, stride);
     const int each = g.n <= kFew ? 1 : 4;
     const int64_t grid = grid_of(g.n, each);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256)) return hipErrorInvalidValue;
     const float *xf = static_cast<const float *>(x);
     const uint16_t *xb = static_cast<const uint16_t *>(x);
     if (fp32 && each == 1) hipLaunchKernelGGL((quant_mxfp4_kernel<float, 1>), dim3((unsigned)grid), dim3(256), 0, stream, xf, g, codes, scales);
@@ -132,7 +137,7 @@ hipError_t launch_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int
     const Groups g = groups_of(M, K, stride);
     const int each = g.n <= kFew ? 1 : 4;
     const int64_t grid = grid_of(g.n, each);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256)) return hipErrorInvalidValue;
     float *of = static_cast<float *>(out);
     uint16_t *ob = static_cast<uint16_t *>(out);
     if (fp32 && each == 1) hipLaunchKernelGGL((dequant_mxfp4_kernel<float, 1>), dim3((unsigned)grid), dim3(256), 0, stream, codes, scales, g, of);

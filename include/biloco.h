@@ -480,13 +480,13 @@ biloco_status biloco_norm_gate_residual(const uint16_t *x, int64_t x_stride,
  * A block that holds a NaN or an infinity gets scale byte 255 and zero codes.
  *   x [M][K] bf16, or fp32 if x_fp32 != 0; x_stride in elements, a multiple of
  *     8, at least K
- * M = 0 does nothing.  One launch.  Bit-exact. */
+ * M = 0 does nothing, M * K of 2^37 and more is refused.  One launch.  Bit-exact. */
 biloco_status biloco_quant_mxfp4(const void *x, int64_t x_stride, int32_t x_fp32, int32_t M,
                                  int32_t K, uint8_t *codes, uint8_t *scales, hipStream_t stream);
 
 /* The values that codes and scales stand for, as bf16 (exact while finite), or
  * fp32 if out_fp32 != 0; magnitudes past the type's range become infinities.
- * out_stride in elements, a multiple of 8, at least K.  M = 0 does nothing.
+ * out_stride in elements, a multiple of 8, at least K.  M and K as above.
  * One launch. */
 biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int32_t M,
                                    int32_t K, void *out, int64_t out_stride, int32_t out_fp32,
@@ -500,7 +500,8 @@ biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, 
  *   y [M][N] bf16, or fp32 if y_fp32 != 0; y_stride in elements, at least N
  *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
  *     not shared by calls that can run at the same time.
- * 0 <= M <= 2^30 (0 does nothing), 1 <= N <= 2^30.  The result does not depend
+ * 0 <= M <= 2^30 (0 does nothing), 1 <= N <= 2^30; 2^24 tiles of 256 x 256 or
+ * more are refused.  The result does not depend
  * on what else runs: sums are taken in a fixed order.  One to three launches, and for
  * up to 32 rows one for every 2^26 columns. */
 biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
@@ -539,7 +540,8 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
  * max_shared_len bounds shared_len on the host; it shapes the launch.
  * workspace: >= biloco_attn_shared_workspace_bytes(...) bytes, no fill needed; not
  *   shared by calls that can run at the same time.
- * 1 <= n_groups <= 65535.  Contents that break these rules give unspecified values,
+ * 1 <= n_groups <= 65535; B * kv_heads times the rows of a sequence (64 at most) below
+ * 2^26 (more is refused).  Contents that break these rules give unspecified values,
  * but no access outside the arrays.  T = 0 or B = 0 does nothing.  One to six
  * launches. */
 biloco_status biloco_attn_shared(const uint8_t *k_codes, const uint8_t *v_codes,

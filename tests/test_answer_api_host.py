@@ -285,3 +285,20 @@ def test_shared_workspace_is_made_of_aligned_arrays(dim):
     and all are multiples of 16 long."""
     for b, hq, hk, q in ((1, 1, 1, 1), (3, 5, 1, 1), (3, 5, 1, 3), (5, 9, 3, 1), (7, 21, 7, 5), (1, 63, 1, 1), (2, 5, 1, 1)):
         assert B.biloco_attn_shared_workspace_bytes(b, b * q, hq, hk, dim, q, 500, 1, 300) % 16 == 0, (b, hq, hk, q)
+
+
+def test_more_work_than_a_launch_takes_is_refused():
+    """Past 2^32 threads, before anything is launched."""
+    big = (1 << 30)
+    for call in (quant, dequant):
+        assert call(M=(1 << 31) - 1, K=1 << 20, sx=1 << 20) == UNS
+    for M, N in ((big, big), (1 << 20, 1 << 26), (1000, big), (big, 1000)):
+        assert product(M=M, N=N, sy=N, K=32) == product_quant(M=M, N=N, sy=N, K=32, sx=32) == UNS, (M, N)
+        with pytest.raises(B.BilocoError, match="UNSUPPORTED|unsupported"):
+            B.biloco_gemm_mxfp4_workspace_bytes(M, N, 32)
+    assert B.biloco_gemm_mxfp4_workspace_bytes(700, big, 32) > 0      # 3 x 2^22 tiles
+    kw = dict(B=65535, hq=40, hk=40, dim=64, sq=2560, so=2560, T=70000)
+    assert shared(mq=64, **kw) == UNS
+    with pytest.raises(B.BilocoError, match="UNSUPPORTED|unsupported"):
+        B.biloco_attn_shared_workspace_bytes(65535, 70000, 40, 40, 64, 64, 1000, 2, 500)
+    assert B.biloco_attn_shared_workspace_bytes(65535, 70000, 40, 40, 64, 4, 1000, 2, 500) > 0
