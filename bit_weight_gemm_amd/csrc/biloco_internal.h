@@ -101,6 +101,9 @@ inline size_t ws_total_bytes(int M, int N, int K, int r) {
     return b > 0 ? ws_mfma_offset(M, 0) + b : 0;
 }
 
+// A launch counts its threads along x in 32 bits; more wrap to fewer, without an error.
+inline bool fits_grid(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
+
 hipError_t launch_pack_signs(const int8_t *signs, int64_t rows, int64_t cols, uint32_t *packed,
                              hipStream_t stream);
 hipError_t launch_quant_act(const uint16_t *x, int M, int K, uint8_t *codes, uint8_t *scales,
@@ -190,9 +193,6 @@ struct NormArgs {
     uint8_t *a_codes, *a_scales;
 };
 hipError_t launch_norm(const NormArgs &a, hipStream_t stream);
-
-// A launch counts its threads along x in 32 bits; more wrap to fewer, without an error.
-inline bool fits_grid(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
 
 // ---------------------------------------------------------------- several answers to one prompt
 bool mxfp4_rows_fit(int64_t M, int64_t K);      // a launch of the two below

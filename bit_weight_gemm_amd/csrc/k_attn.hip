@@ -252,12 +252,12 @@ template <int D>
 hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
     const int which = p.tiles ? kFewRows : kAllSeqs;
     if (p.whole) {
-        if (p.items > 0x7FFFFFFF) return hipErrorInvalidValue;
+        if (!fits_grid(p.items, 64 * kWholeWaves)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((attn_whole_kernel<D>), dim3((unsigned)p.items), dim3(64 * kWholeWaves), 0, stream, a, which,
                            p.most_rows);
         return hipGetLastError();
     }
-    if (p.items + kPieces > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(p.items + kPieces, 64 * kSplitWaves)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((attn_split_kernel<D, PagedRows>), dim3((unsigned)(p.items + kPieces)), dim3(64 * kSplitWaves), 0,
                        stream, PagedRows{a}, which, p.most_rows);
     const hipError_t e = hipGetLastError();
@@ -265,7 +265,7 @@ hipError_t launch(const AttnArgs &a, const Plan &p, hipStream_t stream) {
     // few rows: four waves a row; many: a wave
     const int ways = p.items * p.most_rows <= 1024 ? 4 : 1;
     const int64_t grid = p.items * ((p.most_rows + 4 / ways - 1) / (4 / ways));
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256)) return hipErrorInvalidConfiguration;
     if (ways == 4)
         hipLaunchKernelGGL((attn_join_kernel<D, 4>), dim3((unsigned)grid), dim3(256), 0, stream, a, which, p.most_rows,
                            (int)p.items);

@@ -140,7 +140,7 @@ hipError_t launch(const AttnArgs &a, int which, hipStream_t stream) {
     const TilesPlan p = attn_tiles_plan(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_kv, a.window, a.sinks);
     const int64_t grid = (int64_t)p.tiles * p.splits * a.kv_heads;
     const int64_t join = (int64_t)p.tiles * a.kv_heads * (kTileRows / 4);
-    if (grid > 0x7FFFFFFF || join > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256) || (p.splits > 1 && !fits_grid(join, 256))) return hipErrorInvalidConfiguration;
     const PagedTiles k{a, which, p.tiles};
     hipLaunchKernelGGL((attn_tiles_kernel<D, PagedTiles>), dim3((unsigned)grid), dim3(256), 0, stream, k, p.splits);
     hipError_t e = hipGetLastError();

@@ -360,7 +360,7 @@ hipError_t launch(const KvAppendArgs &a, hipStream_t stream) {
     const int parts = (int)(touched < a.max_pages ? touched : a.max_pages);
     const int64_t items = (int64_t)a.B * parts * a.kv_heads * 2;
     const int64_t grid = q_blocks + (items + 4 / NW - 1) / (4 / NW);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((kv_append_kernel<D, NW, PASSES>), dim3((unsigned)grid), dim3(256), 0, stream, a, q_blocks,
                        parts, items);
     return hipGetLastError();

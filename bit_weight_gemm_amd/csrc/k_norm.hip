@@ -259,6 +259,7 @@ template <int NW, int PER>
 hipError_t launch_vec(const NormArgs &a, hipStream_t stream) {
     constexpr int ROWS = NW < 4 ? 4 / NW : 1, NT = NW < 4 ? 256 : 64 * NW;
     const unsigned grid = (unsigned)(((int64_t)a.T + ROWS - 1) / ROWS);
+    if (!fits_grid(grid, NT)) return hipErrorInvalidConfiguration;
     if (a.res_fp32) hipLaunchKernelGGL((norm_vec_kernel<NW, PER, true>), dim3(grid), dim3(NT), 0, stream, a);
     else hipLaunchKernelGGL((norm_vec_kernel<NW, PER, false>), dim3(grid), dim3(NT), 0, stream, a);
     return hipGetLastError();
@@ -266,6 +267,7 @@ hipError_t launch_vec(const NormArgs &a, hipStream_t stream) {
 
 template <int NW, int PER>
 hipError_t launch_any(const NormArgs &a, hipStream_t stream) {
+    if (!fits_grid(a.T, 64 * NW)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((norm_any_kernel<NW, PER>), dim3((unsigned)a.T), dim3(64 * NW), 0, stream, a);
     return hipGetLastError();
 }
@@ -296,6 +298,7 @@ hipError_t launch_norm(const NormArgs &a, hipStream_t stream) {
     if (a.C <= 1024) return launch_any<4, 4>(a, stream);
     if (a.C <= 4096) return launch_any<16, 4>(a, stream);
     if (a.C <= 16384) return launch_any<16, 16>(a, stream);
+    if (!fits_grid(a.T, kLongThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(norm_long_kernel, dim3((unsigned)a.T), dim3(kLongThreads), 0, stream, a);
     return hipGetLastError();
 }

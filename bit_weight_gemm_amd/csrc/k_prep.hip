@@ -27,7 +27,7 @@ hipError_t launch_pack_signs(const int8_t *signs, int64_t rows, int64_t cols, ui
                              hipStream_t stream) {
     const int64_t W = (rows + 31) / 32;
     const int64_t cb = (cols + 255) / 256;
-    if (W * cb > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(W * cb, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(pack_signs_kernel, dim3((unsigned)(W * cb)), dim3(256), 0, stream, signs,
                        rows, cols, cb, packed);
     return hipGetLastError();
@@ -47,7 +47,7 @@ hipError_t launch_quant_act(const uint16_t *x, int M, int K, uint8_t *codes, uin
                             hipStream_t stream) {
     const int64_t nblocks = (int64_t)M * (K / 16);
     const int64_t grid = (nblocks + 255) / 256;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!fits_grid(grid, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(quant_act_kernel, dim3((unsigned)grid), dim3(256), 0, stream, x, nblocks,
                        codes, scales);
     return hipGetLastError();
