@@ -20,7 +20,7 @@ SOURCES = ["biloco_api.cpp", "k_prep.hip", "k_unfused.hip", "k_fused_gemv.hip", 
            "k_composed.hip", "k_peel.hip", "scratch.hip", "biloco_layer_api.cpp", "k_kv_append.hip",
            "k_attn.hip", "k_attn_tiles.hip", "k_norm.hip", "biloco_answer_api.cpp", "k_mxfp4.hip", "k_gemm_mxfp4.hip",
            "k_sample.hip", "k_attn_shared.hip"]
-HEADERS = ["biloco_device.h", "biloco_internal.h", "attn_device.h", "attn_rows.h", "attn_tiles.h", "mx_device.h", "api_checks.h", os.path.join("..", "..", "include", "biloco.h")]
+HEADERS = ["biloco_device.h", "biloco_internal.h", "attn_device.h", "attn_rows.h", "attn_tiles.h", "mx_device.h", "mx_plan.h", "api_checks.h", os.path.join("..", "..", "include", "biloco.h")]
 
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")

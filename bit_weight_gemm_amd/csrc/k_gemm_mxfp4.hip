@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "mx_device.h"
+#include "mx_plan.h"
 
 namespace biloco {
 
@@ -347,7 +348,7 @@ mxfp4_held_kernel(const Mx p, int tiles) {
 // 175 us of its own, 3.2 PFLOP/s, and 190 to 203 with the quantisation; the instruction alone on random
 // operands 90 us (6.1 PFLOP/s, from registers) or 103 (from LDS).  Two buffers of 256 k
 // instead 200 us with it where this one took 205; eight waves then 194, but their registers spill.
-constexpr int kStages = 4, kGroup = 8;      // stages in LDS; stages whose scales come together
+constexpr int kStages = 4;      // in LDS; the scales of kGroup of them come together
 
 template <int BM, int BN>
 struct StageLds {
@@ -649,43 +650,12 @@ mxfp4_scales_kernel(const uint8_t *__restrict__ a, int M, const uint8_t *__restr
     }
 }
 
-// Rows of A up to which W is streamed.  32 rows of 5120 to 13824 20.0 us, in tiles 22.2; 8192
-// to 8192 16.8 and 19.6; 17 rows of 5120 to 5120 9.5 and 14.2; 48 are past the kernels' operands.
-constexpr int kRows = 32;
-// Workgroups that the pieces of K are to make, one a CU: 200 rows of 13824 to 5120 in 3
-// pieces (240 workgroups) 31.4 us, in 2 36.7, in 6 34.0, in 9 44.
-constexpr int kWant = 256;
-
-constexpr int kCUs = 256;
-
 // Every workgroup quantises all of A, which pays where it has much of W to read or A is
 // short.  M rows of K to N, held against streamed: 1 x 5120 to 5120 8.0 and 8.0 us, 8 rows 9.4
 // and 9.0, 32 rows 15.0 and 10.9; to 13824 1 row 12.0 and 12.9, 8 rows 13.5 and 14.9, 32 rows
 // 20.0 and 20.5; 8192 to 8192 1 row 11.5 and 13.2, 16 rows 16.8 and 15.9.
 bool held(int M, int N, int K) {
     return M <= kRows && (M <= 4 || N >= 48 * kCUs) && K % 512 == 0 && held_of(M, K).bytes <= kHeldLds;
-}
-struct MxPlan {
-    bool rows;
-    int bm, bn, pieces;
-    size_t part_bytes;
-};
-MxPlan plan_of(int M, int N, int K) {
-    MxPlan p{M <= kRows, 0, 0, 1, 0};
-    if (p.rows) return p;
-    const auto tiles = [&](int b) { return (int64_t)((M + b - 1) / b) * ((N + b - 1) / b); };
-    // Large tiles where they fill at least four fifths of their rounds over the CUs: 2048 x
-    // 8192 x 8192 (256 of them) 87 us, in small ones 109; 4096 x 4096 x 4096 54 and 60; but
-    // 4096 x 5120 x 5120 (320) 110 and 84, 1500 x 13824 x 5120 (324) 114 and 95.
-    const int64_t large = tiles(256), rounds = (large + kCUs - 1) / kCUs;
-    p.bm = p.bn = 5 * large >= 4 * kCUs * rounds ? 256 : 128;
-    const int64_t n = tiles(p.bm);
-    int64_t pieces = n >= kWant ? 1 : (kWant + n / 2) / n;
-    const int64_t most = ((int64_t)K + 128 * kGroup - 1) / (128 * kGroup);      // groups of stages
-    if (pieces > most) pieces = most;
-    p.pieces = pieces < 1 ? 1 : (int)pieces;
-    if (p.pieces > 1) p.part_bytes = (size_t)p.pieces * M * N * 4;
-    return p;
 }
 // Of A's and W's rows of scales in multiples of four bytes, where they are not so already.
 size_t padded_bytes(int64_t M, int64_t N, int K) {
