@@ -187,6 +187,7 @@ struct TilesPlan {
 };
 TilesPlan attn_tiles_plan(int B, int T, int q_heads, int kv_heads, int dim, int max_kv, int window, int sinks);
 size_t attn_tiles_most_bytes(int B, int T, int q_heads, int kv_heads, int dim, int max_kv);
-hipError_t launch_attn_tiles(const AttnArgs &a, int which, hipStream_t stream);
+// terms: of a weight, 1 or 2 (attn_tiles.h)
+hipError_t launch_attn_tiles(const AttnArgs &a, int which, int terms, hipStream_t stream);
 
 }  // namespace biloco

@@ -116,9 +116,10 @@ struct Loader {
 // kernel for few rows; their sum is taken before that.  The second term brings o's error
 // to that of its own rounding (from 1.3 to 1.4 times that, root mean square) and takes half
 // as many matrix instructions again: on sequences of many rows 259 us for 210 on a prompt of
-// 4096 tokens, 441 for 348 on chunks of 64 channels, so these have one term.  Shared tokens
-// have two, so that a row's result is as exact as without sharing: four answers behind 608
-// tokens 19.2 us for 18.1, 64 behind 16384 84 for 77.
+// 4096 tokens, 441 for 348 on chunks of 64 channels, so the paged call has one term there.
+// The call with shared tokens has two for all of its rows, so that none of its results is
+// less exact than the paged call's of few rows: four answers behind 608 tokens 19.2 us for
+// 18.1, 64 behind 16384 84 for 77; four sequences of 128 tokens behind 8192 203 for 166.
 template <int D, int TERMS>
 struct Rows32 {
     u32x4_t q[D / 16];

@@ -288,7 +288,7 @@ hipError_t launch_attn(const AttnArgs &a, size_t ws_bytes, hipStream_t stream) {
     const Plan p = plan_of(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_q, a.max_kv, a.window, a.sinks);
     if (p.bytes > ws_bytes) return hipErrorInvalidValue;
     if (p.tiles) {      // first: the longest workgroups
-        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, stream);
+        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, 1, stream);
         if (e != hipSuccess || !p.rows) return e;
     }
     return a.dim == 64 ? launch<64>(a, p, stream) : launch<128>(a, p, stream);

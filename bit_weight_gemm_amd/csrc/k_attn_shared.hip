@@ -8,8 +8,9 @@
 //           shared token is read and made wide once for 128 rows, not once a sequence
 //   own     the kernel for few rows, from the first own token on
 // A row's position is its own sequence's, so that masks by position (causality, window,
-// first tokens) hold in both parts.  Sequences of more than kMostRows rows fill tiles by
-// themselves and share nothing: the kernel for many rows takes them whole.
+// first tokens) hold in both parts.  Sequences of more than kMostRows rows make tiles by
+// themselves and share nothing: the kernel for many rows takes them whole, here with
+// weights of two terms, so that all of the call's results are of one exactness.
 #include "attn_rows.h"
 #include "attn_tiles.h"
 
@@ -380,7 +381,7 @@ hipError_t launch_attn_shared(const AttnArgs &a, const SharedAttnArgs &s, size_t
                                  a.sinks);
     if (p.bytes > ws_bytes) return hipErrorInvalidValue;
     if (p.tiles) {
-        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, stream);
+        const hipError_t e = launch_attn_tiles(a, p.rows ? kManyRows : kAllSeqs, 2, stream);
         if (e != hipSuccess || !p.rows) return e;
     }
     return a.dim == 64 ? launch<64>(a, s, p, stream) : launch<128>(a, s, p, stream);

@@ -43,9 +43,10 @@ __device__ __forceinline__ int64_t tiles_of(const AttnArgs &a, const Seq &s) {
 // Workgroups: row tile (the last first: under causality the longest),
 // split, key/value head.  Heads run fastest, so the tiles of one head meet in
 // one XCD's L2 where the number of heads is a multiple of 8.
+template <int TERMS>
 struct PagedTiles {
     using Args = AttnArgs;
-    static constexpr int kTerms = 1;
+    static constexpr int kTerms = TERMS;
     struct Lds {};
     AttnArgs a;
     int which, tiles;
@@ -135,14 +136,14 @@ attn_tiles_join_kernel(const AttnArgs a, int which, int splits) {
     if (a.lse && lane == 0) a.lse[t * a.q_heads + h * G + g] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-template <int D>
+template <int D, int TERMS>
 hipError_t launch(const AttnArgs &a, int which, hipStream_t stream) {
     const TilesPlan p = attn_tiles_plan(a.B, a.T, a.q_heads, a.kv_heads, a.dim, a.max_kv, a.window, a.sinks);
     const int64_t grid = (int64_t)p.tiles * p.splits * a.kv_heads;
     const int64_t join = (int64_t)p.tiles * a.kv_heads * (kTileRows / 4);
     if (!fits_grid(grid, 256) || (p.splits > 1 && !fits_grid(join, 256))) return hipErrorInvalidConfiguration;
-    const PagedTiles k{a, which, p.tiles};
-    hipLaunchKernelGGL((attn_tiles_kernel<D, PagedTiles>), dim3((unsigned)grid), dim3(256), 0, stream, k, p.splits);
+    const PagedTiles<TERMS> k{a, which, p.tiles};
+    hipLaunchKernelGGL((attn_tiles_kernel<D, PagedTiles<TERMS>>), dim3((unsigned)grid), dim3(256), 0, stream, k, p.splits);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attn_tiles_join_kernel<D>), dim3((unsigned)join), dim3(256), 0, stream, a, which, p.splits);
@@ -189,8 +190,9 @@ size_t attn_tiles_most_bytes(int B, int T, int q_heads, int kv_heads, int dim, i
     return (size_t)most * kTileRows * (dim + 2) * sizeof(float);
 }
 
-hipError_t launch_attn_tiles(const AttnArgs &a, int which, hipStream_t stream) {
-    return a.dim == 64 ? launch<64>(a, which, stream) : launch<128>(a, which, stream);
+hipError_t launch_attn_tiles(const AttnArgs &a, int which, int terms, hipStream_t stream) {
+    if (terms == 2) return a.dim == 64 ? launch<64, 2>(a, which, stream) : launch<128, 2>(a, which, stream);
+    return a.dim == 64 ? launch<64, 1>(a, which, stream) : launch<128, 1>(a, which, stream);
 }
 
 }  // namespace biloco

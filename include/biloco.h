@@ -533,10 +533,10 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
  * biloco_attn_paged on sequences whose tables name the same pages first.
  * shared_len may end inside a page, and may pass a sequence's kv_len (its rows then
  * see the shared tokens up to their position).
- * For the product with v a weight of a shared token is the sum of two bf16, as are
- * those of own tokens.  A sequence of more than 64 rows (new tokens times q_heads /
- * kv_heads) fills the matrix cores by itself: its tokens are read through its own
- * table, which has to name the shared pages too.
+ * For the product with v every weight is the sum of two bf16 (within 2^-16 of it), those
+ * of sequences of more than 64 rows (new tokens times q_heads / kv_heads) too.  Such a
+ * sequence shares nothing: its tokens are read through its own table, which has to name
+ * the shared pages too.
  * max_shared_len bounds shared_len on the host; it shapes the launch.
  * workspace: >= biloco_attn_shared_workspace_bytes(...) bytes, no fill needed; not
  *   shared by calls that can run at the same time.

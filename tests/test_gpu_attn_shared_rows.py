@@ -59,9 +59,13 @@ def _one_term(c):
     ([(200, [(1, 201), (1, 230), (2, 300)])], 2, 2),
     ([(513, [(1, 514 + i) for i in range(40)])], 8, 1),      # more rows than a tile's
     ([(640, [(1, 700), (3, 650)]), (64, [(1, 65)] * 3), (130, [(5, 140), (1, 131)])], 16, 2),
-    ([(1500, [(1, 1501), (4, 1600)])], 4, 2)])      # in pieces
+    ([(1500, [(1, 1501), (4, 1600)])], 4, 2),      # in pieces
+    # sequences of many rows, which share nothing, alone and among others, in pieces
+    ([(300, [(40, 400)])], 4, 2), ([(128, [(1, 140), (30, 260), (2, 150)])], 8, 1), ([(1408, [(33, 1500), (34, 1450)])], 4, 2)])
 def test_weights_of_shared_tokens(dim, groups, hq, hk):
     c = Case(groups, hq, hk, dim, 32, seed=dim + hq)
+    for g, n in enumerate(c.shared):
+        c.table[c.group_start[g]:c.group_start[g + 1], :n // 32] = c.table[c.group_start[g], :n // 32]
     _cancel(c, seed=3)
     want, _, size, terms = c.want(0, 0)
     e = 2 * (dim + 8) * 2.0 ** -24 * terms[..., None] + 2.0 ** -20 + 2.0 ** -16
