@@ -235,8 +235,8 @@ struct OwnRows {
 };
 
 // Both in one launch, the tiles' workgroups first; neither waits for the other.  Four answers
-// behind 16 shared pages, groups with drafts and many answers: 18.1, 39.2 and 77 us, as two
-// launches 25.5, 48.5 and 82.
+// behind 608 shared tokens, groups with drafts and many answers: 20.1, 43.1 and 86 us.  With
+// weights of one term they took 18.1, 39.2 and 77, and as two launches 25.5, 48.5 and 82.
 template <int D>
 __global__ void __launch_bounds__(256, 2)
 attn_shared_kernel(const AttnArgs a, const SharedAttnArgs s, int which, int most_rows, int tiles, int splits) {

@@ -651,7 +651,8 @@ mxfp4_scales_kernel(const uint8_t *__restrict__ a, int M, const uint8_t *__restr
 }
 
 // Every workgroup quantises all of A, which pays where it has much of W to read or A is
-// short.  M rows of K to N, held against streamed: 1 x 5120 to 5120 8.0 and 8.0 us, 8 rows 9.4
+// short.  M rows of K to N, held against streamed, on twelve weights in turn (one row to 13824
+// on three, which stay in the last cache, 10.0 and 11.0): 1 x 5120 to 5120 8.0 and 8.0 us, 8 rows 9.4
 // and 9.0, 32 rows 15.0 and 10.9; to 13824 1 row 12.0 and 12.9, 8 rows 13.5 and 14.9, 32 rows
 // 20.0 and 20.5; 8192 to 8192 1 row 11.5 and 13.2, 16 rows 16.8 and 15.9.
 bool held(int M, int N, int K) {

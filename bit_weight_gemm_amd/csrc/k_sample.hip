@@ -43,7 +43,8 @@ struct Shared {
     double exp[64];      // 2^(j / 64)
 };
 
-// A row as 16-byte blocks: the first may begin before it, the last end behind it.
+// A row as 16-byte blocks: the first may begin before it, the last end behind it.  Blocks are
+// aligned and hold something of the row, so that no page but its own is touched.
 template <class T>
 struct Row {
     static constexpr int E = 16 / sizeof(T);
@@ -962,7 +963,7 @@ sample_pick_kernel(const SampleArgs a, int S) {
 // Slices a row where the rows alone leave CUs idle: at most kMostSlices, of at least
 // kLeastSlice logits each, and only if a workgroup is spared kLeastSpared logits, which is
 // what the launches cost.  In slices against a workgroup a row (fp32, p 0.9): one row of 16000
-// 41.6 and 31.0 us, of 32000 44.6 and 45.9, of 50000 48.5 and 63.5, of 262144 89 and 247; 32
+// 41.6 and 31.0 us, of 32000 44.6 and 45.9 (either way within the spread of calls), of 50000 48.5 and 63.5, of 262144 89 and 247; 32
 // rows of 32000 47.9 and 46.7, of 100000 66.5 and 112; 64 of 50000 58.9 and 66.6; 128 of 64000
 // (two slices) 83.5 and 77.3, of 150000 147 and 157.
 constexpr int kCUs = 256, kLeastSlice = 4096, kLeastSpared = 32768;

@@ -114,7 +114,8 @@ class AttentionBlock:
     def step(self, h, codes, scales, res, positions, q_start, kv_len, block_table, max_q_len: int, shared=None):
         """h [T][width] bf16 with its FP4 codes and scales (unused by an MxLinear: any), res
         [T][width] (updated in place) -> (h, codes, scales) of the next block.  shared: None,
-        or (group_start, shared_len) of biloco_attn_shared, shared tokens up to max_kv_len."""
+        or (group_start, shared_len) of biloco_attn_shared, shared tokens up to max_kv_len,
+        for which the launch is cut."""
         T, heads, kv, d = h.shape[0], self.heads, self.kv_heads, self.dim
         if T > self.max_tokens:
             raise ValueError(f"at most {self.max_tokens} new tokens a step")

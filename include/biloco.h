@@ -501,9 +501,8 @@ biloco_status biloco_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, 
  *   workspace: >= biloco_gemm_mxfp4_workspace_bytes(...) bytes, no fill needed;
  *     not shared by calls that can run at the same time.
  * 0 <= M <= 2^30 (0 does nothing), 1 <= N <= 2^30; 2^24 tiles of 256 x 256 or
- * more are refused.  The result does not depend
- * on what else runs: sums are taken in a fixed order.  One to three launches, and for
- * up to 32 rows one for every 2^26 columns. */
+ * more are refused.  The result does not depend on what else runs: sums are taken in a
+ * fixed order.  One to three launches, and for up to 32 rows one for every 2^26 columns. */
 biloco_status biloco_gemm_mxfp4(const uint8_t *a_codes, const uint8_t *a_scales,
                                 const uint8_t *w_codes, const uint8_t *w_scales, int32_t M,
                                 int32_t N, int32_t K, void *y, int64_t y_stride, int32_t y_fp32,
@@ -542,7 +541,7 @@ biloco_status biloco_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K,
  *   shared by calls that can run at the same time.
  * 1 <= n_groups <= 65535; B * kv_heads times the rows of a sequence (64 at most) below
  * 2^26 (more is refused).  Contents that break these rules give unspecified values,
- * but no access outside the arrays.  T = 0 or B = 0 does nothing.  One to six
+ * but no access outside the arrays.  T = 0 or B = 0 does nothing.  One to five
  * launches. */
 biloco_status biloco_attn_shared(const uint8_t *k_codes, const uint8_t *v_codes,
                                  const uint8_t *k_scales, const uint8_t *v_scales,
