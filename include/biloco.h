@@ -453,7 +453,8 @@ biloco_status biloco_attn_workspace_bytes(int32_t B, int32_t T, int32_t q_heads,
  *   strides in elements, at least C.  res_out may be res (same stride).
  *   a_codes [T][C/2], a_scales [T][C/16]: C % 32 == 0.
  * 1 <= C <= 32768, any C (multiples of 8 with strides that are multiples of 8
- * run faster).  T = 0 does nothing.  One launch. */
+ * run faster).  T = 0 does nothing.  From 2^22 rows on (narrow ones up to 2^26) a launch
+ * cannot count its threads, and BILOCO_ERR_HIP is returned.  One launch. */
 biloco_status biloco_norm_gate_residual(const uint16_t *x, int64_t x_stride,
                                         const uint16_t *post_w, const uint16_t *gate,
                                         int64_t gate_stride, float res_scale, const void *res,
